@@ -65,8 +65,9 @@ extern "C" {
 
 #define SSD_VERSION 100 /* 1.0.0 */
 
-/* Element types. */
-enum { SSD_F32 = 0, SSD_BF16 = 1 };
+/* Element types.  The integer types are taken by reset, lengths and positions
+ * only. */
+enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_U8 = 2, SSD_I32 = 3, SSD_I64 = 4 };
 
 /* Status codes. */
 enum {
@@ -368,6 +369,114 @@ int ssd_scan_bwd_gated(const ssd_tensor *x, const ssd_tensor *dt,
                        ssd_tensor *ddt, ssd_tensor *ddt_bias, ssd_tensor *dA,
                        ssd_tensor *dB, ssd_tensor *dC, ssd_tensor *dD,
                        ssd_tensor *dz, ssd_tensor *dinit_state, void *stream);
+
+/*
+ * Gated linear recurrence: ssd_glr_fwd, ssd_glr_bwd, ssd_glr_step
+ * ----------------------------------------------------------------
+ * One scalar state per channel, both gates computed from the input.  It is
+ * the forget-gate / input-gate recurrence of "Mamba-3 deep dive ch. 2"
+ * (171host.com, section 2.1.2) with a diagonal state and gates of its own:
+ *
+ *     s_t = sigmoid(r_t + r_bias)              recurrence gate
+ *     a_t = exp(A * s_t)                       decay, A normally < 0
+ *     h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * sigmoid(i_t + i_bias) * x_t
+ *
+ * for every batch row and channel; out_t = h_t.  The factor sqrt(1 - a^2)
+ * keeps the variance of h at that of its input (taken as 0 where a > 1).
+ *
+ * Packed and padded batches.  reset [b, L] marks (nonzero) the first token of
+ * each document: it starts from a zero state (a_t = 0, so the factor is 1).
+ * lengths [b] says how many tokens of each row exist (values outside [0, L]
+ * count as the nearer end): the tokens behind are not read, their outputs are
+ * left as they were, and the final state is the one after the last token that
+ * exists (the initial state if there is none).  What the state held before a
+ * reset, NaN and infinities among it, does not reach what follows.
+ *
+ * Layout: x, r, i and dout may be strided views (slices of a fused
+ * projection, broadcast batches): the last dimension contiguous, other
+ * strides >= 0, the token stride at most 2^21 elements.  All other tensors are
+ * dense row-major.  Pointers need the alignment of their element; rows are
+ * moved 16 bytes at a time where every width, stride and pointer allows it.
+ *
+ * Workspace: these calls take no scratch of the library's.  The caller passes
+ * `workspace`, 16-byte aligned device memory of at least
+ * ssd_glr_workspace(...) bytes (NULL if that is 0), which the call may write
+ * until its work on `stream` has finished; its contents need not be set and
+ * are of no further use.  Calls that may run at the same time, and graphs that
+ * may be replayed at the same time, need a workspace each.  The calls allocate
+ * nothing and record no event, so they may be captured into a HIP graph.
+ *
+ * Arithmetic: everything in fp32; out and the gradients of x, r and i are
+ * rounded once to the dtype of x.  Values below 2^-126 count as 0 (a gate
+ * that nearly shut leaves a_t = 1 and the factor 0).  Results do not vary from
+ * run to run.
+ * Supported: any D in [1, 2^20], 1 <= L <= 2^24, up to 2^22 tiles of 64
+ * channels by 256 tokens (128 for the gradients) over the batch.
+ */
+
+/* Tokens between the saved states of ssd_glr_fwd. */
+#define SSD_GLR_SEGMENT 128
+
+/* Workspace bytes of ssd_glr_fwd (backward = 0) or ssd_glr_bwd (1); -1 for a
+ * shape those calls refuse.  Host only. */
+int64_t ssd_glr_workspace(int64_t b, int64_t L, int64_t D, int backward);
+
+/*
+ * ssd_glr_fwd -- whole sequences.
+ *
+ *   x, r, i     [b, L, D]  f32 or bf16, one dtype; r and i before bias and
+ *                          sigmoid                             required
+ *   A           [D]        f32                                 required
+ *   r_bias, i_bias [D]     f32                                 NULL => 0
+ *   reset       [b, L]     u8                                  NULL => none
+ *   lengths     [b]        i32                                 NULL => L
+ *   init_state  [b, D]     f32                                 NULL => 0
+ *   out         [b, L, D]  dtype of x, written                 required
+ *   final_state [b, D]     f32, written; may be init_state     NULL => skip
+ *   states      [b, ceil(L / SSD_GLR_SEGMENT), D]  f32, written: the state
+ *                          entering every segment that holds a token (and
+ *                          the first), for ssd_glr_bwd         NULL => skip
+ * Other overlaps of an output with any argument are refused.
+ */
+int ssd_glr_fwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i,
+                const ssd_tensor *A, const ssd_tensor *r_bias,
+                const ssd_tensor *i_bias, const ssd_tensor *reset,
+                const ssd_tensor *lengths, const ssd_tensor *init_state,
+                ssd_tensor *out, ssd_tensor *final_state, ssd_tensor *states,
+                void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * ssd_glr_bwd -- gradients of ssd_glr_fwd for <dout, out> +
+ * <dfinal_state, final state>.  Inputs as for ssd_glr_fwd;
+ * states is what ssd_glr_fwd wrote for the same inputs, or NULL: then they
+ * are formed again from the inputs (one more pass over x, r and i).
+ * dout [b, L, D] has the dtype of x; dfinal_state [b, D] f32 may be NULL.
+ * Written in full: dx, dr, di [b, L, D] in the dtype of x (zero behind a
+ * row's length); dA, dr_bias, di_bias [D] and dinit_state [b, D] f32, each of
+ * these four may be NULL.  Where sqrt(1 - a^2) is 0 the gradient through it
+ * is taken as 0.  No output may overlap any other argument.
+ */
+int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i,
+                const ssd_tensor *A, const ssd_tensor *r_bias,
+                const ssd_tensor *i_bias, const ssd_tensor *reset,
+                const ssd_tensor *lengths, const ssd_tensor *init_state,
+                const ssd_tensor *states, const ssd_tensor *dout,
+                const ssd_tensor *dfinal_state, ssd_tensor *dx, ssd_tensor *dr,
+                ssd_tensor *di, ssd_tensor *dA, ssd_tensor *dr_bias,
+                ssd_tensor *di_bias, ssd_tensor *dinit_state, void *workspace,
+                int64_t workspace_bytes, void *stream);
+
+/*
+ * ssd_glr_step -- one token for every row (serving).  state [b, D] f32;
+ * x, r, i [b, D]; reset [b] u8 or NULL (nonzero: the slot starts anew);
+ * new_state [b, D] f32, written, may be `state`; out [b, D] dtype of x,
+ * written.  b * ceil(D / 1024) at most 2^22.
+ */
+int ssd_glr_step(const ssd_tensor *state, const ssd_tensor *x,
+                 const ssd_tensor *r, const ssd_tensor *i, const ssd_tensor *A,
+                 const ssd_tensor *r_bias, const ssd_tensor *i_bias,
+                 const ssd_tensor *reset, ssd_tensor *new_state,
+                 ssd_tensor *out, void *stream);
 
 /*
  * ssd_scan_plan -- the plan SSD_ALGO_AUTO uses for a shape on a device with

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "ssd.h"
+#include "ssd_check.h"
 #include "ssd_internal.h"
 
 // Scratch of the allocation-free entry point ssd_scan_fwd_noalloc: a fixed
@@ -28,11 +29,21 @@
 #define SSD_FIXED_SCRATCH_BYTES ((size_t)64 << 20)
 static __device__ __align__(256) unsigned char scratch[SSD_FIXED_SCRATCH_BYTES];
 
+using ssd::Range;
+using ssd::check_addressable;
+using ssd::elem_size;
+using ssd::fail;
+using ssd::hip_fail;
+using ssd::numel;
+using ssd::overlap;
+
 namespace {
-
 thread_local std::string g_last_error;
+} // namespace
 
-int fail(int status, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace ssd {
+void clear_error() { g_last_error.clear(); }
+
 int fail(int status, const char *fmt, ...) {
   char buf[512];
   va_list ap;
@@ -43,18 +54,37 @@ int fail(int status, const char *fmt, ...) {
   return status;
 }
 
-int elem_size(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
-
-int64_t numel(const ssd_tensor *t) {
-  int64_t n = 1;
-  for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
-  return n;
+int hip_fail(hipError_t e, const char *what) {
+  return fail(SSD_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-struct Range {
-  uintptr_t lo = 0, hi = 0; // [lo, hi)
-  bool empty() const { return hi <= lo; }
-};
+// Every tensor must be memory the current device can address: device memory
+// of the current device, managed memory, or pinned host memory.  Pageable
+// host memory or another device's memory is refused here, before any launch
+// (a kernel would fault on it).
+int check_addressable(const ssd_tensor *const *ts, const char *const *names, int n) {
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess) {
+    (void)hipGetLastError();
+    return fail(SSD_ERR_LAYOUT, "no current HIP device");
+  }
+  for (int i = 0; i < n; ++i) {
+    if (!ts[i]) continue;
+    hipPointerAttribute_t a;
+    if (hipPointerGetAttributes(&a, ts[i]->data) != hipSuccess) {
+      (void)hipGetLastError();
+      return fail(SSD_ERR_LAYOUT, "%s: not memory a HIP device can address (pageable host memory?)", names[i]);
+    }
+    if (a.type == hipMemoryTypeUnregistered)
+      return fail(SSD_ERR_LAYOUT, "%s: not memory a HIP device can address (pageable host memory?)", names[i]);
+    if (a.type == hipMemoryTypeDevice && a.device != dev)
+      return fail(SSD_ERR_LAYOUT, "%s: on device %d, but device %d is current", names[i], a.device, dev);
+  }
+  return SSD_OK;
+}
+} // namespace ssd
+
+namespace {
 
 Range range_of(const ssd_tensor *t) {
   Range r;
@@ -62,10 +92,6 @@ Range range_of(const ssd_tensor *t) {
   r.lo = (uintptr_t)t->data;
   r.hi = r.lo + (uintptr_t)(numel(t) * elem_size(t->dtype));
   return r;
-}
-
-bool overlap(const Range &a, const Range &b) {
-  return !a.empty() && !b.empty() && a.lo < b.hi && b.lo < a.hi;
 }
 
 // Checks presence, dtype, rank, exact shape, dense row-major strides and
@@ -96,12 +122,6 @@ int check_tensor(const ssd_tensor *t, const char *name, int want_dtype, int ndim
     return fail(SSD_ERR_LAYOUT, "%s: data pointer is not 16-byte aligned", name);
   return SSD_OK;
 }
-
-#define SSD_CHECK(expr)                                                                   \
-  do {                                                                                    \
-    int _s = (expr);                                                                      \
-    if (_s != SSD_OK) return _s;                                                          \
-  } while (0)
 
 bool valid_pn(int64_t v) { return v == 16 || v == 32 || v == 64 || v == 128; }
 
@@ -172,10 +192,6 @@ int validate_scan(const ssd_tensor *x, const ssd_tensor *dt, const ssd_tensor *d
   }
   if (overlap(ro, rf)) return fail(SSD_ERR_ALIAS, "out overlaps final_state");
   return SSD_OK;
-}
-
-int hip_fail(hipError_t e, const char *what) {
-  return fail(SSD_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 // Scratch memory.  A stream-ordered allocate/free pair on every call makes the
@@ -425,31 +441,6 @@ void scratch_usage(size_t *slots, size_t *bytes) {
   size_t t = 0;
   for (const ScratchSlot &s : g_scratch) t += s.cap;
   *bytes = t;
-}
-
-// Every tensor must be memory the current device can address: device memory
-// of the current device, managed memory, or pinned host memory.  Pageable
-// host memory or another device's memory is refused here, before any launch
-// (a kernel would fault on it).
-int check_addressable(const ssd_tensor *const *ts, const char *const *names, int n) {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess) {
-    (void)hipGetLastError();
-    return fail(SSD_ERR_LAYOUT, "no current HIP device");
-  }
-  for (int i = 0; i < n; ++i) {
-    if (!ts[i]) continue;
-    hipPointerAttribute_t a;
-    if (hipPointerGetAttributes(&a, ts[i]->data) != hipSuccess) {
-      (void)hipGetLastError();
-      return fail(SSD_ERR_LAYOUT, "%s: not memory a HIP device can address (pageable host memory?)", names[i]);
-    }
-    if (a.type == hipMemoryTypeUnregistered)
-      return fail(SSD_ERR_LAYOUT, "%s: not memory a HIP device can address (pageable host memory?)", names[i]);
-    if (a.type == hipMemoryTypeDevice && a.device != dev)
-      return fail(SSD_ERR_LAYOUT, "%s: on device %d, but device %d is current", names[i], a.device, dev);
-  }
-  return SSD_OK;
 }
 
 int run_fused(const ssd_tensor *x, const ssd_tensor *dt, const ssd_tensor *dt_bias,

@@ -167,4 +167,47 @@ hipError_t launch_bwd(int dtype, int P, int N, const BwdParams &p, hipStream_t s
 // dz = dout * y * silu'(z) in fp32; n elements, a multiple of 4.
 hipError_t launch_gate_bwd(int dtype, const void *y, const void *z, const void *dout, void *dy, float *dz,
                            int64_t n, hipStream_t stream);
+
+// The gated linear recurrence.  A workgroup of the forward takes kGlrChunk
+// tokens of 64 channels, one of the backward kGlrSegment tokens (the spacing
+// of the saved states).
+constexpr int kGlrChunk = 256;
+constexpr int kGlrSegment = 128; // SSD_GLR_SEGMENT
+struct GlrParams {
+  const void *x, *r, *i, *dout;          // [b, L, D], last dim contiguous
+  int64_t xb, rb_, ib_, db;              // batch strides, elements
+  int xt, rt, it, dt;                    // token strides, elements
+  const float *A, *rbias, *ibias;        // [D]; the biases may be null
+  const uint8_t *reset;                  // [b, L] or null
+  const int32_t *lengths;                // [b] or null
+  const float *init;                     // [b, D] or null
+  void *out;                             // [b, L, D] dense, or null (states only)
+  float *fin;                            // [b, D] or null; may be init (inplace)
+  float *states;                         // [b, ceil(L/kGlrSegment), D] or null
+  const float *dfin;                     // [b, D] or null
+  void *dx, *dr, *di;                    // [b, L, D] dense
+  float *dinit;                          // [b, D] or null
+  float *part;                           // [b, nchunk, 3, D]
+  uint64_t *words;                       // chain words [b, nchunk, ntile*64], null if nchunk == 1
+  uint32_t *ticket;                      // behind the words
+  int b, L, D, nchunk, ntile;
+  int inplace;
+};
+// Bytes of the chain words and the ticket behind them.
+inline int64_t glr_chain_bytes(int64_t b, int64_t nchunk, int64_t ntile) { return b * nchunk * ntile * 512 + 16; }
+// dtype 1 = bf16, 0 = fp32; vec: widths, strides and pointers allow 16-byte rows.
+hipError_t launch_glr(int dtype, bool vec, bool back, const GlrParams &p, hipStream_t stream);
+// Sums n partial rows [3][D] into dA, d r_bias, d i_bias (each may be null).
+hipError_t launch_glr_sum(const float *part, int n, int D, float *dA, float *drb, float *dib, hipStream_t stream);
+struct GlrStepParams {
+  const void *x, *r, *i;          // [b, D]
+  int64_t xb, rb_, ib_;           // batch strides
+  const float *A, *rbias, *ibias; // [D]
+  const uint8_t *reset;           // [b] or null
+  const float *state;             // [b, D]
+  float *new_state;               // [b, D], may be state
+  void *out;                      // [b, D]
+  int b, D, nblk;                 // nblk is set by the launch
+};
+hipError_t launch_glr_step(int dtype, bool vec, const GlrStepParams &p, hipStream_t stream);
 } // namespace ssd

@@ -20,7 +20,8 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libssd.so")
 
-SSD_F32, SSD_BF16 = 0, 1
+SSD_F32, SSD_BF16, SSD_U8, SSD_I32, SSD_I64 = 0, 1, 2, 3, 4
+SSD_GLR_SEGMENT = 128
 SSD_ALGO_AUTO, SSD_ALGO_FUSED, SSD_ALGO_CHUNKED, SSD_ALGO_ROWS, SSD_ALGO_QUAD = 0, 1, 2, 3, 4
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL", 2: "SSD_ERR_SHAPE", 3: "SSD_ERR_DTYPE",
           4: "SSD_ERR_LAYOUT", 5: "SSD_ERR_UNSUPPORTED", 6: "SSD_ERR_ALIAS",
@@ -83,11 +84,21 @@ def lib():
                                                             ctypes.POINTER(ctypes.c_int),
                                                             ctypes.POINTER(ctypes.c_int)]
         L.ssd_scan_plan.restype = ctypes.c_int
+        I64 = ctypes.c_int64
+        L.ssd_glr_workspace.argtypes = [I64] * 3 + [ctypes.c_int]
+        L.ssd_glr_workspace.restype = I64
+        L.ssd_glr_fwd.argtypes = [P] * 13 + [I64, P]
+        L.ssd_glr_fwd.restype = ctypes.c_int
+        L.ssd_glr_bwd.argtypes = [P] * 20 + [I64, P]
+        L.ssd_glr_bwd.restype = ctypes.c_int
+        L.ssd_glr_step.argtypes = [P] * 11
+        L.ssd_glr_step.restype = ctypes.c_int
         _lib = L
     return _lib
 
 
-_DTYPE_CODE = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+_DTYPE_CODE = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16, torch.uint8: SSD_U8, torch.bool: SSD_U8,
+               torch.int32: SSD_I32, torch.int64: SSD_I64}
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -320,6 +331,107 @@ def ssd_step(state, x, dt, A, B, C, D=None, out=None, stream=None):
         st = _stream(stream, state)
         keep, d = _descs(state, x, dt, A, B, C, D, out)
         status = lib().ssd_step(*d, st)
+    _check(status)
+    return out
+
+
+def _workspace(nbytes: int, t, stream):
+    """Workspace of one call from torch's allocator, on the stream the call
+    runs on (so that the memory is handed out again only behind the call;
+    under graph capture it belongs to the graph)."""
+    if nbytes <= 0:
+        return None
+    cur = torch.cuda.current_stream(t.device).cuda_stream if t.is_cuda else None
+    if stream is None or not t.is_cuda or stream == cur:
+        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+
+
+def ssd_glr_workspace(b: int, L: int, D: int, backward: bool = False) -> int:
+    """Workspace bytes of ssd_glr_fwd or ssd_glr_bwd (-1: a shape they refuse)."""
+    return int(lib().ssd_glr_workspace(int(b), int(L), int(D), int(backward)))
+
+
+def _glr_workspace(x, backward, stream):
+    if x.dim() != 3:
+        return None  # refused by the call
+    return _workspace(ssd_glr_workspace(*x.shape, backward), x, stream)
+
+
+def ssd_glr_states(x):
+    """An uninitialised ``states`` tensor for ssd_glr_fwd on this x [b, L, D]."""
+    b, L, D = x.shape
+    return torch.empty((b, (L + SSD_GLR_SEGMENT - 1) // SSD_GLR_SEGMENT, D), dtype=torch.float32,
+                       device=x.device)
+
+
+def ssd_glr_fwd(x, r, i, A, r_bias=None, i_bias=None, *, reset=None, lengths=None, init_state=None,
+                out=None, final_state=None, states=None, stream=None, return_final_state: bool = True):
+    """Gated linear recurrence over whole sequences, per channel
+
+        h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t + i_bias) x_t,
+        a_t = exp(A sigmoid(r_t + r_bias)),
+
+    x, r, i [b, L, D] (views allowed), reset [b, L] uint8 or bool, lengths [b]
+    int32; ``states`` (see ssd_glr_states) is filled for ssd_glr_bwd.  Returns
+    (out, final_state or None); tokens behind a row's length are not written."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if final_state is None and return_final_state:
+        final_state = torch.empty((x.shape[0], x.shape[-1]), dtype=torch.float32, device=x.device)
+    with _on_device(x):
+        st = _stream(stream, x)
+        ws = _glr_workspace(x, False, st)
+        keep, d = _descs(x, r, i, A, r_bias, i_bias, reset, lengths, init_state, out, final_state, states)
+        status = lib().ssd_glr_fwd(*d, ws.data_ptr() if ws is not None else None,
+                                   ws.numel() if ws is not None else 0, st)
+    _check(status)
+    return out, final_state
+
+
+def ssd_glr_bwd(x, r, i, A, r_bias=None, i_bias=None, *, reset=None, lengths=None, init_state=None,
+                dout, dfinal_state=None, states=None, want_bias: bool = True, want_init: bool = True,
+                out: dict = None, stream=None):
+    """Gradients of ssd_glr_fwd for <dout, out> + <dfinal_state, final state>.
+
+    Returns a dict: dx, dr, di (dtype of x), dA and, when asked for, dr_bias,
+    di_bias, dinit (fp32).  ``states`` as filled by ssd_glr_fwd saves a pass
+    over the inputs.  ``out`` may hold preallocated tensors under those names."""
+    D, dev = x.shape[-1], x.device
+    g = dict(out or {})
+    for k in ("dx", "dr", "di"):
+        if g.get(k) is None:
+            g[k] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    small = dict(dA=(D,), dr_bias=(D,) if want_bias else None, di_bias=(D,) if want_bias else None,
+                 dinit=(x.shape[0], D) if want_init else None)
+    for k, shp in small.items():
+        if shp is None:
+            g[k] = None
+        elif g.get(k) is None:
+            g[k] = torch.empty(shp, dtype=torch.float32, device=dev)
+    with _on_device(x):
+        st = _stream(stream, x)
+        ws = _glr_workspace(x, True, st)
+        keep, d = _descs(x, r, i, A, r_bias, i_bias, reset, lengths, init_state, states, dout, dfinal_state,
+                         g["dx"], g["dr"], g["di"], g["dA"], g["dr_bias"], g["di_bias"], g["dinit"])
+        status = lib().ssd_glr_bwd(*d, ws.data_ptr() if ws is not None else None,
+                                   ws.numel() if ws is not None else 0, st)
+    _check(status)
+    return g
+
+
+def ssd_glr_step(state, x, r, i, A, r_bias=None, i_bias=None, *, reset=None, out=None, new_state=None,
+                 stream=None):
+    """One token of the gated linear recurrence for every row: state [b, D] is
+    updated in place (or written to ``new_state``); returns out [b, D]."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    with _on_device(state):
+        st = _stream(stream, state)
+        keep, d = _descs(state, x, r, i, A, r_bias, i_bias, reset,
+                         state if new_state is None else new_state, out)
+        status = lib().ssd_glr_step(*d, st)
     _check(status)
     return out
 
