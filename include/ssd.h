@@ -479,6 +479,61 @@ int ssd_glr_step(const ssd_tensor *state, const ssd_tensor *x,
                  ssd_tensor *out, void *stream);
 
 /*
+ * Norm and rotation of queries and keys
+ * -------------------------------------
+ * In the dual (attention) form of the scan, C holds the queries and B the keys
+ * ("Mamba-3 deep dive ch. 2", 171host.com, section 2.2.2, the linear-attention
+ * view).  Turning both by an angle that grows with the position gives the
+ * scalar decay of a head an imaginary part per pair of state indices; normed
+ * queries and keys bound the scores.  For every token and head vector x of
+ * q [b, L, Hq, N] or k [b, L, Hk, N]:
+ *
+ *     n = x / sqrt(mean(x^2) + eps),    y = R(position) (weight * n)
+ *
+ * R turns pair j by position * freqs[j] (radians): the pair (j, j + npair), or
+ * with interleaved = 1 (2j, 2j + 1), of the first 2 * npair elements;
+ * npair = the length of freqs (NULL: no rotation).  Hq and Hk are free of each
+ * other (shared keys: Hk < Hq).
+ *
+ *   q, k         f32 or bf16, one dtype; views allowed: the last dimension
+ *                contiguous, other strides >= 0, token and head strides at
+ *                most 2^21 elements                           required
+ *   q_weight, k_weight [N]  f32                               NULL => 1
+ *   freqs        [npair]    f32                               NULL => none
+ *   positions    [b, L]     i32 or i64, any value             NULL => 0..L-1
+ *   q_out, k_out dtype and shape of q and k, dense, written
+ *
+ * Supported: N a multiple of 8 up to 256, npair a multiple of 4 up to N / 2,
+ * L at most 2^24, Hq and Hk at most 2^16, b * L * (Hq + Hk) at most 2^26.
+ * Arithmetic: fp32, angles reduced to a turn in 64 bits; results are rounded
+ * once.  Results do not vary from run to run.  No output may overlap any other
+ * argument.  Nothing is allocated; the calls may be captured into a HIP graph.
+ */
+int ssd_norm_rotate_fwd(const ssd_tensor *q, const ssd_tensor *k,
+                        const ssd_tensor *q_weight, const ssd_tensor *k_weight,
+                        const ssd_tensor *freqs, const ssd_tensor *positions,
+                        ssd_tensor *q_out, ssd_tensor *k_out, float eps,
+                        int interleaved, void *stream);
+
+/* Workspace bytes of ssd_norm_rotate_bwd (see Workspace above); -1 for an N it
+ * refuses.  Host only. */
+int64_t ssd_norm_rotate_workspace(int64_t N);
+
+/*
+ * ssd_norm_rotate_bwd -- gradients for <dq_out, q_out> + <dk_out, k_out>.
+ * dq_out, dk_out: dtype and shape of q and k, views allowed.  Written in full:
+ * dq, dk (dtype of q, dense) and dq_weight, dk_weight [N] f32, each of these
+ * two may be NULL.  Nothing of the forward is needed but its inputs.
+ */
+int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k,
+                        const ssd_tensor *q_weight, const ssd_tensor *k_weight,
+                        const ssd_tensor *freqs, const ssd_tensor *positions,
+                        const ssd_tensor *dq_out, const ssd_tensor *dk_out,
+                        ssd_tensor *dq, ssd_tensor *dk, ssd_tensor *dq_weight,
+                        ssd_tensor *dk_weight, float eps, int interleaved,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * ssd_scan_plan -- the plan SSD_ALGO_AUTO uses for a shape on a device with
  * `cus` compute units for inputs of element type `dtype` (SSD_BF16 or
  * SSD_F32), host only, no HIP call: *algo is SSD_ALGO_FUSED,

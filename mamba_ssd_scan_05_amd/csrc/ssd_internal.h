@@ -210,4 +210,30 @@ struct GlrStepParams {
   int b, D, nblk;                 // nblk is set by the launch
 };
 hipError_t launch_glr_step(int dtype, bool vec, const GlrStepParams &p, hipStream_t stream);
+
+// Norm of queries and keys for each head with the position rotation.
+constexpr int kNormRotGroups = 1024; // workgroups (and partial rows) of the backward
+struct NormRotParams {
+  const void *q, *k;                      // [b, L, Hq / Hk, N], last dim contiguous
+  int64_t qb, qt, qh, kb, kt, kh;         // strides, elements
+  const void *dyq, *dyk;                  // gradients at the outputs (backward)
+  int64_t dqb, dqt, dqh, dkb, dkt, dkh;
+  const float *qw, *kw;                   // [N] or null
+  const float *freqs;                     // [npair]
+  const int32_t *pos32;                   // [b, L], or
+  const int64_t *pos64;                   // [b, L], or both null: 0 .. L-1
+  void *oq, *ok;                          // outputs or gradients, dense
+  float *part;                            // [nwg, 2, N] (backward)
+  float *dqw, *dkw;                       // [N] or null
+  float eps;
+  int L, Hq, Hk, N, npair, interleaved;
+  int64_t ntok;
+  // set by norm_rotate_plan
+  int64_t nitem;
+  int hg_log, per, split, nwg;
+};
+// N a multiple of 8 up to 256, npair a multiple of 4 up to N/2.
+void norm_rotate_plan(NormRotParams *p);
+// dtype 1 = bf16, 0 = fp32; vec: strides and pointers allow 4-element accesses.
+hipError_t launch_norm_rotate(int dtype, bool vec, bool back, const NormRotParams &p, hipStream_t stream);
 } // namespace ssd

@@ -1,5 +1,5 @@
-// ssd_seq_api.hip -- the C ABI of the gated linear recurrence: argument
-// validation, workspace layout and launches.  Declarations and the contract
+// ssd_seq_api.hip -- the C ABI of the gated linear recurrence and of the
+// norm with rotation: argument validation, workspace layout and launches.  Declarations and the contract
 // are in include/ssd.h.  As in ssd_api.hip every check runs on the host
 // before the first launch.
 #include <hip/hip_runtime.h>
@@ -19,6 +19,10 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 24;
 constexpr int64_t kMaxWidth = (int64_t)1 << 20;  // channels of the recurrence
 constexpr int64_t kMaxStride = (int64_t)1 << 21; // token stride: 256 fp32 rows within 2^31 bytes
 constexpr int64_t kMaxOuter = (int64_t)1 << 36;  // batch stride
+constexpr int64_t kMaxHeads = (int64_t)1 << 16;
+// head vectors of the norm: there are at least two to a token, so that a launch
+// has at most 2^25 waves
+constexpr int64_t kMaxVectors = (int64_t)1 << 26;
 constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // workgroups of 512 threads in one launch
 
 const char *dtype_name(int d) {
@@ -231,6 +235,85 @@ void set_chain(GlrParams *p, int64_t nchunk, void *ws) {
   p->ticket = nchunk > 1 ? (uint32_t *)((char *)ws + glr_chain_bytes(p->b, nchunk, p->ntile) - 16) : nullptr;
 }
 
+// ---------------------------------------------------------------------------
+// norm and rotation of queries and keys
+// ---------------------------------------------------------------------------
+// Element groups of four at 8 (bf16) or 16 bytes (f32).
+bool rows4(const ssd_tensor *t) {
+  if (!t) return true;
+  if ((uintptr_t)t->data % (uintptr_t)(4 * elem_size(t->dtype)) != 0) return false;
+  for (int i = 0; i < t->ndim - 1; ++i)
+    if (t->shape[i] != 1 && t->strides[i] % 4 != 0) return false;
+  return true;
+}
+
+int64_t norm_rotate_bytes(int64_t N) { return (int64_t)kNormRotGroups * 2 * N * 4; }
+
+int validate_norm_rotate(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *q_weight,
+                         const ssd_tensor *k_weight, const ssd_tensor *freqs, const ssd_tensor *positions, float eps,
+                         int interleaved, NormRotParams *p, Args *args) {
+  if (!q) return fail(SSD_ERR_NULL, "q: descriptor is NULL");
+  if (!k) return fail(SSD_ERR_NULL, "k: descriptor is NULL");
+  if (q->ndim != 4) return fail(SSD_ERR_SHAPE, "q: rank %d, expected 4 [b,L,Hq,N]", q->ndim);
+  if (k->ndim != 4) return fail(SSD_ERR_SHAPE, "k: rank %d, expected 4 [b,L,Hk,N]", k->ndim);
+  const int64_t b = q->shape[0], L = q->shape[1], Hq = q->shape[2], N = q->shape[3], Hk = k->shape[2];
+  if (b < 1 || L < 1 || Hq < 1 || Hk < 1 || N < 1)
+    return fail(SSD_ERR_SHAPE, "empty problem: b=%lld L=%lld Hq=%lld Hk=%lld N=%lld", (long long)b, (long long)L,
+                (long long)Hq, (long long)Hk, (long long)N);
+  if (N % 8 != 0 || N > 256)
+    return fail(SSD_ERR_UNSUPPORTED, "N=%lld is not a multiple of 8 up to 256", (long long)N);
+  if (L > kMaxTokens || b > kMaxTokens || Hq > kMaxHeads || Hk > kMaxHeads || b * L > kMaxVectors ||
+      b * L * (Hq + Hk) > kMaxVectors)
+    return fail(SSD_ERR_UNSUPPORTED, "problem too large: b=%lld L=%lld Hq=%lld Hk=%lld", (long long)b, (long long)L,
+                (long long)Hq, (long long)Hk);
+  if (!(eps >= 0.f) || eps > 1e30f) return fail(SSD_ERR_UNSUPPORTED, "eps=%g is not a finite number >= 0", (double)eps);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(SSD_ERR_UNSUPPORTED, "interleaved=%d is not 0 or 1", interleaved);
+  SSD_CHECK(act_dtype(q, "q"));
+  const int64_t sq[4] = {b, L, Hq, N}, sk[4] = {b, L, Hk, N}, sw[1] = {N}, sp[2] = {b, L};
+  SSD_CHECK(check_arg(q, "q", q->dtype, 4, sq, true));
+  SSD_CHECK(check_arg(k, "k", q->dtype, 4, sk, true));
+  if (q_weight) SSD_CHECK(check_arg(q_weight, "q_weight", SSD_F32, 1, sw));
+  if (k_weight) SSD_CHECK(check_arg(k_weight, "k_weight", SSD_F32, 1, sw));
+  int64_t npair = 0;
+  if (freqs) {
+    if (freqs->ndim != 1) return fail(SSD_ERR_SHAPE, "freqs: rank %d, expected 1", freqs->ndim);
+    npair = freqs->shape[0];
+    if (npair < 1 || 2 * npair > N)
+      return fail(SSD_ERR_SHAPE, "freqs: %lld pairs do not fit in N=%lld", (long long)npair, (long long)N);
+    if (npair % 4 != 0)
+      return fail(SSD_ERR_UNSUPPORTED, "freqs: %lld pairs, not a multiple of 4", (long long)npair);
+    SSD_CHECK(check_arg(freqs, "freqs", SSD_F32, 1, &npair));
+  }
+  if (positions) {
+    if (positions->dtype != SSD_I32 && positions->dtype != SSD_I64)
+      return fail(SSD_ERR_DTYPE, "positions: dtype %s, expected i32 or i64", dtype_name(positions->dtype));
+    SSD_CHECK(check_arg(positions, "positions", positions->dtype, 2, sp));
+  }
+  args->add(q, "q", false);
+  args->add(k, "k", false);
+  args->add(q_weight, "q_weight", false);
+  args->add(k_weight, "k_weight", false);
+  args->add(freqs, "freqs", false);
+  args->add(positions, "positions", false);
+  p->q = q->data;
+  p->k = k->data;
+  p->qb = q->strides[0]; p->qt = q->strides[1]; p->qh = q->strides[2];
+  p->kb = k->strides[0]; p->kt = k->strides[1]; p->kh = k->strides[2];
+  p->qw = fptr(q_weight);
+  p->kw = fptr(k_weight);
+  p->freqs = fptr(freqs);
+  p->pos32 = positions && positions->dtype == SSD_I32 ? (const int32_t *)positions->data : nullptr;
+  p->pos64 = positions && positions->dtype == SSD_I64 ? (const int64_t *)positions->data : nullptr;
+  p->eps = eps;
+  p->L = (int)L; p->Hq = (int)Hq; p->Hk = (int)Hk; p->N = (int)N;
+  p->npair = (int)npair;
+  p->interleaved = interleaved;
+  p->ntok = b * L;
+  norm_rotate_plan(p);
+  return SSD_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -383,6 +466,68 @@ int ssd_glr_step(const ssd_tensor *state, const ssd_tensor *x, const ssd_tensor 
                    (uintptr_t)new_state->data % 16 == 0;
   const hipError_t e = launch_glr_step(x->dtype, vec, p, (hipStream_t)stream);
   return e == hipSuccess ? SSD_OK : hip_fail(e, "gated recurrence step launch");
+}
+
+int64_t ssd_norm_rotate_workspace(int64_t N) { return N >= 8 && N <= 256 && N % 8 == 0 ? norm_rotate_bytes(N) : -1; }
+
+int ssd_norm_rotate_fwd(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *q_weight,
+                        const ssd_tensor *k_weight, const ssd_tensor *freqs, const ssd_tensor *positions,
+                        ssd_tensor *q_out, ssd_tensor *k_out, float eps, int interleaved, void *stream) {
+  clear_error();
+  NormRotParams p{};
+  Args args;
+  SSD_CHECK(validate_norm_rotate(q, k, q_weight, k_weight, freqs, positions, eps, interleaved, &p, &args));
+  SSD_CHECK(check_arg(q_out, "q_out", q->dtype, 4, q->shape));
+  SSD_CHECK(check_arg(k_out, "k_out", q->dtype, 4, k->shape));
+  args.add(q_out, "q_out", true);
+  args.add(k_out, "k_out", true);
+  SSD_CHECK(args.overlaps(nullptr, nullptr));
+  SSD_CHECK(args.addressable(nullptr));
+  p.oq = q_out->data;
+  p.ok = k_out->data;
+  const bool vec = rows4(q) && rows4(k) && rows4(q_weight) && rows4(k_weight) && rows4(q_out) && rows4(k_out);
+  const hipError_t e = launch_norm_rotate(q->dtype, vec, false, p, (hipStream_t)stream);
+  return e == hipSuccess ? SSD_OK : hip_fail(e, "norm and rotation launch");
+}
+
+int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *q_weight,
+                        const ssd_tensor *k_weight, const ssd_tensor *freqs, const ssd_tensor *positions,
+                        const ssd_tensor *dq_out, const ssd_tensor *dk_out, ssd_tensor *dq, ssd_tensor *dk,
+                        ssd_tensor *dq_weight, ssd_tensor *dk_weight, float eps, int interleaved, void *workspace,
+                        int64_t workspace_bytes, void *stream) {
+  clear_error();
+  NormRotParams p{};
+  Args args;
+  SSD_CHECK(validate_norm_rotate(q, k, q_weight, k_weight, freqs, positions, eps, interleaved, &p, &args));
+  SSD_CHECK(check_arg(dq_out, "dq_out", q->dtype, 4, q->shape, true));
+  SSD_CHECK(check_arg(dk_out, "dk_out", q->dtype, 4, k->shape, true));
+  SSD_CHECK(check_arg(dq, "dq", q->dtype, 4, q->shape));
+  SSD_CHECK(check_arg(dk, "dk", q->dtype, 4, k->shape));
+  const int64_t sw[1] = {q->shape[3]};
+  if (dq_weight) SSD_CHECK(check_arg(dq_weight, "dq_weight", SSD_F32, 1, sw));
+  if (dk_weight) SSD_CHECK(check_arg(dk_weight, "dk_weight", SSD_F32, 1, sw));
+  args.add(dq_out, "dq_out", false);
+  args.add(dk_out, "dk_out", false);
+  args.add(dq, "dq", true);
+  args.add(dk, "dk", true);
+  args.add(dq_weight, "dq_weight", true);
+  args.add(dk_weight, "dk_weight", true);
+  SSD_CHECK(args.overlaps(nullptr, nullptr));
+  SSD_CHECK(args.workspace(workspace, workspace_bytes, norm_rotate_bytes(q->shape[3])));
+  SSD_CHECK(args.addressable(workspace));
+  p.dyq = dq_out->data;
+  p.dyk = dk_out->data;
+  p.dqb = dq_out->strides[0]; p.dqt = dq_out->strides[1]; p.dqh = dq_out->strides[2];
+  p.dkb = dk_out->strides[0]; p.dkt = dk_out->strides[1]; p.dkh = dk_out->strides[2];
+  p.oq = dq->data;
+  p.ok = dk->data;
+  p.dqw = fptr_out(dq_weight);
+  p.dkw = fptr_out(dk_weight);
+  p.part = (float *)workspace;
+  const bool vec = rows4(q) && rows4(k) && rows4(q_weight) && rows4(k_weight) && rows4(dq_out) && rows4(dk_out) &&
+                   rows4(dq) && rows4(dk);
+  const hipError_t e = launch_norm_rotate(q->dtype, vec, true, p, (hipStream_t)stream);
+  return e == hipSuccess ? SSD_OK : hip_fail(e, "norm and rotation backward launch");
 }
 
 } // extern "C"

@@ -93,6 +93,12 @@ def lib():
         L.ssd_glr_bwd.restype = ctypes.c_int
         L.ssd_glr_step.argtypes = [P] * 11
         L.ssd_glr_step.restype = ctypes.c_int
+        L.ssd_norm_rotate_workspace.argtypes = [I64]
+        L.ssd_norm_rotate_workspace.restype = I64
+        L.ssd_norm_rotate_fwd.argtypes = [P] * 8 + [ctypes.c_float, ctypes.c_int, P]
+        L.ssd_norm_rotate_fwd.restype = ctypes.c_int
+        L.ssd_norm_rotate_bwd.argtypes = [P] * 12 + [ctypes.c_float, ctypes.c_int, P, I64, P]
+        L.ssd_norm_rotate_bwd.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -434,6 +440,51 @@ def ssd_glr_step(state, x, r, i, A, r_bias=None, i_bias=None, *, reset=None, out
         status = lib().ssd_glr_step(*d, st)
     _check(status)
     return out
+
+
+def ssd_norm_rotate_fwd(q, k, q_weight=None, k_weight=None, freqs=None, positions=None, *,
+                        eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Norm of queries q [b, L, Hq, N] and keys k [b, L, Hk, N] (C and B of the
+    scan) for each head, then the rotation of their first 2 * len(freqs)
+    elements by position * freqs; positions [b, L] int32 or int64 (default
+    0..L-1).  Returns (q_out, k_out)."""
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    with _on_device(q):
+        st = _stream(stream, q)
+        keep, d = _descs(q, k, q_weight, k_weight, freqs, positions, q_out, k_out)
+        status = lib().ssd_norm_rotate_fwd(*d, float(eps), int(interleaved), st)
+    _check(status)
+    return q_out, k_out
+
+
+def ssd_norm_rotate_bwd(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_out, *,
+                        eps: float = 1e-6, interleaved: bool = False, want_weights: bool = True,
+                        out: dict = None, stream=None):
+    """Gradients of ssd_norm_rotate_fwd for <dq_out, q_out> + <dk_out, k_out>:
+    a dict of dq, dk (dtype of q) and, when asked for, dq_weight, dk_weight
+    (fp32).  ``out`` may hold preallocated tensors under those names."""
+    g = dict(out or {})
+    for n, t in (("dq", q), ("dk", k)):
+        if g.get(n) is None:
+            g[n] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    for n in ("dq_weight", "dk_weight"):
+        if not want_weights:
+            g[n] = None
+        elif g.get(n) is None:
+            g[n] = torch.empty((q.shape[-1],), dtype=torch.float32, device=q.device)
+    with _on_device(q):
+        st = _stream(stream, q)
+        ws = _workspace(int(lib().ssd_norm_rotate_workspace(q.shape[-1])), q, st)
+        keep, d = _descs(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_out, g["dq"], g["dk"],
+                         g["dq_weight"], g["dk_weight"])
+        status = lib().ssd_norm_rotate_bwd(*d, float(eps), int(interleaved),
+                                           ws.data_ptr() if ws is not None else None,
+                                           ws.numel() if ws is not None else 0, st)
+    _check(status)
+    return g
 
 
 def ssd_scan_plan(b, L, H, P, G, N, dtype=torch.bfloat16, cus: int = 256):
