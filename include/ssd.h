@@ -395,8 +395,8 @@ int ssd_scan_bwd_gated(const ssd_tensor *x, const ssd_tensor *dt,
  * Layout: x, r, i and dout may be strided views (slices of a fused
  * projection, broadcast batches): the last dimension contiguous, other
  * strides >= 0, the token stride at most 2^21 elements.  All other tensors are
- * dense row-major.  Pointers need the alignment of their element; rows are
- * moved 16 bytes at a time where every width, stride and pointer allows it.
+ * dense row-major.  Pointers need the alignment of their element; bf16
+ * rows of odd width, stride or alignment are moved two bytes at a time.
  *
  * Workspace: these calls take no scratch of the library's.  The caller passes
  * `workspace`, 16-byte aligned device memory of at least
@@ -411,11 +411,11 @@ int ssd_scan_bwd_gated(const ssd_tensor *x, const ssd_tensor *dt,
  * that nearly shut leaves a_t = 1 and the factor 0).  Results do not vary from
  * run to run.
  * Supported: any D in [1, 2^20], 1 <= L <= 2^24, up to 2^22 tiles of 64
- * channels by 256 tokens (128 for the gradients) over the batch.
+ * channels by 128 tokens (64 for the gradients) over the batch.
  */
 
 /* Tokens between the saved states of ssd_glr_fwd. */
-#define SSD_GLR_SEGMENT 128
+#define SSD_GLR_SEGMENT 64
 
 /* Workspace bytes of ssd_glr_fwd (backward = 0) or ssd_glr_bwd (1); -1 for a
  * shape those calls refuse.  Host only. */
@@ -470,7 +470,7 @@ int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i,
  * ssd_glr_step -- one token for every row (serving).  state [b, D] f32;
  * x, r, i [b, D]; reset [b] u8 or NULL (nonzero: the slot starts anew);
  * new_state [b, D] f32, written, may be `state`; out [b, D] dtype of x,
- * written.  b * ceil(D / 1024) at most 2^22.
+ * written.  b * ceil(D / 256) at most 2^22.
  */
 int ssd_glr_step(const ssd_tensor *state, const ssd_tensor *x,
                  const ssd_tensor *r, const ssd_tensor *i, const ssd_tensor *A,

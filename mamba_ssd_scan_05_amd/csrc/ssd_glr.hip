@@ -9,17 +9,20 @@
 // Both are chains of affine maps v -> A v + w, which compose associatively:
 // (A2, w2) after (A1, w1) is (A2 A1, A2 w1 + w2).
 //
-// Decomposition.  A workgroup owns 64 channels (128 B of a bf16 row) of one
-// batch row over one chunk of tokens.  A lane owns V channels (16 B) and T
-// successive tokens; its data is read once into registers.  The lanes' maps
-// are composed inside the wave by lane shuffles, between the waves through
-// LDS, and between the chunks through one 64-bit word per (chunk, channel)
-// in the workspace: a chunk publishes its own map as soon as it is known and
-// the finished state once its predecessor's is; a later chunk looks back over
-// kLook words at a time.  So the data crosses HBM once in each direction
-// however the time axis is split.  The fold over words always runs forward
-// from a finished state with one fma per chunk, the same operations that
-// produced the words in between, so results do not depend on timing.
+// Decomposition.  A workgroup owns 256 bytes of channels of one batch row over
+// one chunk of tokens.  A lane owns one or two channels, a wave a run of
+// successive tokens, read once into registers: the walk over them needs no
+// exchange between lanes, and what is per token (its existence, a reset, its
+// address) is per wave.  (Measured before: 16 bytes a lane with the token groups
+// of a wave composed by shuffles, b4 L4096 D5120 bf16 forward 265 us against
+// 154.)  The waves' maps are composed through LDS, and the chunks' through
+// one 64-bit word per (chunk, channel) in the workspace: a chunk publishes its
+// own map as soon as it is known and the finished state once its
+// predecessor's is; a later chunk looks back over kLook words at a time.  So
+// the data crosses HBM once in each direction however the time axis is
+// split.  The fold over words always runs forward from a finished state with
+// one fma per chunk, the same operations that produced the words in between,
+// so results do not depend on timing.
 //
 // Workgroups take their chunk from a ticket counter, chunks in time order:
 // a workgroup waits only for lower tickets, which were handed to workgroups
@@ -30,10 +33,16 @@
 namespace ssd {
 namespace {
 
-constexpr int kTile = 64; // channels of a workgroup
+
+// Waves of a workgroup, and the tokens whose decays are formed together (two
+// branches, of which a wave takes one; more at a time need more registers
+// than two workgroups a compute unit leave).
 constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kLook = 8; // words examined per look back
+constexpr int kTogether = 2;
+// Words examined per look back: fewer leave long chains waiting on each hop
+// (0.7 us), more cost traffic (b1 L32768 D2048: 1 word 362 us, 4 words 152,
+// 8 words 148, 24 words 175; b4 L4096 D5120: 162 / 162 / 166 / 210).
+constexpr int kLook = 4;
 
 // Words of the chunk chain: {A (high half), value (low half)}.  A is a
 // product of values in [0, inf) or a canonical NaN, so two other NaN
@@ -82,100 +91,86 @@ __device__ __forceinline__ float look_back(const uint64_t *prev, int64_t step, i
   }
 }
 
-template <typename T> struct Geo; // V channels per lane (16 bytes)
-template <> struct Geo<__bf16> { static constexpr int V = 8; };
-template <> struct Geo<float> { static constexpr int V = 4; };
-
-// V elements of one row.  VEC: one 16-byte access; otherwise V single ones
-// (odd widths or strides).  Reads past the resource's range give zero.
-template <typename T, bool VEC> struct Row;
-template <> struct Row<__bf16, true> {
-  i32x4 d;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    d = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
-  }
-  __device__ __forceinline__ float get(int e) const {
-    const uint32_t w = (uint32_t)d[e >> 1];
-    return __builtin_bit_cast(float, (e & 1) ? (w & 0xFFFF0000u) : (w << 16));
-  }
-};
-template <> struct Row<float, true> {
-  i32x4 d;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    d = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
-  }
-  __device__ __forceinline__ float get(int e) const {
-    const int w = d[e]; // a bit cast of the vector's element itself reads element 0
-    return __builtin_bit_cast(float, w);
-  }
-};
-template <> struct Row<__bf16, false> {
-  uint16_t d[8];
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+// V elements of one row at byte offset off (per lane) + so (per wave), in one
+// access of 2, 4 or 16 bytes.  A lane without channels passes kNowhere: its
+// reads give zero and its stores are dropped.
+constexpr uint32_t kNowhere = 0xFFFFFF00u; // past every range
+template <typename T, int V> struct Row {
+  static constexpr int kBytes = V * (int)sizeof(T);
+  static constexpr int W = kBytes < 4 ? 1 : kBytes / 4; // 32-bit words held
+  static_assert(kBytes == 2 || kBytes == 4 || kBytes == 16, "one access");
+  uint32_t d[W];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 2 * e), 0, 0);
+    for (int e = 0; e < W; ++e) d[e] = 0;
   }
-  __device__ __forceinline__ float get(int e) const { return __builtin_bit_cast(float, (uint32_t)d[e] << 16); }
-};
-template <> struct Row<float, false> {
-  int d[4];
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  // A gate of -infinity: s = 0, so a = 1 and beta = 0 whatever A and the bias
+  // are; a token that does not exist passes the state on.
+  __device__ __forceinline__ void shut() {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) d[e] = (int)__builtin_amdgcn_raw_buffer_load_b32(r, (int)(off + 4 * e), 0, 0);
+    for (int e = 0; e < W; ++e) d[e] = sizeof(T) == 4 ? 0xFF800000u : V == 1 ? 0xFF80u : 0xFF80FF80u;
   }
-  __device__ __forceinline__ float get(int e) const { return __builtin_bit_cast(float, d[e]); }
-};
-
-// Stores V values, rounded once to T; the first `n` of them if !VEC.  A lane
-// whose row or channels do not exist passes n = 0.
-constexpr uint32_t kNowhere = 0xFFFFFF00u; // an offset past every range: the store is dropped
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t off, const float *v, int n) {
-  constexpr int V = Geo<T>::V;
-  if constexpr (VEC) {
-    i32x4 d;
-    if constexpr (V == 8) {
-      bf16x8 t;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = (__bf16)v[e];
-      d = __builtin_bit_cast(i32x4, t);
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off, int so) {
+    if constexpr (W == 4) {
+      const i32x4 v = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, so, 0));
+      d[0] = (uint32_t)v[0], d[1] = (uint32_t)v[1], d[2] = (uint32_t)v[2], d[3] = (uint32_t)v[3];
+    } else if constexpr (kBytes == 4) {
+      d[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, so, 0);
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = __builtin_bit_cast(int, v[e]);
+      d[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, so, 0);
     }
-    __builtin_amdgcn_raw_buffer_store_b128(d, r, (int)(n ? off : kNowhere), 0, 0);
-  } else {
+  }
+  // Makes the value opaque here, so that nothing computed from it is moved
+  // above: the compiler otherwise unpacks every row early and runs out of
+  // registers.
+  __device__ __forceinline__ void pin() {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const uint32_t o = e < n ? off + (uint32_t)(e * sizeof(T)) : kNowhere;
-      if constexpr (V == 8)
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (__bf16)v[e]), r, (int)o, 0, 0);
-      else
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v[e]), r, (int)o, 0, 0);
+    for (int e = 0; e < W; ++e) __asm__ volatile("" : "+v"(d[e]));
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, d[e]);
+    else return __builtin_bit_cast(float, (e & 1) ? (d[e >> 1] & 0xFFFF0000u) : (d[e >> 1] << 16));
+  }
+};
+
+// Stores V values, rounded once to T.
+template <typename T, int V>
+__device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t off, int so, const float *v) {
+  constexpr int W = Row<T, V>::W;
+  if constexpr (Row<T, V>::kBytes == 2) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (__bf16)v[0]), r, (int)off, so, 0);
+  } else {
+    int d[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      if constexpr (sizeof(T) == 2) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        bf16x2 t;
+        t[0] = (__bf16)v[2 * k], t[1] = (__bf16)v[2 * k + 1];
+        d[k] = __builtin_bit_cast(int, t);
+      } else {
+        d[k] = __builtin_bit_cast(int, v[k]);
+      }
+    }
+    if constexpr (W == 4) {
+      const i32x4 t = {d[0], d[1], d[2], d[3]};
+      __builtin_amdgcn_raw_buffer_store_b128(t, r, (int)off, so, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b32(d[0], r, (int)off, so, 0);
     }
   }
 }
 
-// sigmoid(v + bias) from v and nb = -bias * log2(e).  e is capped so that
-// e * s stays finite: the backward forms 1 - s = e * s without cancellation.
-struct Sig {
-  float s, e;
-};
-__device__ __forceinline__ Sig sigmoid2(float v, float nb) {
-  Sig g;
-  g.e = fminf(hw_exp2(fmaf(v, -kLog2e, nb)), 0x1p120f);
-  g.s = __builtin_amdgcn_rcpf(1.f + g.e);
-  return g;
-}
+// sigmoid(v + bias) from v and nb = -bias * log2(e).
 __device__ __forceinline__ float sigmoid1(float v, float nb) {
   return __builtin_amdgcn_rcpf(1.f + hw_exp2(fmaf(v, -kLog2e, nb)));
 }
 
-// 1 - a^2 from l = log2(a) <= 0 and a.  Near a = 1 the subtraction cancels:
-// with y = 2 ln(a) in (-1/4, 0], -expm1(y) = -y (1 + y/2 + y^2/6 + ...) to
+// beta = sqrt(1 - a^2) from l = log2(a) and a.  Near a = 1 the subtraction
+// cancels: with y = 2 ln(a) in (-1/4, 0], 1 - a^2 = -y (1 + y/2 + y^2/6 + ...) to
 // y^6/720 (remainder below 5e-8 of the sum); elsewhere 1 - a^2 itself is good to
-// 4e-7.  Its root halves both.  For A > 0 the result is clamped at 0.
-__device__ __forceinline__ float one_minus_sq(float l, float a) {
+// 4e-7.  Its root halves both.  For A > 0 it is 0.
+__device__ __forceinline__ float beta_any(float l, float a) {
   const float y = l * (2.f * kLn2);
   float p = fmaf(y, 1.f / 720.f, 1.f / 120.f);
   p = fmaf(p, y, 1.f / 24.f);
@@ -183,48 +178,52 @@ __device__ __forceinline__ float one_minus_sq(float l, float a) {
   p = fmaf(p, y, 0.5f);
   p = fmaf(p, y, 1.f);
   const float q = y > -0.25f ? -y * p : fmaf(-a, a, 1.f);
-  return fmaxf(q, 0.f);
+  return __builtin_amdgcn_sqrtf(q < 0.f ? 0.f : q);
 }
 
-// Exclusive composition of the lanes' maps over the TG token groups of a
-// wave (lane = channel group + LPR * token group).  In: each lane's own map;
-// out: the composed map of the earlier groups (identity for the first) and, in
-// inc*, the inclusive one.  BACK runs over later groups instead.  cut: this
-// lane's tokens hold a reset, so nothing passes through it.
-template <int V, bool BACK, bool CUT>
-__device__ __forceinline__ void wave_compose(float *A, float *w, bool &cut, float *exA, float *exw, bool &excut) {
-  constexpr int LPR = 64 / V, TG = V;
-  const int lane = threadIdx.x & 63, tg = lane / LPR;
-#pragma unroll
-  for (int k = 1; k < TG; k *= 2) {
-    const bool take = BACK ? tg + k < TG : tg >= k;
-    const int src = BACK ? lane + k * LPR : lane - k * LPR;
-    bool c2 = false;
-    if constexpr (CUT) c2 = __shfl((int)cut, src & 63) != 0;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float A1 = __shfl(A[e], src & 63), w1 = __shfl(w[e], src & 63);
-      if (take && (!CUT || !cut)) {
-        w[e] = fmaf(A[e], w1, w[e]);
-        A[e] *= A1;
-      }
-    }
-    if constexpr (CUT) cut = cut || (take && c2);
+// One token's gates of one channel.  SMALL: |A| <= 1/2, so y = 2 A s > -1 and
+// beta = sqrt(-2 A) sqrt(s) g(l) with g = sqrt((1 - e^y) / -y), a fifth-degree
+// minimax polynomial in l = y / 2 ln 2 (off by 2.4e-9, evaluated to 2^-24 * 1.3);
+// sqrt(s) = 1 / sqrt(1 + e^-v) then costs no root of its own: five
+// transcendentals a token instead of six, and no selection.
+struct Chan {
+  float A2, K, nrb, nib; // A log2 e, sqrt(-2 A), -bias * log2 e
+};
+struct Gate {
+  float s, a, beta;
+};
+template <bool SMALL> __device__ __forceinline__ Gate gate_of(const Chan &c, float r) {
+  Gate g;
+  const float e1 = 1.f + hw_exp2(fmaf(r, -kLog2e, c.nrb));
+  if constexpr (SMALL) {
+    const float t = __builtin_amdgcn_rsqf(e1);
+    g.s = t * t;
+    const float l = c.A2 * g.s;
+    g.a = hw_exp2(l);
+    float p = fmaf(l, 0x1.391178p-12f, 0x1.972de2p-9f);
+    p = fmaf(p, l, 0x1.54a87ep-6f);
+    p = fmaf(p, l, 0x1.99f8aep-4f);
+    p = fmaf(p, l, 0x1.62e42p-2f);
+    p = fmaf(p, l, 1.f);
+    g.beta = c.K * t * p;
+  } else {
+    g.s = __builtin_amdgcn_rcpf(e1);
+    const float l = c.A2 * g.s;
+    g.a = hw_exp2(l);
+    g.beta = beta_any(l, g.a);
   }
-  const bool first = BACK ? tg == TG - 1 : tg == 0;
-  const int src = (BACK ? lane + LPR : lane - LPR) & 63;
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const float a1 = __shfl(A[e], src), w1 = __shfl(w[e], src);
-    exA[e] = first ? 1.f : a1;
-    exw[e] = first ? 0.f : w1;
-  }
-  excut = false;
-  if constexpr (CUT) {
-    const bool c1 = __shfl((int)cut, src) != 0;
-    excut = !first && c1;
-  }
+  return g;
 }
+__device__ __forceinline__ Chan chan_of(const float *A_, const float *rbias, const float *ibias, int c) {
+  Chan k;
+  const float A = A_[c];
+  k.A2 = A * kLog2e;
+  k.K = __builtin_amdgcn_sqrtf(fmaxf(-2.f * A, 0.f));
+  k.nrb = rbias ? -kLog2e * rbias[c] : 0.f;
+  k.nib = ibias ? -kLog2e * ibias[c] : 0.f;
+  return k;
+}
+__device__ __forceinline__ bool small_decay(float A2) { return fabsf(A2) <= 0.5f * kLog2e; }
 
 // Where this workgroup is: chunk, batch row, channel tile.
 struct Place {
@@ -264,108 +263,125 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base, in
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  Chunk of 256 tokens; T tokens per lane.  Bound by HBM (3 tensors
-// read, 1 written) with the vector ALU close behind: about 50 full-rate slots
-// an element, 24 of them in its six transcendentals.
+// Forward.  A wave takes TT successive tokens of the tile's channels, a lane V
+// of them.  Bound by HBM (3 tensors read, 1 written) with the vector ALU close
+// behind.
 // ---------------------------------------------------------------------------
-template <typename T, bool VEC, bool CUT>
-__global__ __launch_bounds__(kThreads) void glr_fwd_kernel(GlrParams p) {
-  constexpr int V = Geo<T>::V, LPR = 64 / V, TG = V, TT = kGlrChunk / (kWaves * TG), ES = (int)sizeof(T);
-  __shared__ float aggA[kWaves][kTile], aggw[kWaves][kTile], carry[kWaves][kTile];
-  __shared__ int aggcut[kWaves];
+template <typename T, int V, int NW, bool CUT>
+__global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
+  constexpr int kTile = 64 * V, TT = kGlrChunk / NW, ES = (int)sizeof(T);
+  __shared__ float aggA[NW][kTile], aggw[NW][kTile], carry[NW][kTile];
+  __shared__ int aggcut[NW];
   const Place pl = take_place(p, false);
   const int len = row_length(p, pl.row);
   const int t0 = pl.chunk * kGlrChunk;
   if (pl.chunk > 0 && t0 >= len) return; // nothing here, and nothing after it
   const int nt = min(kGlrChunk, len - t0);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tg = lane / LPR, c0 = pl.tile * kTile + (lane % LPR) * V;
-  const int nch = max(0, min(V, p.D - c0));
-  const int lt0 = (wave * TG + tg) * TT; // this lane's first token in the chunk
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c0 = pl.tile * kTile + lane * V; // V divides D: all of a lane's channels exist or none
+  const int lt0 = wave * TT, ntw = max(0, min(TT, nt - lt0)); // the wave's first token, its tokens that exist
+  const uint32_t off = c0 < p.D ? (uint32_t)(c0 * ES) : kNowhere;
 
   const __amdgpu_buffer_rsrc_t rx = rows_rsrc(p.x, pl.row * p.xb + (int64_t)t0 * p.xt, p.xt, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t rr = rows_rsrc(p.r, pl.row * p.rb_ + (int64_t)t0 * p.rt, p.rt, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t ri = rows_rsrc(p.i, pl.row * p.ib_ + (int64_t)t0 * p.it, p.it, nt, p.D, ES);
-  Row<T, VEC> dx[TT], dr[TT], di[TT];
+  Row<T, V> vx[TT], vr[TT], vi[TT];
+  if (ntw == TT) {
 #pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    dr[j].load(rr, (uint32_t)(((lt0 + j) * p.rt + c0) * ES));
-    di[j].load(ri, (uint32_t)(((lt0 + j) * p.it + c0) * ES));
-    dx[j].load(rx, (uint32_t)(((lt0 + j) * p.xt + c0) * ES));
-  }
-  bool rs[TT];
+    for (int j = 0; j < TT; ++j) {
+      vr[j].load(rr, off, (lt0 + j) * p.rt * ES);
+      vi[j].load(ri, off, (lt0 + j) * p.it * ES);
+      vx[j].load(rx, off, (lt0 + j) * p.xt * ES);
+    }
+  } else {
 #pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    rs[j] = false;
-    if constexpr (CUT)
-      if (lt0 + j < nt) rs[j] = p.reset[(int64_t)pl.row * p.L + t0 + lt0 + j] != 0;
+    for (int j = 0; j < TT; ++j) {
+      if (j < ntw) {
+        vr[j].load(rr, off, (lt0 + j) * p.rt * ES);
+        vi[j].load(ri, off, (lt0 + j) * p.it * ES);
+        vx[j].load(rx, off, (lt0 + j) * p.xt * ES);
+      } else {
+        vr[j].shut(), vi[j].zero(), vx[j].zero();
+      }
+    }
   }
-  float A2[V], nrb[V], nib[V];
+  // bit j: the wave's token j is a reset
+  uint64_t resets = 0;
+  if constexpr (CUT)
+    resets = __ballot(lane < ntw && p.reset[(int64_t)pl.row * p.L + t0 + lt0 + (lane < ntw ? lane : 0)] != 0);
+  Chan ch[V];
+  bool sm = true;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const int c = min(c0 + e, p.D - 1);
-    A2[e] = p.A[c] * kLog2e;
-    nrb[e] = p.rbias ? -kLog2e * p.rbias[c] : 0.f;
-    nib[e] = p.ibias ? -kLog2e * p.ibias[c] : 0.f;
+    ch[e] = chan_of(p.A, p.rbias, p.ibias, min(c0 + e, p.D - 1));
+    sm = sm && small_decay(ch[e].A2);
   }
 
-  // the lane's own maps
+  const bool small = __all(sm); // the same for every wave: they share the tile's channels
+
+  // the wave's own map
   float a[TT][V], b[TT][V], A[V], w[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) A[e] = 1.f, w[e] = 0.f;
-  bool cut = false;
+  constexpr int GR = TT < kTogether ? TT : kTogether;
 #pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const bool gone = lt0 + j >= nt;
+  for (int j0 = 0; j0 < TT; j0 += GR) {
+    float beta[GR][V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float l = A2[e] * sigmoid1(dr[j].get(e), nrb[e]);
-      const float al = hw_exp2(l);
-      const float q = CUT && rs[j] ? 1.f : one_minus_sq(l, al);
-      const float u = sigmoid1(di[j].get(e), nib[e]) * dx[j].get(e);
-      b[j][e] = gone ? 0.f : __builtin_amdgcn_sqrtf(q) * u;
-      a[j][e] = gone ? 1.f : al;
-      if (CUT && rs[j]) {
-        a[j][e] = 0.f;
-        A[e] = 0.f;
-        w[e] = b[j][e];
-      } else {
+    for (int j = j0; j < j0 + GR; ++j) vr[j].pin(), vi[j].pin(), vx[j].pin();
+    if (small) {
+#pragma unroll
+      for (int j = 0; j < GR; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const Gate g = gate_of<true>(ch[e], vr[j0 + j].get(e));
+          a[j0 + j][e] = g.a, beta[j][e] = g.beta;
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < GR; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const Gate g = gate_of<false>(ch[e], vr[j0 + j].get(e));
+          a[j0 + j][e] = g.a, beta[j][e] = g.beta;
+        }
+    }
+#pragma unroll
+    for (int j = j0; j < j0 + GR; ++j) {
+      const bool rs = CUT && ((resets >> j) & 1);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float u = sigmoid1(vi[j].get(e), ch[e].nib) * vx[j].get(e);
+        a[j][e] = rs ? 0.f : a[j][e];
+        b[j][e] = rs ? u : beta[j - j0][e] * u;
         A[e] *= a[j][e];
-        w[e] = fmaf(a[j][e], w[e], b[j][e]);
+        w[e] = rs ? u : fmaf(a[j][e], w[e], b[j][e]);
       }
     }
-    cut = cut || rs[j];
   }
-  float exA[V], exw[V];
-  bool excut;
-  wave_compose<V, false, CUT>(A, w, cut, exA, exw, excut);
-  if (tg == TG - 1) {
-    const int cl = (lane % LPR) * V;
 #pragma unroll
-    for (int e = 0; e < V; ++e) aggA[wave][cl + e] = A[e], aggw[wave][cl + e] = w[e];
-    if (CUT && lane == 63) aggcut[wave] = cut;
-  }
+  for (int e = 0; e < V; ++e) aggA[wave][lane * V + e] = A[e], aggw[wave][lane * V + e] = w[e];
+  if (CUT && lane == 0) aggcut[wave] = resets != 0;
   __syncthreads();
 
-  // between waves and chunks: lane = channel of the tile
-  if (wave == 0) {
-    const int c = pl.tile * kTile + lane;
+  // between waves and chunks: one thread per channel of the tile
+  if (tid < kTile) {
+    const int c = pl.tile * kTile + tid;
     const bool live = c < p.D;
     float cA = 1.f, cw = 0.f;
     bool ccut = false;
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
+    for (int v = 0; v < NW; ++v) {
       const bool k = CUT && aggcut[v];
-      cw = k ? aggw[v][lane] : fmaf(aggA[v][lane], cw, aggw[v][lane]);
-      cA *= aggA[v][lane];
+      cw = k ? aggw[v][tid] : fmaf(aggA[v][tid], cw, aggw[v][tid]);
+      cA *= aggA[v][tid];
       ccut = ccut || k;
     }
     const int last = len > 0 ? (len - 1) / kGlrChunk : 0;
     float h = 0.f;
     if (live) {
       uint64_t *word = nullptr;
-      const int64_t step = (int64_t)p.ntile * kTile;
-      if (p.words) word = p.words + ((int64_t)pl.row * p.nchunk + pl.chunk) * step + c;
+      if (p.words) word = p.words + ((int64_t)pl.row * p.nchunk + pl.chunk) * p.wstride + c;
       const bool more = pl.chunk < last;
       // A chunk with a reset hands on a finished state at once, unless the
       // final state overwrites the initial one: then "finished" also says
@@ -376,7 +392,7 @@ __global__ __launch_bounds__(kThreads) void glr_fwd_kernel(GlrParams p) {
       } else {
         if (more && early) publish(word, make_word(kFinished, cw));
         else if (more && !ccut) publish(word, make_word(decay_bits(cA), cw));
-        h = look_back(word - step, -step, pl.chunk);
+        h = look_back(word - p.wstride, -p.wstride, pl.chunk);
       }
       // the initial state has been read before anything is published
       if (p.inplace) __asm__ volatile("" ::"v"(h) : "memory");
@@ -385,79 +401,77 @@ __global__ __launch_bounds__(kThreads) void glr_fwd_kernel(GlrParams p) {
       if (p.fin && pl.chunk == last) p.fin[(int64_t)pl.row * p.D + c] = hend;
     }
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
-      carry[v][lane] = h;
-      h = CUT && aggcut[v] ? aggw[v][lane] : fmaf(aggA[v][lane], h, aggw[v][lane]);
+    for (int v = 0; v < NW; ++v) {
+      carry[v][tid] = h;
+      h = CUT && aggcut[v] ? aggw[v][tid] : fmaf(aggA[v][tid], h, aggw[v][tid]);
     }
   }
   __syncthreads();
 
-  // the states, from the one entering the lane's tokens
+  // the states, from the one entering the wave's tokens
   float h[V];
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const float hc = carry[wave][(lane % LPR) * V + e];
-    h[e] = CUT && excut ? exw[e] : fmaf(exA[e], hc, exw[e]);
-  }
-  if (p.states && lt0 % kGlrSegment == 0 && (lt0 < nt || t0 + lt0 == 0)) {
+  for (int e = 0; e < V; ++e) h[e] = carry[wave][lane * V + e];
+  if (p.states && (t0 + lt0) % kGlrSegment == 0 && (ntw > 0 || t0 + lt0 == 0)) {
     const int64_t nseg = (p.L + kGlrSegment - 1) / kGlrSegment;
     float *s = p.states + ((int64_t)pl.row * nseg + (t0 + lt0) / kGlrSegment) * p.D + c0;
+    if (c0 < p.D) {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < nch) s[e] = h[e];
+      for (int e = 0; e < V; ++e) s[e] = h[e];
+    }
   }
   if (!p.out) return;
   const __amdgpu_buffer_rsrc_t ro = rows_rsrc(p.out, ((int64_t)pl.row * p.L + t0) * p.D, p.D, nt, p.D, ES);
 #pragma unroll
-  for (int j = 0; j < TT; ++j) {
+  for (int j = 0; j < TT; ++j)
+    if (j < ntw) {
+      const bool rs = CUT && ((resets >> j) & 1);
 #pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = CUT && rs[j] ? b[j][e] : fmaf(a[j][e], h[e], b[j][e]);
-    store_row<T, VEC>(ro, (uint32_t)(((lt0 + j) * p.D + c0) * ES), h, lt0 + j < nt ? nch : 0);
-  }
+      for (int e = 0; e < V; ++e) h[e] = rs ? b[j][e] : fmaf(a[j][e], h[e], b[j][e]);
+      store_row<T, V>(ro, off, (lt0 + j) * p.D * ES, h);
+    }
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  Chunk of 128 tokens, entering state given; the chain runs from
-// the last chunk to the first.  4 tensors read, 3 written.
+// Backward.  Chunks of kGlrSegment tokens, entering state given; the chain runs
+// from the last chunk to the first.  4 tensors read, 3 written.
 // ---------------------------------------------------------------------------
-template <typename T, bool VEC, bool CUT>
-__global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
-  constexpr int V = Geo<T>::V, LPR = 64 / V, TG = V, TT = kGlrSegment / (kWaves * TG), ES = (int)sizeof(T);
-  __shared__ float fA[kWaves][kTile], fw[kWaves][kTile], bA[kWaves][kTile], bw[kWaves][kTile];
-  __shared__ float fcarry[kWaves][kTile], bcarry[kWaves][kTile];
-  __shared__ int aggcut[kWaves];
-  __shared__ float psum[kWaves * TG / 2][3][kTile];
+template <typename T, int V, int NW, bool CUT>
+__global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
+  constexpr int kTile = 64 * V, TT = kGlrSegment / NW, ES = (int)sizeof(T);
+  __shared__ float fA[NW][kTile], fw[NW][kTile], bA[NW][kTile], bw[NW][kTile];
+  __shared__ float fcarry[NW][kTile], bcarry[NW][kTile];
+  __shared__ int aggcut[NW];
   const Place pl = take_place(p, true);
   const int len = row_length(p, pl.row);
   const int t0 = pl.chunk * kGlrSegment;
   const int last = len > 0 ? (len - 1) / kGlrSegment : 0;
-  const int ntp = min(kGlrSegment, p.L - t0);        // rows of the gradients
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lt0 = wave * TT;
   const int nt = max(0, min(kGlrSegment, len - t0)); // rows that exist
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tg = lane / LPR, cl = (lane % LPR) * V, c0 = pl.tile * kTile + cl;
-  const int nch = max(0, min(V, p.D - c0));
-  const int lt0 = (wave * TG + tg) * TT;
+  const int ntw = max(0, min(TT, nt - lt0));
+  const int ntp = min(kGlrSegment, p.L - t0), ntpw = max(0, min(TT, ntp - lt0)); // rows of the gradients
+  const int c0 = pl.tile * kTile + lane * V; // V divides D: all of a lane's channels exist or none
+  const uint32_t off = c0 < p.D ? (uint32_t)(c0 * ES) : kNowhere;
   const int64_t prow = ((int64_t)pl.row * p.nchunk + pl.chunk) * 3 * p.D; // row of the partial sums
   const int64_t g0 = ((int64_t)pl.row * p.L + t0) * p.D;
   const __amdgpu_buffer_rsrc_t odx = rows_rsrc(p.dx, g0, p.D, ntp, p.D, ES);
   const __amdgpu_buffer_rsrc_t odr = rows_rsrc(p.dr, g0, p.D, ntp, p.D, ES);
   const __amdgpu_buffer_rsrc_t odi = rows_rsrc(p.di, g0, p.D, ntp, p.D, ES);
+  float zero[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) zero[e] = 0.f;
 
-  if (pl.chunk > last) { // behind the row's length: zero gradients
-    float z[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) z[e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      const uint32_t off = (uint32_t)(((lt0 + j) * p.D + c0) * ES);
-      const int n = lt0 + j < ntp ? nch : 0;
-      store_row<T, VEC>(odx, off, z, n);
-      store_row<T, VEC>(odr, off, z, n);
-      store_row<T, VEC>(odi, off, z, n);
-    }
-    if (tid < 3 * kTile) {
-      const int c = pl.tile * kTile + tid % kTile;
-      if (c < p.D) p.part[prow + (int64_t)(tid / kTile) * p.D + c] = 0.f;
+  // behind the row's length: zero gradients
+  for (int j = ntw; j < ntpw; ++j) {
+    store_row<T, V>(odx, off, (lt0 + j) * p.D * ES, zero);
+    store_row<T, V>(odr, off, (lt0 + j) * p.D * ES, zero);
+    store_row<T, V>(odi, off, (lt0 + j) * p.D * ES, zero);
+  }
+  if (pl.chunk > last) {
+    for (int k = tid; k < 3 * kTile; k += 64 * NW) {
+      const int c = pl.tile * kTile + k % kTile;
+      if (c < p.D) p.part[prow + (int64_t)(k / kTile) * p.D + c] = 0.f;
     }
     return;
   }
@@ -466,195 +480,197 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrParams p) {
   const __amdgpu_buffer_rsrc_t rr = rows_rsrc(p.r, pl.row * p.rb_ + (int64_t)t0 * p.rt, p.rt, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t ri = rows_rsrc(p.i, pl.row * p.ib_ + (int64_t)t0 * p.it, p.it, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t rd = rows_rsrc(p.dout, pl.row * p.db + (int64_t)t0 * p.dt, p.dt, nt, p.D, ES);
-  Row<T, VEC> vx[TT], vr[TT], vi[TT], vd[TT];
+  Row<T, V> vx[TT], vr[TT], vi[TT], vd[TT];
+  if (ntw == TT) {
 #pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    vr[j].load(rr, (uint32_t)(((lt0 + j) * p.rt + c0) * ES));
-    vi[j].load(ri, (uint32_t)(((lt0 + j) * p.it + c0) * ES));
-    vx[j].load(rx, (uint32_t)(((lt0 + j) * p.xt + c0) * ES));
-    // zero behind the row's length (a token stride of 0 stays in range there)
-    vd[j].load(rd, lt0 + j < nt ? (uint32_t)(((lt0 + j) * p.dt + c0) * ES) : kNowhere);
-  }
-  bool rs[TT];
+    for (int j = 0; j < TT; ++j) {
+      vr[j].load(rr, off, (lt0 + j) * p.rt * ES);
+      vi[j].load(ri, off, (lt0 + j) * p.it * ES);
+      vx[j].load(rx, off, (lt0 + j) * p.xt * ES);
+      vd[j].load(rd, off, (lt0 + j) * p.dt * ES);
+    }
+  } else {
 #pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    rs[j] = false;
-    if constexpr (CUT)
-      if (lt0 + j < nt) rs[j] = p.reset[(int64_t)pl.row * p.L + t0 + lt0 + j] != 0;
-  }
-  float Ac[V], nrb[V], nib[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const int c = min(c0 + e, p.D - 1);
-    Ac[e] = p.A[c];
-    nrb[e] = p.rbias ? -kLog2e * p.rbias[c] : 0.f;
-    nib[e] = p.ibias ? -kLog2e * p.ibias[c] : 0.f;
-  }
-
-  // ir = 1 / beta (0 where beta is 0), so beta = q ir
-  float a[TT][V], q[TT][V], ir[TT][V];
-  float A[V], w[V], Ab[V], wb[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) A[e] = 1.f, w[e] = 0.f, wb[e] = 0.f;
-  bool cut = false;
-#pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const bool gone = lt0 + j >= nt;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float l = Ac[e] * kLog2e * sigmoid1(vr[j].get(e), nrb[e]);
-      const float al = hw_exp2(l);
-      q[j][e] = CUT && rs[j] ? 1.f : one_minus_sq(l, al);
-      if (gone) q[j][e] = 0.f;
-      ir[j][e] = q[j][e] > 0.f ? __builtin_amdgcn_rsqf(q[j][e]) : 0.f;
-      a[j][e] = gone ? 1.f : al;
-      const float b = q[j][e] * ir[j][e] * sigmoid1(vi[j].get(e), nib[e]) * vx[j].get(e);
-      if (CUT && rs[j]) {
-        a[j][e] = 0.f;
-        A[e] = 0.f;
-        w[e] = b;
+    for (int j = 0; j < TT; ++j) {
+      if (j < ntw) {
+        vr[j].load(rr, off, (lt0 + j) * p.rt * ES);
+        vi[j].load(ri, off, (lt0 + j) * p.it * ES);
+        vx[j].load(rx, off, (lt0 + j) * p.xt * ES);
+        vd[j].load(rd, off, (lt0 + j) * p.dt * ES);
       } else {
-        A[e] *= a[j][e];
-        w[e] = fmaf(a[j][e], w[e], b);
+        vr[j].shut(), vi[j].zero(), vx[j].zero(), vd[j].zero();
       }
     }
-    cut = cut || rs[j];
+  }
+  uint64_t resets = 0;
+  if constexpr (CUT)
+    resets = __ballot(lane < ntw && p.reset[(int64_t)pl.row * p.L + t0 + lt0 + (lane < ntw ? lane : 0)] != 0);
+  Chan ch[V];
+  bool sm = true;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    ch[e] = chan_of(p.A, p.rbias, p.ibias, min(c0 + e, p.D - 1));
+    sm = sm && small_decay(ch[e].A2);
+  }
+
+  const bool small = __all(sm); // the same for every wave: they share the tile's channels
+
+  // decay, factor and input of every token; the wave's map
+  float a[TT][V], be[TT][V], b[TT][V], A[V], w[V], wb[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) A[e] = 1.f, w[e] = 0.f, wb[e] = 0.f;
+  constexpr int GR = TT < kTogether ? TT : kTogether;
+#pragma unroll
+  for (int j0 = 0; j0 < TT; j0 += GR) {
+#pragma unroll
+    for (int j = j0; j < j0 + GR; ++j) vr[j].pin(), vi[j].pin(), vx[j].pin();
+    if (small) {
+#pragma unroll
+      for (int j = j0; j < j0 + GR; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const Gate g = gate_of<true>(ch[e], vr[j].get(e));
+          a[j][e] = g.a, be[j][e] = g.beta;
+        }
+    } else {
+#pragma unroll
+      for (int j = j0; j < j0 + GR; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const Gate g = gate_of<false>(ch[e], vr[j].get(e));
+          a[j][e] = g.a, be[j][e] = g.beta;
+        }
+    }
+#pragma unroll
+    for (int j = j0; j < j0 + GR; ++j) {
+      const bool rs = CUT && ((resets >> j) & 1);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (rs) a[j][e] = 0.f, be[j][e] = 1.f;
+        b[j][e] = be[j][e] * (sigmoid1(vi[j].get(e), ch[e].nib) * vx[j].get(e));
+        A[e] *= a[j][e];
+        w[e] = rs ? b[j][e] : fmaf(a[j][e], w[e], b[j][e]);
+      }
+    }
   }
 #pragma unroll
-  for (int j = TT - 1; j >= 0; --j)
+  for (int j = TT - 1; j >= 0; --j) {
+    const bool rs = CUT && ((resets >> j) & 1);
 #pragma unroll
-    for (int e = 0; e < V; ++e) wb[e] = CUT && rs[j] ? 0.f : a[j][e] * (vd[j].get(e) + wb[e]);
-#pragma unroll
-  for (int e = 0; e < V; ++e) Ab[e] = A[e];
-  float fexA[V], fexw[V], bexA[V], bexw[V];
-  bool fexcut, bexcut, cutb = cut;
-  wave_compose<V, false, CUT>(A, w, cut, fexA, fexw, fexcut);
-  wave_compose<V, true, CUT>(Ab, wb, cutb, bexA, bexw, bexcut);
-  if (tg == TG - 1) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) fA[wave][cl + e] = A[e], fw[wave][cl + e] = w[e];
-    if (CUT && lane == 63) aggcut[wave] = cut;
+    for (int e = 0; e < V; ++e) wb[e] = rs ? 0.f : a[j][e] * (vd[j].get(e) + wb[e]);
   }
-  if (tg == 0) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) bA[wave][cl + e] = Ab[e], bw[wave][cl + e] = wb[e];
+  for (int e = 0; e < V; ++e) {
+    fA[wave][lane * V + e] = A[e], fw[wave][lane * V + e] = w[e];
+    bw[wave][lane * V + e] = wb[e];
   }
+  if (CUT && lane == 0) aggcut[wave] = resets != 0;
   __syncthreads();
 
-  if (wave == 0) {
-    const int c = pl.tile * kTile + lane;
+  if (tid < kTile) {
+    const int c = pl.tile * kTile + tid;
     const bool live = c < p.D;
     float cA = 1.f, cw = 0.f;
     bool ccut = false;
 #pragma unroll
-    for (int v = kWaves - 1; v >= 0; --v) {
+    for (int v = NW - 1; v >= 0; --v) {
       const bool k = CUT && aggcut[v];
-      cw = k ? bw[v][lane] : fmaf(bA[v][lane], cw, bw[v][lane]);
-      cA *= bA[v][lane];
+      cw = k ? bw[v][tid] : fmaf(fA[v][tid], cw, bw[v][tid]);
+      cA *= fA[v][tid];
       ccut = ccut || k;
     }
     float cin = 0.f, h = 0.f;
     if (live) {
-      const int64_t nseg = (p.L + kGlrSegment - 1) / kGlrSegment;
       uint64_t *word = nullptr;
-      const int64_t step = (int64_t)p.ntile * kTile;
-      if (p.words) word = p.words + ((int64_t)pl.row * p.nchunk + pl.chunk) * step + c;
+      if (p.words) word = p.words + ((int64_t)pl.row * p.nchunk + pl.chunk) * p.wstride + c;
       const bool more = pl.chunk > 0;
+      h = p.states[((int64_t)pl.row * p.nchunk + pl.chunk) * p.D + c];
       if (pl.chunk == last) {
         cin = p.dfin ? p.dfin[(int64_t)pl.row * p.D + c] : 0.f;
       } else {
         if (more) publish(word, ccut ? make_word(kFinished, cw) : make_word(decay_bits(cA), cw));
-        cin = look_back(word + step, step, last - pl.chunk);
+        cin = look_back(word + p.wstride, p.wstride, last - pl.chunk);
       }
       const float cend = ccut ? cw : fmaf(cA, cin, cw);
       if (more && !(ccut && pl.chunk != last)) publish(word, make_word(kFinished, cend));
       if (p.dinit && pl.chunk == 0) p.dinit[(int64_t)pl.row * p.D + c] = cend;
-      h = p.states[((int64_t)pl.row * nseg + pl.chunk) * p.D + c];
     }
 #pragma unroll
-    for (int v = kWaves - 1; v >= 0; --v) {
-      bcarry[v][lane] = cin;
-      cin = CUT && aggcut[v] ? bw[v][lane] : fmaf(bA[v][lane], cin, bw[v][lane]);
+    for (int v = NW - 1; v >= 0; --v) {
+      bcarry[v][tid] = cin;
+      cin = CUT && aggcut[v] ? bw[v][tid] : fmaf(fA[v][tid], cin, bw[v][tid]);
     }
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
-      fcarry[v][lane] = h;
-      h = CUT && aggcut[v] ? fw[v][lane] : fmaf(fA[v][lane], h, fw[v][lane]);
+    for (int v = 0; v < NW; ++v) {
+      fcarry[v][tid] = h;
+      h = CUT && aggcut[v] ? fw[v][tid] : fmaf(fA[v][tid], h, fw[v][tid]);
     }
   }
   __syncthreads();
 
-  float hp[TT][V], c[V];
+  // the states before each token, in the place of the inputs
+  float c[V], sA[V], sr[V], si[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float hc = fcarry[wave][cl + e], cc = bcarry[wave][cl + e];
-    float h = CUT && fexcut ? fexw[e] : fmaf(fexA[e], hc, fexw[e]);
-    c[e] = CUT && bexcut ? bexw[e] : fmaf(bexA[e], cc, bexw[e]);
+    float h = fcarry[wave][lane * V + e];
+    c[e] = bcarry[wave][lane * V + e];
+    sA[e] = sr[e] = si[e] = 0.f;
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
-      hp[j][e] = h;
-      if (j + 1 < TT) {
-        const float b = q[j][e] * ir[j][e] * sigmoid1(vi[j].get(e), nib[e]) * vx[j].get(e);
-        h = CUT && rs[j] ? b : fmaf(a[j][e], h, b);
-      }
+      const float n = CUT && ((resets >> j) & 1) ? b[j][e] : fmaf(a[j][e], h, b[j][e]);
+      b[j][e] = h;
+      h = n;
     }
   }
-  float sA[V], sr[V], si[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) sA[e] = sr[e] = si[e] = 0.f;
+  // the gates once more: less than it costs to keep them
 #pragma unroll
   for (int j = TT - 1; j >= 0; --j) {
+    if (j >= ntw) continue; // passes c on and adds nothing to the sums
     float ox[V], orr[V], oi[V];
-    const bool gone = lt0 + j >= nt;
+    const bool rs = CUT && ((resets >> j) & 1);
+    vr[j].pin(), vi[j].pin(), vx[j].pin(), vd[j].pin();
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float g = vd[j].get(e) + c[e];
-      const Sig s = sigmoid2(vr[j].get(e), nrb[e]), gi = sigmoid2(vi[j].get(e), nib[e]);
-      const float x = vx[j].get(e), ak = a[j][e];
-      const float beta = q[j][e] * ir[j][e];
-      const float gb = g * beta * gi.s;                 // dx
-      const float dl = g * ak * (hp[j][e] - ak * (gi.s * x) * ir[j][e]); // at log a
-      ox[e] = gb;
-      oi[e] = gb * x * (gi.e * gi.s);
-      orr[e] = dl * Ac[e] * s.s * (s.e * s.s);
-      float da = dl * s.s;
-      c[e] = ak * g;
-      if (CUT && rs[j]) orr[e] = 0.f, da = 0.f, c[e] = 0.f;
-      if (gone) {
-        ox[e] = orr[e] = oi[e] = da = 0.f;
-        c[e] = g;
-      }
-      sA[e] += da;
+      // capped, so that 1 - s = e s and 1 - gi = e gi stay finite
+      const float er = fminf(hw_exp2(fmaf(vr[j].get(e), -kLog2e, ch[e].nrb)), 0x1p120f);
+      const float ei = fminf(hw_exp2(fmaf(vi[j].get(e), -kLog2e, ch[e].nib)), 0x1p120f);
+      const float sg = __builtin_amdgcn_rcpf(1.f + er), gi = __builtin_amdgcn_rcpf(1.f + ei);
+      const float x = vx[j].get(e), ak = a[j][e], beta = be[j][e];
+      const float rb = beta > 0.f ? __builtin_amdgcn_rcpf(beta) : 0.f;
+      const float ag = ak * g;
+      const float dl = ag * fmaf(-ak * (gi * x), rb, b[j][e]); // at log a
+      ox[e] = g * beta * gi;
+      oi[e] = ox[e] * x * (ei * gi);
+      float ds = dl * sg;
+      orr[e] = ds * (er * sg) * (ch[e].A2 * kLn2);
+      c[e] = ag;
+      if (CUT && rs) orr[e] = ds = c[e] = 0.f;
+      sA[e] += ds;
       sr[e] += orr[e];
       si[e] += oi[e];
     }
-    const uint32_t off = (uint32_t)(((lt0 + j) * p.D + c0) * ES);
-    const int n = lt0 + j < ntp ? nch : 0;
-    store_row<T, VEC>(odx, off, ox, n);
-    store_row<T, VEC>(odr, off, orr, n);
-    store_row<T, VEC>(odi, off, oi, n);
+    store_row<T, V>(odx, off, (lt0 + j) * p.D * ES, ox);
+    store_row<T, V>(odr, off, (lt0 + j) * p.D * ES, orr);
+    store_row<T, V>(odi, off, (lt0 + j) * p.D * ES, oi);
   }
-  // parameter gradients: pairs of token groups by shuffle, the rest in LDS
-  // in a fixed order
+  // parameter gradients: the waves' sums in a fixed order (fA, fw and bA are
+  // read no more once every wave has its carries)
+  __syncthreads();
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    sA[e] += __shfl_xor(sA[e], LPR);
-    sr[e] += __shfl_xor(sr[e], LPR);
-    si[e] += __shfl_xor(si[e], LPR);
-    if ((tg & 1) == 0) {
-      const int k = wave * (TG / 2) + tg / 2;
-      psum[k][0][cl + e] = sA[e];
-      psum[k][1][cl + e] = sr[e];
-      psum[k][2][cl + e] = si[e];
-    }
+    fA[wave][lane * V + e] = sA[e];
+    fw[wave][lane * V + e] = sr[e];
+    bA[wave][lane * V + e] = si[e];
   }
   __syncthreads();
-  if (tid < 3 * kTile) {
-    const int ch = tid % kTile, what = tid / kTile;
+  for (int k = tid; k < 3 * kTile; k += 64 * NW) {
+    const int cl = k % kTile, what = k / kTile;
+    const float (*src)[kTile] = what == 0 ? fA : what == 1 ? fw : bA;
     float s = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < kWaves * TG / 2; ++k) s += psum[k][what][ch];
-    if (pl.tile * kTile + ch < p.D) p.part[prow + (int64_t)what * p.D + pl.tile * kTile + ch] = s;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) s += src[v][cl];
+    if (pl.tile * kTile + cl < p.D) p.part[prow + (int64_t)what * p.D + pl.tile * kTile + cl] = s;
   }
 }
 
@@ -688,74 +704,74 @@ __global__ __launch_bounds__(256) void glr_fill_kernel(uint4 *p, int64_t n) {
 
 // One token: V channels per lane; bound by the launch at small batches and by
 // HBM (the fp32 state in and out) at large ones.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void glr_step_kernel(GlrStepParams p) {
-  constexpr int V = Geo<T>::V, ES = (int)sizeof(T);
+template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_kernel(GlrStepParams p) {
+  constexpr int ES = (int)sizeof(T);
   const int row = (int)(blockIdx.x / (uint32_t)p.nblk);
   const int c0 = ((int)(blockIdx.x - (uint32_t)row * (uint32_t)p.nblk) * 256 + (int)threadIdx.x) * V;
   if (c0 >= p.D) return;
-  const int nch = min(V, p.D - c0);
-  Row<T, VEC> vr, vi, vx;
-  vr.load(rows_rsrc(p.r, row * p.rb_, 0, 1, p.D, ES), (uint32_t)(c0 * ES));
-  vi.load(rows_rsrc(p.i, row * p.ib_, 0, 1, p.D, ES), (uint32_t)(c0 * ES));
-  vx.load(rows_rsrc(p.x, row * p.xb, 0, 1, p.D, ES), (uint32_t)(c0 * ES));
+  Row<T, V> vr, vi, vx;
+  vr.load(rows_rsrc(p.r, row * p.rb_, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0);
+  vi.load(rows_rsrc(p.i, row * p.ib_, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0);
+  vx.load(rows_rsrc(p.x, row * p.xb, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0);
   const bool rs = p.reset && p.reset[row] != 0;
   const float *st = p.state + (int64_t)row * p.D + c0;
   float *ns = p.new_state + (int64_t)row * p.D + c0;
   float h[V];
-  if constexpr (VEC) {
+  if constexpr (V > 1) {
 #pragma unroll
     for (int e = 0; e < V; e += 4) {
       const float4 v = *reinterpret_cast<const float4 *>(st + e);
       h[e] = v.x, h[e + 1] = v.y, h[e + 2] = v.z, h[e + 3] = v.w;
     }
   } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = e < nch ? st[e] : 0.f;
+    h[0] = st[0];
   }
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const int c = min(c0 + e, p.D - 1);
-    const float l = p.A[c] * kLog2e * sigmoid1(vr.get(e), p.rbias ? -kLog2e * p.rbias[c] : 0.f);
-    const float a = hw_exp2(l);
-    const float u = sigmoid1(vi.get(e), p.ibias ? -kLog2e * p.ibias[c] : 0.f) * vx.get(e);
-    h[e] = rs ? u : fmaf(a, h[e], __builtin_amdgcn_sqrtf(one_minus_sq(l, a)) * u);
+    const Chan ch = chan_of(p.A, p.rbias, p.ibias, c0 + e);
+    const Gate g = gate_of<false>(ch, vr.get(e));
+    const float u = sigmoid1(vi.get(e), ch.nib) * vx.get(e);
+    h[e] = rs ? u : fmaf(g.a, h[e], g.beta * u);
   }
-  if constexpr (VEC) {
+  if constexpr (V > 1) {
 #pragma unroll
     for (int e = 0; e < V; e += 4) *reinterpret_cast<float4 *>(ns + e) = make_float4(h[e], h[e + 1], h[e + 2], h[e + 3]);
   } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < nch) ns[e] = h[e];
+    ns[0] = h[0];
   }
-  store_row<T, VEC>(rows_rsrc(p.out, (int64_t)row * p.D, 0, 1, p.D, ES), (uint32_t)(c0 * ES), h, nch);
+  store_row<T, V>(rows_rsrc(p.out, (int64_t)row * p.D, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0, h);
 }
 
-template <typename T, bool VEC, bool CUT>
-hipError_t scan_launch(bool back, const GlrParams &p, hipStream_t st) {
+template <typename T, int V> hipError_t scan_launch(bool back, const GlrParams &p, hipStream_t st) {
   const dim3 grid((uint32_t)p.b * (uint32_t)p.ntile * (uint32_t)p.nchunk);
-  if (back) glr_bwd_kernel<T, VEC, CUT><<<grid, kThreads, 0, st>>>(p);
-  else glr_fwd_kernel<T, VEC, CUT><<<grid, kThreads, 0, st>>>(p);
+  if (p.reset) {
+    if (back) glr_bwd_kernel<T, V, kWaves, true><<<grid, 64 * kWaves, 0, st>>>(p);
+    else glr_fwd_kernel<T, V, kWaves, true><<<grid, 64 * kWaves, 0, st>>>(p);
+  } else {
+    if (back) glr_bwd_kernel<T, V, kWaves, false><<<grid, 64 * kWaves, 0, st>>>(p);
+    else glr_fwd_kernel<T, V, kWaves, false><<<grid, 64 * kWaves, 0, st>>>(p);
+  }
   return hipGetLastError();
 }
 
 } // namespace
 
-hipError_t launch_glr(int dtype, bool vec, bool back, const GlrParams &p, hipStream_t st) {
+// Four bytes a lane (256 of a row per workgroup) where bf16 rows allow it;
+// two where the width, a stride or a pointer is odd.
+hipError_t launch_glr(int dtype, bool vec, bool back, const GlrParams &p0, hipStream_t st) {
+  GlrParams p = p0;
+  const int V = dtype == 1 && vec ? 2 : 1;
+  p.ntile = (p.D + 64 * V - 1) / (64 * V);
   if (p.words) {
     // words and the ticket behind them, in 16-byte pieces
-    const int64_t n = glr_chain_bytes(p.b, p.nchunk, p.ntile) / 16;
+    const int64_t n = glr_chain_bytes(p.b, p.nchunk, p.D) / 16;
     const int64_t blocks = (n + 255) / 256;
     glr_fill_kernel<<<(uint32_t)(blocks < 2048 ? blocks : 2048), 256, 0, st>>>((uint4 *)p.words, n);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const bool cut = p.reset != nullptr;
-#define SSD_GLR(T, VEC) (cut ? scan_launch<T, VEC, true>(back, p, st) : scan_launch<T, VEC, false>(back, p, st))
-  if (dtype == 1) return vec ? SSD_GLR(__bf16, true) : SSD_GLR(__bf16, false);
-  return vec ? SSD_GLR(float, true) : SSD_GLR(float, false);
-#undef SSD_GLR
+  if (dtype != 1) return scan_launch<float, 1>(back, p, st);
+  return vec ? scan_launch<__bf16, 2>(back, p, st) : scan_launch<__bf16, 1>(back, p, st);
 }
 
 hipError_t launch_glr_sum(const float *part, int n, int D, float *dA, float *drb, float *dib, hipStream_t st) {
@@ -764,16 +780,16 @@ hipError_t launch_glr_sum(const float *part, int n, int D, float *dA, float *drb
 }
 
 hipError_t launch_glr_step(int dtype, bool vec, const GlrStepParams &p0, hipStream_t st) {
-  const int V = dtype == 1 ? 8 : 4;
+  const int V = !vec ? 1 : dtype == 1 ? 8 : 4;
   GlrStepParams p = p0;
   p.nblk = (p.D + 256 * V - 1) / (256 * V);
-  const dim3 grid((uint32_t)p.nblk * (uint32_t)p.b);
+  const uint32_t grid = (uint32_t)p.nblk * (uint32_t)p.b;
   if (dtype == 1) {
-    if (vec) glr_step_kernel<__bf16, true><<<grid, 256, 0, st>>>(p);
-    else glr_step_kernel<__bf16, false><<<grid, 256, 0, st>>>(p);
+    if (vec) glr_step_kernel<__bf16, 8><<<grid, 256, 0, st>>>(p);
+    else glr_step_kernel<__bf16, 1><<<grid, 256, 0, st>>>(p);
   } else {
-    if (vec) glr_step_kernel<float, true><<<grid, 256, 0, st>>>(p);
-    else glr_step_kernel<float, false><<<grid, 256, 0, st>>>(p);
+    if (vec) glr_step_kernel<float, 4><<<grid, 256, 0, st>>>(p);
+    else glr_step_kernel<float, 1><<<grid, 256, 0, st>>>(p);
   }
   return hipGetLastError();
 }

@@ -169,10 +169,10 @@ hipError_t launch_gate_bwd(int dtype, const void *y, const void *z, const void *
                            int64_t n, hipStream_t stream);
 
 // The gated linear recurrence.  A workgroup of the forward takes kGlrChunk
-// tokens of 64 channels, one of the backward kGlrSegment tokens (the spacing
-// of the saved states).
-constexpr int kGlrChunk = 256;
-constexpr int kGlrSegment = 128; // SSD_GLR_SEGMENT
+// tokens, one of the backward kGlrSegment tokens (the spacing of the saved
+// states), of 64 or 128 channels.
+constexpr int kGlrChunk = 128;
+constexpr int kGlrSegment = 64; // SSD_GLR_SEGMENT
 struct GlrParams {
   const void *x, *r, *i, *dout;          // [b, L, D], last dim contiguous
   int64_t xb, rb_, ib_, db;              // batch strides, elements
@@ -188,14 +188,18 @@ struct GlrParams {
   void *dx, *dr, *di;                    // [b, L, D] dense
   float *dinit;                          // [b, D] or null
   float *part;                           // [b, nchunk, 3, D]
-  uint64_t *words;                       // chain words [b, nchunk, ntile*64], null if nchunk == 1
+  uint64_t *words;                       // chain words [b, nchunk, wstride], null if nchunk == 1
   uint32_t *ticket;                      // behind the words
-  int b, L, D, nchunk, ntile;
+  int64_t wstride;
+  int b, L, D, nchunk;
+  int ntile; // set by the launch
   int inplace;
 };
-// Bytes of the chain words and the ticket behind them.
-inline int64_t glr_chain_bytes(int64_t b, int64_t nchunk, int64_t ntile) { return b * nchunk * ntile * 512 + 16; }
-// dtype 1 = bf16, 0 = fp32; vec: widths, strides and pointers allow 16-byte rows.
+// Words of a chunk, bytes of the chain words and the ticket behind them.
+inline int64_t glr_wstride(int64_t D) { return (D + 127) / 128 * 128; }
+inline int64_t glr_chain_bytes(int64_t b, int64_t nchunk, int64_t D) { return b * nchunk * glr_wstride(D) * 8 + 16; }
+// dtype 1 = bf16, 0 = fp32; vec: bf16 widths, strides and pointers allow 4-byte
+// accesses.
 hipError_t launch_glr(int dtype, bool vec, bool back, const GlrParams &p, hipStream_t stream);
 // Sums n partial rows [3][D] into dA, d r_bias, d i_bias (each may be null).
 hipError_t launch_glr_sum(const float *part, int n, int D, float *dA, float *drb, float *dib, hipStream_t stream);

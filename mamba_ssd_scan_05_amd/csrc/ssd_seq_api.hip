@@ -145,12 +145,12 @@ struct GlrPlan {
 };
 bool glr_plan(int64_t b, int64_t L, int64_t D, bool back, GlrPlan *q) {
   if (b < 1 || L < 1 || D < 1 || L > kMaxTokens || D > kMaxWidth || b > kMaxTiles) return false;
-  q->ntile = (D + 63) / 64;
+  q->ntile = (D + 63) / 64; // of the narrower tiles
   q->nfwd = (L + kGlrChunk - 1) / kGlrChunk;
   q->nseg = (L + kGlrSegment - 1) / kGlrSegment;
   if (b * q->ntile > kMaxTiles || b * q->ntile * (back ? q->nseg : q->nfwd) > kMaxTiles) return false;
-  q->chain_f = q->nfwd > 1 ? glr_chain_bytes(b, q->nfwd, q->ntile) : 0;
-  q->chain_b = q->nseg > 1 ? glr_chain_bytes(b, q->nseg, q->ntile) : 0;
+  q->chain_f = q->nfwd > 1 ? glr_chain_bytes(b, q->nfwd, D) : 0;
+  q->chain_b = q->nseg > 1 ? glr_chain_bytes(b, q->nseg, D) : 0;
   q->part = b * q->nseg * 3 * D * 4;
   q->state = b * q->nseg * D * 4;
   return true;
@@ -215,24 +215,26 @@ GlrParams glr_params(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor 
   p.lengths = lengths ? (const int32_t *)lengths->data : nullptr;
   p.init = fptr(init_state);
   p.b = (int)x->shape[0]; p.L = (int)x->shape[1]; p.D = (int)x->shape[2];
-  p.ntile = (int)plan.ntile;
+  p.wstride = glr_wstride(p.D);
   return p;
 }
 
-// 16-byte rows: the width, the strides that are used and the pointers are
-// multiples of 16 bytes.
-bool rows16(const ssd_tensor *t) {
-  const int V = 16 / elem_size(t->dtype), n = t->ndim;
-  if ((uintptr_t)t->data % 16 != 0 || t->shape[n - 1] % V != 0) return false;
+// Rows in pieces of `bytes`: the width, the strides that are used and the
+// pointers are multiples of them.
+bool rows_of(const ssd_tensor *t, int bytes) {
+  const int V = bytes / elem_size(t->dtype), n = t->ndim;
+  if ((uintptr_t)t->data % (uintptr_t)bytes != 0 || t->shape[n - 1] % V != 0) return false;
   for (int i = 0; i < n - 1; ++i)
     if (t->shape[i] != 1 && t->strides[i] % V != 0) return false;
   return true;
 }
+bool rows4b(const ssd_tensor *t) { return rows_of(t, 4); }
+bool rows16(const ssd_tensor *t) { return rows_of(t, 16); }
 
 void set_chain(GlrParams *p, int64_t nchunk, void *ws) {
   p->nchunk = (int)nchunk;
   p->words = nchunk > 1 ? (uint64_t *)ws : nullptr;
-  p->ticket = nchunk > 1 ? (uint32_t *)((char *)ws + glr_chain_bytes(p->b, nchunk, p->ntile) - 16) : nullptr;
+  p->ticket = nchunk > 1 ? (uint32_t *)((char *)ws + glr_chain_bytes(p->b, nchunk, p->D) - 16) : nullptr;
 }
 
 // ---------------------------------------------------------------------------
@@ -349,7 +351,7 @@ int ssd_glr_fwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, c
   p.states = fptr_out(states);
   p.inplace = final_state && init_state && final_state->data == init_state->data;
   set_chain(&p, plan.nfwd, workspace);
-  const bool vec = rows16(x) && rows16(r) && rows16(i) && rows16(out);
+  const bool vec = rows4b(x) && rows4b(r) && rows4b(i) && rows4b(out);
   const hipError_t e = launch_glr(x->dtype, vec, false, p, (hipStream_t)stream);
   return e == hipSuccess ? SSD_OK : hip_fail(e, "gated recurrence launch");
 }
@@ -393,7 +395,7 @@ int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, c
   char *ws = (char *)workspace;
   p.part = (float *)(ws + up256(plan.chain_f > plan.chain_b ? plan.chain_f : plan.chain_b));
   hipStream_t st = (hipStream_t)stream;
-  const bool vec = rows16(x) && rows16(r) && rows16(i);
+  const bool vec = rows4b(x) && rows4b(r) && rows4b(i);
   hipError_t e;
   if (states) {
     p.states = (float *)states->data;
@@ -410,7 +412,7 @@ int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, c
   p.dx = dx->data; p.dr = dr->data; p.di = di->data;
   p.dinit = fptr_out(dinit_state);
   set_chain(&p, plan.nseg, ws);
-  e = launch_glr(x->dtype, vec && rows16(dout) && rows16(dx) && rows16(dr) && rows16(di), true, p, st);
+  e = launch_glr(x->dtype, vec && rows4b(dout) && rows4b(dx) && rows4b(dr) && rows4b(di), true, p, st);
   if (e != hipSuccess) return hip_fail(e, "gated recurrence backward launch");
   e = launch_glr_sum(p.part, (int)(b * plan.nseg), (int)D, fptr_out(dA), fptr_out(dr_bias), fptr_out(di_bias), st);
   return e == hipSuccess ? SSD_OK : hip_fail(e, "gated recurrence parameter sums launch");
@@ -424,7 +426,7 @@ int ssd_glr_step(const ssd_tensor *state, const ssd_tensor *x, const ssd_tensor 
   if (x->ndim != 2) return fail(SSD_ERR_SHAPE, "x: rank %d, expected 2 [b,D]", x->ndim);
   const int64_t b = x->shape[0], D = x->shape[1];
   if (b < 1 || D < 1) return fail(SSD_ERR_SHAPE, "empty problem: b=%lld D=%lld", (long long)b, (long long)D);
-  if (D > kMaxWidth || b > kMaxTiles || b * ((D + 1023) / 1024) > kMaxTiles)
+  if (D > kMaxWidth || b > kMaxTiles || b * ((D + 255) / 256) > kMaxTiles)
     return fail(SSD_ERR_UNSUPPORTED, "problem too large: b=%lld D=%lld", (long long)b, (long long)D);
   SSD_CHECK(act_dtype(x, "x"));
   const int64_t sx[2] = {b, D}, sd[1] = {D}, sb[1] = {b};

@@ -12,7 +12,7 @@ BF, F32 = torch.bfloat16, torch.float32
 
 
 def fwd_args(b=2, L=300, D=24, dtype=BF):
-    ns = (L + 127) // 128
+    ns = -(-L // ssd.SSD_GLR_SEGMENT)
     return dict(x=torch.zeros(b, L, D, dtype=dtype), r=torch.zeros(b, L, D, dtype=dtype),
                 i=torch.zeros(b, L, D, dtype=dtype), A=-torch.ones(D), r_bias=torch.zeros(D), i_bias=torch.zeros(D),
                 reset=torch.zeros(b, L, dtype=torch.uint8), lengths=torch.zeros(b, dtype=torch.int32),
@@ -87,8 +87,8 @@ def test_forward_refuses_overlaps():
 def test_workspace_checks():
     need = ssd.ssd_glr_workspace(2, 300, 24)
     assert need >= 2 * 2 * 64 * 8
-    assert ssd.ssd_glr_workspace(2, 256, 24) == 0
-    assert ssd.ssd_glr_workspace(2, 256, 24, backward=True) > 0
+    assert ssd.ssd_glr_workspace(2, 64, 24) == 0
+    assert ssd.ssd_glr_workspace(2, 64, 24, backward=True) > 0
     assert ssd.ssd_glr_workspace(0, 256, 24) == -1 and ssd.ssd_glr_workspace(1, (1 << 24) + 1, 24) == -1
     assert ssd.ssd_glr_workspace(1 << 22, 1, 65) == -1
     st, msg = call_fwd(fwd_args(), ws=None)

@@ -67,6 +67,8 @@ SHAPES = [
     (2, 127, 40, "dense", 0.02, None, True),
     (1, 128, 130, "dense", 0, None, True),
     (2, 129, 64, "offset", 0.01, [129, 128], True),
+    (3, 130, 128, "fused", 0.02, [65, 64, 63], True),
+    (2, 200, 256, "dense", 0, [16, 17], True),
     (1, 255, 56, "fused", 0, None, False),
     (2, 256, 8, "dense", 0, None, True),
     (4, 257, 96, "broadcast", 0.01, [257, 256, 1, 0], True),
@@ -100,9 +102,10 @@ def test_forward_and_gradients(case, dtype):
     for s in range(states.shape[1]):
         for row in range(b):
             n = L if lengths is None else lengths[row]
-            if s == 0 or s * 128 < n:
-                assert np.all(np.abs(st[row, s] - f["hp"][row, s * 128]) <=
-                              f["ehp"][row, s * 128] + glr_ref.U * np.abs(f["hp"][row, s * 128])), (row, s)
+            k = s * ssd.SSD_GLR_SEGMENT
+            if s == 0 or k < n:
+                assert np.all(np.abs(st[row, s] - f["hp"][row, k]) <=
+                              f["ehp"][row, k] + glr_ref.U * np.abs(f["hp"][row, k])), (row, s)
     ref = glr_ref.backward(**h, dout=dout.float().cpu().double().numpy(), dfin=dfin.cpu().double().numpy())
     for saved in (states, None):
         pre = {k: torch.full((b, L, D), float("nan"), dtype=dtype, device=DEV) for k in ("dx", "dr", "di")}
