@@ -3,7 +3,9 @@
     python -m mamba_ssd_scan_05_amd.build
 
 Each .hip source is compiled to an object by hipcc in parallel, then the
-objects are linked into a shared library with a C ABI (include/ssd.h).
+objects are linked into a shared library with a C ABI (include/ssd.h).  The
+CPython module _pydesc (tensor descriptors for the Python binding) is built
+beside it by g++ against torch's headers.
 """
 from __future__ import annotations
 
@@ -11,12 +13,14 @@ import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssd.so")
+PYDESC = os.path.join(PKG, "_pydesc.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["ssd_api.hip", "ssd_kernels.hip", "ssd_prep.hip", "ssd_quad.hip", "ssd_rwalk.hip", "ssd_sscan.hip", "ssd_bwd.hip",
@@ -44,10 +48,29 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_pydesc() -> None:
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = PYDESC + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-Wall", "-Werror", "-I" + os.path.join(ROOT, "include")]
+    for d in include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "ssd_pydesc.cpp"), "-o", tmp]
+    for d in library_paths():  # torch's, loaded already when the module is imported
+        cmd += ["-L" + d, "-Wl,-rpath," + d]
+    cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for ssd_pydesc.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, PYDESC)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        desc = ex.submit(_compile_pydesc)
         objs = list(ex.map(_compile, SOURCES))
+        desc.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
