@@ -24,26 +24,51 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Four elements at element offset `o` from p.
-template <typename T, bool VEC> __device__ __forceinline__ void load4(const T *p, float *v) {
-  if constexpr (!VEC) {
+// A lane's eight elements of a head vector as they lie in memory: four at lo
+// and four at hi.  VEC: two accesses of four elements, otherwise eight.
+template <typename T, bool VEC> struct Raw {
+  static constexpr int W = sizeof(T) == 2 ? (VEC ? 4 : 8) : 8;
+  uint32_t d[W];
+  __device__ __forceinline__ void load(const T *lo, const T *hi) {
+    if constexpr (!VEC) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = to_f(p[e]);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    v[0] = __builtin_bit_cast(float, w.x << 16), v[1] = __builtin_bit_cast(float, w.x & 0xFFFF0000u);
-    v[2] = __builtin_bit_cast(float, w.y << 16), v[3] = __builtin_bit_cast(float, w.y & 0xFFFF0000u);
-  } else {
-    const float4 w = *reinterpret_cast<const float4 *>(p);
-    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) {
+          d[e] = (uint32_t) reinterpret_cast<const uint16_t *>(lo)[e] << 16;
+          d[4 + e] = (uint32_t) reinterpret_cast<const uint16_t *>(hi)[e] << 16;
+        } else {
+          d[e] = __builtin_bit_cast(uint32_t, lo[e]), d[4 + e] = __builtin_bit_cast(uint32_t, hi[e]);
+        }
+      }
+    } else if constexpr (sizeof(T) == 2) {
+      const uint2 a = *reinterpret_cast<const uint2 *>(lo), b = *reinterpret_cast<const uint2 *>(hi);
+      d[0] = a.x, d[1] = a.y, d[2] = b.x, d[3] = b.y;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4 *>(lo), b = *reinterpret_cast<const uint4 *>(hi);
+      d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+    }
   }
-}
-template <typename T, bool VEC> __device__ __forceinline__ void store4(T *p, const float *v) {
+  // element k of the eight
+  __device__ __forceinline__ float at(int k) const {
+    if constexpr (W == 8) return __builtin_bit_cast(float, d[k]);
+    else return __builtin_bit_cast(float, (k & 1) ? (d[k >> 1] & 0xFFFF0000u) : (d[k >> 1] << 16));
+  }
+  // as four pairs: v[e] turns with v[4 + e]
+  template <bool INTER> __device__ __forceinline__ void pairs(float *v) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = at(INTER ? 2 * e : e), v[4 + e] = at(INTER ? 2 * e + 1 : 4 + e);
+  }
+};
+template <typename T, bool VEC, bool INTER> __device__ __forceinline__ void store8(T *lo, T *hi, const float *v) {
+  float o[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[INTER ? 2 * e : e] = v[e], o[INTER ? 2 * e + 1 : 4 + e] = v[4 + e];
   if constexpr (VEC) {
-    st4<T>(p, v[0], v[1], v[2], v[3]);
+    st4<T>(lo, o[0], o[1], o[2], o[3]);
+    st4<T>(hi, o[4], o[5], o[6], o[7]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = (T)v[e];
+    for (int e = 0; e < 4; ++e) lo[e] = (T)o[e], hi[e] = (T)o[4 + e];
   }
 }
 
@@ -63,47 +88,45 @@ struct Slot {
   int lo, hi, pair0;
   bool in, turns;
 };
-__device__ __forceinline__ Slot lane_slot(const NormRotParams &p, int l) {
+template <bool INTER> __device__ __forceinline__ Slot lane_slot(const NormRotParams &p, int l) {
   Slot s;
   s.in = 8 * l < p.N;
   s.turns = 4 * l < p.npair;
   s.pair0 = 4 * l;
-  const bool apart = s.turns && !p.interleaved;
+  const bool apart = s.turns && !INTER;
   s.lo = apart ? 4 * l : 8 * l;
   s.hi = apart ? p.npair + 4 * l : 8 * l + 4;
   return s;
 }
 
-// cos and sin of the lane's four angles at a position.
+// cos and sin of the lane's four angles at a position (1 and 0 where it does
+// not turn).
 struct Turn {
   float c[4], s[4];
 };
 __device__ __forceinline__ Turn angles(const NormRotParams &p, const Slot &sl, int64_t tok, int t) {
   Turn a;
-  double pos;
-  if (p.pos32) pos = (double)p.pos32[tok];
-  else if (p.pos64) pos = (double)p.pos64[tok];
-  else pos = (double)t;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a.c[e] = 1.f, a.s[e] = 0.f;
+  if (!sl.turns) return a;
+  const double pos = p.pos32 ? (double)p.pos32[tok] : p.pos64 ? (double)p.pos64[tok] : (double)t;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const double f = sl.turns ? (double)p.freqs[sl.pair0 + e] : 0.0;
-    const double turns = pos * (f * 0.15915494309189533577);
+    const double turns = pos * ((double)p.freqs[sl.pair0 + e] * 0.15915494309189533577);
     const float frac = (float)(turns - rint(turns));
     sincospif(2.f * frac, &a.s[e], &a.c[e]);
   }
   return a;
 }
 
-// y = R x on the lane's elements (back: R^T x).
-__device__ __forceinline__ void turn8(float *v, const Turn &a, const Slot &sl, bool interleaved, bool back) {
-  if (!sl.turns) return;
+// The lane's weights, in pair order.
+template <bool INTER> __device__ __forceinline__ void load_weight(const float *w, const Slot &sl, float *v) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int i = interleaved ? 2 * e : e, j = interleaved ? 2 * e + 1 : e + 4;
-    const float s = back ? -a.s[e] : a.s[e], u = v[i], w = v[j];
-    v[i] = fmaf(u, a.c[e], -(w * s));
-    v[j] = fmaf(u, s, w * a.c[e]);
-  }
+  for (int e = 0; e < 8; ++e) v[e] = 1.f;
+  if (!w || !sl.in) return;
+  Raw<float, false> r;
+  r.load(w + sl.lo, w + sl.hi);
+  r.template pairs<INTER>(v);
 }
 
 // A wave's item: TPW tokens (a power of two, 64 / LH / HG) and a slice of
@@ -129,63 +152,104 @@ template <int LH> __device__ __forceinline__ Item item_of(const NormRotParams &p
   return it;
 }
 
-template <typename T, int LH, bool VEC>
+// The lane group's walk over its heads: queries first, then keys.  Where a
+// head lies is formed at the first one of either kind and advanced from there.
+template <typename T, bool BACK> struct Walk {
+  const T *src, *dy;
+  T *dst;
+  int h;
+  bool isq;
+  __device__ __forceinline__ void at(const NormRotParams &p, const Item &it, const Slot &sl) {
+    isq = h < p.Hq;
+    const int hk = h - p.Hq;
+    src = isq ? (const T *)p.q + it.row * p.qb + it.t * p.qt + h * p.qh
+              : (const T *)p.k + it.row * p.kb + it.t * p.kt + hk * p.kh;
+    if constexpr (BACK)
+      dy = isq ? (const T *)p.dyq + it.row * p.dqb + it.t * p.dqt + h * p.dqh
+               : (const T *)p.dyk + it.row * p.dkb + it.t * p.dkt + hk * p.dkh;
+    dst = isq ? (T *)p.oq + (it.tok * p.Hq + h) * p.N : (T *)p.ok + (it.tok * p.Hk + hk) * p.N;
+    src += sl.lo, dst += sl.lo;
+    if constexpr (BACK) dy += sl.lo;
+  }
+  __device__ __forceinline__ void next(const NormRotParams &p, const Item &it, const Slot &sl, int step) {
+    h += step;
+    if (isq && h >= p.Hq) {
+      at(p, it, sl);
+    } else {
+      src += step * (isq ? p.qh : p.kh);
+      if constexpr (BACK) dy += step * (isq ? p.dqh : p.dkh);
+      dst += step * p.N;
+    }
+  }
+};
+
+// Forward.  The weights are multiplied into the turn's coefficients once per
+// token and kind of head: y_i = n_i (w_i c) - n_j (w_j s), y_j = n_i (w_i s) +
+// n_j (w_j c).  The next head is loaded while one is worked on.
+// b4 L4096 32 + 8 heads N128 bf16: 67 us (5.0 TB/s); addresses, weights and
+// pair order chosen anew for every head kept the vector ALU busy for 73.
+template <typename T, int LH, bool VEC, bool INTER>
 __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams p) {
-  constexpr int U = 2; // rows in flight per lane group
   const int lane = threadIdx.x & 63;
   const Item it = item_of<LH>(p, (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6));
-  if (!it.live) return;
-  const Slot sl = lane_slot(p, lane % LH);
-  const int step = 1 << p.hg_log;
+  if (!it.live || it.head >= it.hend) return;
+  const Slot sl = lane_slot<INTER>(p, lane % LH);
+  const int step = 1 << p.hg_log, gap = sl.hi - sl.lo;
   const float invn = 1.f / (float)p.N;
-  Turn an;
-  if (p.npair) an = angles(p, sl, it.tok, it.t);
-  for (int h0 = it.head; h0 < it.hend; h0 += U * step) {
-    float x[U][8];
+  Walk<T, false> cur;
+  cur.h = it.head;
+  cur.at(p, it, sl);
+  Raw<T, VEC> r{};
+  if (sl.in) r.load(cur.src, cur.src + gap);
+  const Turn an = angles(p, sl, it.tok, it.t);
+  float ci[4], cj[4], si[4], sj[4];
+  bool fresh = true;
+  for (;;) {
+    if (fresh) {
+      float w[8];
+      load_weight<INTER>(cur.isq ? p.qw : p.kw, sl, w);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * step;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
-      if (h < it.hend && sl.in) {
-        const T *src = h < p.Hq ? (const T *)p.q + it.row * p.qb + it.t * p.qt + h * p.qh
-                                : (const T *)p.k + it.row * p.kb + it.t * p.kt + (h - p.Hq) * p.kh;
-        load4<T, VEC>(src + sl.lo, x[u]);
-        load4<T, VEC>(src + sl.hi, x[u] + 4);
+      for (int e = 0; e < 4; ++e) {
+        ci[e] = an.c[e] * w[e], si[e] = an.s[e] * w[e];
+        cj[e] = an.c[e] * w[4 + e], sj[e] = an.s[e] * w[4 + e];
       }
     }
+    Walk<T, false> nxt = cur;
+    nxt.next(p, it, sl, step);
+    fresh = nxt.isq != cur.isq;
+    const bool more = nxt.h < it.hend;
+    Raw<T, VEC> rn{};
+    if (more && sl.in) rn.load(nxt.src, nxt.src + gap);
+    float x[8];
+    r.template pairs<INTER>(x);
+    float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * step;
-      float ss = 0.f;
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    ss = head_sum<LH>(ss);
+    const float rstd = __builtin_amdgcn_rsqf(fmaf(ss, invn, p.eps));
+    float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
-      ss = head_sum<LH>(ss);
-      if (h >= it.hend || !sl.in) continue;
-      const float rstd = __builtin_amdgcn_rsqf(fmaf(ss, invn, p.eps));
-      const bool isq = h < p.Hq;
-      const float *w = isq ? p.qw : p.kw;
-      float y[8], wv[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wv[e] = 1.f;
-      if (w) load4<float, VEC>(w + sl.lo, wv), load4<float, VEC>(w + sl.hi, wv + 4);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[u][e] * rstd * wv[e];
-      turn8(y, an, sl, p.interleaved, false);
-      T *dst = isq ? (T *)p.oq + (it.tok * p.Hq + h) * p.N : (T *)p.ok + (it.tok * p.Hk + (h - p.Hq)) * p.N;
-      store4<T, VEC>(dst + sl.lo, y);
-      store4<T, VEC>(dst + sl.hi, y + 4);
+    for (int e = 0; e < 4; ++e) {
+      const float u = x[e] * rstd, v = x[4 + e] * rstd;
+      y[e] = fmaf(u, ci[e], -(v * sj[e]));
+      y[4 + e] = fmaf(u, si[e], v * cj[e]);
     }
+    if (sl.in) store8<T, VEC, INTER>(cur.dst, cur.dst + gap, y);
+    if (!more) break;
+    cur = nxt;
+    r = rn;
   }
 }
 
-// Persistent: the waves stride over the items, each lane keeps its share of
-// the weights' gradients in registers; one partial row per workgroup.
-template <typename T, int LH, bool VEC>
-__global__ __launch_bounds__(kThreads) void norm_rotate_bwd_kernel(NormRotParams p) {
+// Backward, persistent: the waves stride over the items, each lane keeps its
+// share of the weights' gradients in registers; one partial row per workgroup.
+// Four waves a SIMD hide the loads: b4 L2048 32 + 8 heads N128 bf16 49 us (5.2
+// TB/s); three and the next head loaded ahead, as in the forward, 64 us.
+template <typename T, int LH, bool VEC, bool INTER>
+__global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotParams p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Slot sl = lane_slot(p, lane % LH);
-  const int step = 1 << p.hg_log;
+  const Slot sl = lane_slot<INTER>(p, lane % LH);
+  const int step = 1 << p.hg_log, gap = sl.hi - sl.lo;
   const float invn = 1.f / (float)p.N;
   float aq[8], ak[8];
 #pragma unroll
@@ -193,33 +257,37 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_bwd_kernel(NormRotParams
   for (int64_t item = (int64_t)blockIdx.x * (kThreads / 64) + wave; item < p.nitem;
        item += (int64_t)gridDim.x * (kThreads / 64)) {
     const Item it = item_of<LH>(p, item);
-    if (!it.live) continue;
-    Turn an;
-    if (p.npair) an = angles(p, sl, it.tok, it.t);
-    for (int h = it.head; h < it.hend; h += step) {
-      const bool isq = h < p.Hq;
-      const int hk = h - p.Hq;
-      float x[8], v[8], wv[8];
+    if (!it.live || it.head >= it.hend) continue;
+    Walk<T, true> cur;
+    cur.h = it.head;
+    cur.at(p, it, sl);
+    Raw<T, VEC> rx{}, rv{};
+    if (sl.in) rx.load(cur.src, cur.src + gap), rv.load(cur.dy, cur.dy + gap);
+    const Turn an = angles(p, sl, it.tok, it.t);
+    float w[8], acc[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = v[e] = 0.f, wv[e] = 1.f;
-      if (sl.in) {
-        const T *src = isq ? (const T *)p.q + it.row * p.qb + it.t * p.qt + h * p.qh
-                           : (const T *)p.k + it.row * p.kb + it.t * p.kt + hk * p.kh;
-        const T *dsrc = isq ? (const T *)p.dyq + it.row * p.dqb + it.t * p.dqt + h * p.dqh
-                            : (const T *)p.dyk + it.row * p.dkb + it.t * p.dkt + hk * p.dkh;
-        load4<T, VEC>(src + sl.lo, x);
-        load4<T, VEC>(src + sl.hi, x + 4);
-        load4<T, VEC>(dsrc + sl.lo, v);
-        load4<T, VEC>(dsrc + sl.hi, v + 4);
-        const float *w = isq ? p.qw : p.kw;
-        if (w) load4<float, VEC>(w + sl.lo, wv), load4<float, VEC>(w + sl.hi, wv + 4);
-      }
-      turn8(v, an, sl, p.interleaved, true);
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    bool fresh = true;
+    for (;;) {
+      if (fresh) load_weight<INTER>(cur.isq ? p.qw : p.kw, sl, w);
+      Walk<T, true> nxt = cur;
+      nxt.next(p, it, sl, step);
+      fresh = nxt.isq != cur.isq;
+      const bool more = nxt.h < it.hend;
+      float x[8], dy[8], v[8], wv[8];
+      rx.template pairs<INTER>(x);
+      rv.template pairs<INTER>(dy);
       float ss = 0.f, sv = 0.f;
 #pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = fmaf(dy[e], an.c[e], dy[4 + e] * an.s[e]);
+        v[4 + e] = fmaf(dy[4 + e], an.c[e], -(dy[e] * an.s[e]));
+      }
+#pragma unroll
       for (int e = 0; e < 8; ++e) {
+        wv[e] = v[e] * w[e];
         ss = fmaf(x[e], x[e], ss);
-        sv = fmaf(v[e] * wv[e], x[e], sv);
+        sv = fmaf(wv[e], x[e], sv);
       }
       ss = head_sum<LH>(ss);
       sv = head_sum<LH>(sv);
@@ -229,27 +297,30 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_bwd_kernel(NormRotParams
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float n = x[e] * rstd;
-        d[e] = rstd * fmaf(-n, m, wv[e] * v[e]);
-        const float g = v[e] * n;
-        aq[e] += isq ? g : 0.f;
-        ak[e] += isq ? 0.f : g;
+        d[e] = rstd * fmaf(-n, m, wv[e]);
+        acc[e] = fmaf(v[e], n, acc[e]);
       }
-      if (sl.in) {
-        T *dst = isq ? (T *)p.oq + (it.tok * p.Hq + h) * p.N : (T *)p.ok + (it.tok * p.Hk + hk) * p.N;
-        store4<T, VEC>(dst + sl.lo, d);
-        store4<T, VEC>(dst + sl.hi, d + 4);
+      if (sl.in) store8<T, VEC, INTER>(cur.dst, cur.dst + gap, d);
+      if (fresh || !more) {
+        // the sums of one kind of head
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          aq[e] += cur.isq ? acc[e] : 0.f;
+          ak[e] += cur.isq ? 0.f : acc[e];
+          acc[e] = 0.f;
+        }
       }
+      if (!more) break;
+      cur = nxt;
+      if (sl.in) rx.load(cur.src, cur.src + gap), rv.load(cur.dy, cur.dy + gap);
     }
   }
   // lane groups of the workgroup in a fixed order
-  __shared__ float part[kThreads / LH][2][8 * LH];
+  __shared__ __align__(16) float part[kThreads / LH][2][8 * LH];
   const int g = threadIdx.x / LH;
   if (sl.in) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      part[g][0][sl.lo + e] = aq[e], part[g][0][sl.hi + e] = aq[e + 4];
-      part[g][1][sl.lo + e] = ak[e], part[g][1][sl.hi + e] = ak[e + 4];
-    }
+    store8<float, true, INTER>(&part[g][0][sl.lo], &part[g][0][sl.hi], aq);
+    store8<float, true, INTER>(&part[g][1][sl.lo], &part[g][1][sl.hi], ak);
   }
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * p.N; c += kThreads) {
@@ -267,6 +338,7 @@ __global__ __launch_bounds__(1024) void norm_rotate_sum_kernel(const float *part
   const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
   const int c = (int)blockIdx.x * 16 + col; // 2N is a multiple of 16
   double s = 0.;
+#pragma unroll 16
   for (int k = row; k < n; k += 64) s += part[(int64_t)k * 2 * N + c];
   acc[row][col] = s;
   __syncthreads();
@@ -278,9 +350,14 @@ __global__ __launch_bounds__(1024) void norm_rotate_sum_kernel(const float *part
   }
 }
 
+template <typename T, int LH, bool VEC, bool INTER>
+void launch_pair(bool back, const NormRotParams &p, hipStream_t st) {
+  if (back) norm_rotate_bwd_kernel<T, LH, VEC, INTER><<<(uint32_t)p.nwg, kThreads, 0, st>>>(p);
+  else norm_rotate_fwd_kernel<T, LH, VEC, INTER><<<(uint32_t)((p.nitem + 3) / 4), kThreads, 0, st>>>(p);
+}
 template <typename T, int LH, bool VEC> hipError_t launch_one(bool back, const NormRotParams &p, hipStream_t st) {
-  if (back) norm_rotate_bwd_kernel<T, LH, VEC><<<(uint32_t)p.nwg, kThreads, 0, st>>>(p);
-  else norm_rotate_fwd_kernel<T, LH, VEC><<<(uint32_t)((p.nitem + 3) / 4), kThreads, 0, st>>>(p);
+  if (p.interleaved) launch_pair<T, LH, VEC, true>(back, p, st);
+  else launch_pair<T, LH, VEC, false>(back, p, st);
   return hipGetLastError();
 }
 template <typename T, bool VEC> hipError_t launch_lh(bool back, const NormRotParams &p, hipStream_t st) {
