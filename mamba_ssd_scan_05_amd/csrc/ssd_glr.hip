@@ -18,7 +18,7 @@
 // 154.)  The waves' maps are composed through LDS, and the chunks' through
 // one 64-bit word per (chunk, channel) in the workspace: a chunk publishes its
 // own map as soon as it is known and the finished state once its
-// predecessor's is; a later chunk looks back over kLook words at a time.  So
+// predecessor's is; a later chunk looks back over several words at a time.  So
 // the data crosses HBM once in each direction however the time axis is
 // split.  The fold over words always runs forward from a finished state with
 // one fma per chunk, the same operations that produced the words in between,
@@ -34,15 +34,18 @@ namespace ssd {
 namespace {
 
 
-// Waves of a workgroup, and the tokens whose decays are formed together (two
-// branches, of which a wave takes one; more at a time need more registers
-// than two workgroups a compute unit leave).
-constexpr int kWaves = 8;
+// Tokens of a wave, forward and backward, and the tokens whose decays are
+// formed together (two branches, of which a wave takes one; more at a time need
+// more registers than two workgroups a compute unit leave).
+constexpr int kFwdTokens = 16, kBwdTokens = 8;
 constexpr int kTogether = 2;
-// Words examined per look back: fewer leave long chains waiting on each hop
-// (0.7 us), more cost traffic (b1 L32768 D2048: 1 word 362 us, 4 words 152,
-// 8 words 148, 24 words 175; b4 L4096 D5120: 162 / 162 / 166 / 210).
-constexpr int kLook = 4;
+// A workgroup has eight waves; rows that fewer cover take four or two.
+constexpr int kWaves = 8;
+static_assert(kGlrChunk == kWaves * kFwdTokens && kGlrSegment == kWaves * kBwdTokens, "tokens of a chunk");
+
+// Words read at a time in a look back, and how far back it goes: as long as it
+// finds maps, up to kWindow words.
+constexpr int kRead = 4, kWindow = 16;
 
 // Words of the chunk chain: {A (high half), value (low half)}.  A is a
 // product of values in [0, inf) or a canonical NaN, so two other NaN
@@ -63,29 +66,42 @@ __device__ __forceinline__ void publish(uint64_t *w, uint64_t v) {
 // Carried value entering a chunk: `prev` points at the word of the chunk
 // right before it in chain order, `step` (in words) leads to earlier ones and
 // `n` of them exist (n >= 1; the first one only ever holds kFinished).
-__device__ __forceinline__ float look_back(const uint64_t *prev, int64_t step, int n) {
+// `stash` is this thread's column of kWindow rows of `ld` words in LDS: maps
+// behind the first four wait there, registers are short here.
+__device__ __forceinline__ float look_back(const uint64_t *prev, int64_t step, int n, uint64_t *stash, int ld) {
   for (;;) {
-    uint64_t w[kLook];
+#pragma unroll 1
+    for (int k0 = 0; k0 < kWindow; k0 += kRead) {
+      uint64_t w[kRead];
+      int kp = -1;
+      bool open = true;
 #pragma unroll
-    for (int k = 0; k < kLook; ++k)
-      w[k] = __hip_atomic_load(prev + step * (k < n ? k : n - 1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    int kp = -1;
-    bool open = true;
+      for (int k = 0; k < kRead; ++k)
+        w[k] = __hip_atomic_load(prev + step * (k0 + k < n ? k0 + k : n - 1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-    for (int k = 0; k < kLook; ++k) {
-      const uint32_t hi = (uint32_t)(w[k] >> 32);
-      if (open && hi == kFinished) kp = k;
-      open = open && hi < kFinished;
-    }
-    if (kp >= 0) {
-      float v = 0.f;
-#pragma unroll
-      for (int k = kLook - 1; k >= 0; --k) {
-        const float val = __builtin_bit_cast(float, (uint32_t)w[k]);
-        const float A = __builtin_bit_cast(float, (uint32_t)(w[k] >> 32));
-        v = k == kp ? val : k < kp ? fmaf(A, v, val) : v;
+      for (int k = 0; k < kRead; ++k) {
+        const uint32_t hi = (uint32_t)(w[k] >> 32);
+        if (open && hi == kFinished) kp = k;
+        open = open && hi < kFinished;
       }
-      return v;
+      if (kp >= 0) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = kRead - 1; k >= 0; --k) {
+          const float val = __builtin_bit_cast(float, (uint32_t)w[k]);
+          const float A = __builtin_bit_cast(float, (uint32_t)(w[k] >> 32));
+          v = k == kp ? val : k < kp ? fmaf(A, v, val) : v;
+        }
+#pragma unroll 1
+        for (int k = k0 - 1; k >= 0; --k) {
+          const uint64_t q = stash[k * ld];
+          v = fmaf(__builtin_bit_cast(float, (uint32_t)(q >> 32)), v, __builtin_bit_cast(float, (uint32_t)q));
+        }
+        return v;
+      }
+      if (!open) break;
+#pragma unroll
+      for (int k = 0; k < kRead; ++k) stash[(k0 + k) * ld] = w[k];
     }
     __builtin_amdgcn_s_sleep(2);
   }
@@ -214,13 +230,12 @@ template <bool SMALL> __device__ __forceinline__ Gate gate_of(const Chan &c, flo
   }
   return g;
 }
-__device__ __forceinline__ Chan chan_of(const float *A_, const float *rbias, const float *ibias, int c) {
+__device__ __forceinline__ Chan chan_of(float A, float rbias, float ibias) {
   Chan k;
-  const float A = A_[c];
   k.A2 = A * kLog2e;
   k.K = __builtin_amdgcn_sqrtf(fmaxf(-2.f * A, 0.f));
-  k.nrb = rbias ? -kLog2e * rbias[c] : 0.f;
-  k.nib = ibias ? -kLog2e * ibias[c] : 0.f;
+  k.nrb = -kLog2e * rbias;
+  k.nib = -kLog2e * ibias;
   return k;
 }
 __device__ __forceinline__ bool small_decay(float A2) { return fabsf(A2) <= 0.5f * kLog2e; }
@@ -269,14 +284,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base, in
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NW, bool CUT>
 __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
-  constexpr int kTile = 64 * V, TT = kGlrChunk / NW, ES = (int)sizeof(T);
+  constexpr int kTile = 64 * V, TT = kFwdTokens, kChunk = NW * TT, ES = (int)sizeof(T);
   __shared__ float aggA[NW][kTile], aggw[NW][kTile], carry[NW][kTile];
   __shared__ int aggcut[NW];
+  __shared__ uint64_t stash[kWindow][kTile];
   const Place pl = take_place(p, false);
   const int len = row_length(p, pl.row);
-  const int t0 = pl.chunk * kGlrChunk;
+  const int t0 = pl.chunk * kChunk;
   if (pl.chunk > 0 && t0 >= len) return; // nothing here, and nothing after it
-  const int nt = min(kGlrChunk, len - t0);
+  const int nt = min(kChunk, len - t0);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c0 = pl.tile * kTile + lane * V; // V divides D: all of a lane's channels exist or none
   const int lt0 = wave * TT, ntw = max(0, min(TT, nt - lt0)); // the wave's first token, its tokens that exist
@@ -313,7 +329,8 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
   bool sm = true;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    ch[e] = chan_of(p.A, p.rbias, p.ibias, min(c0 + e, p.D - 1));
+    const int c = min(c0 + e, p.D - 1);
+    ch[e] = chan_of(p.A[c], p.rbias ? p.rbias[c] : 0.f, p.ibias ? p.ibias[c] : 0.f);
     sm = sm && small_decay(ch[e].A2);
   }
 
@@ -326,6 +343,7 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
   constexpr int GR = TT < kTogether ? TT : kTogether;
 #pragma unroll
   for (int j0 = 0; j0 < TT; j0 += GR) {
+    if (j0 >= ntw) continue;
     float beta[GR][V];
 #pragma unroll
     for (int j = j0; j < j0 + GR; ++j) vr[j].pin(), vi[j].pin(), vx[j].pin();
@@ -377,7 +395,7 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
       cA *= aggA[v][tid];
       ccut = ccut || k;
     }
-    const int last = len > 0 ? (len - 1) / kGlrChunk : 0;
+    const int last = len > 0 ? (len - 1) / kChunk : 0;
     float h = 0.f;
     if (live) {
       uint64_t *word = nullptr;
@@ -392,7 +410,7 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
       } else {
         if (more && early) publish(word, make_word(kFinished, cw));
         else if (more && !ccut) publish(word, make_word(decay_bits(cA), cw));
-        h = look_back(word - p.wstride, -p.wstride, pl.chunk);
+        h = look_back(word - p.wstride, -p.wstride, pl.chunk, &stash[0][tid], kTile);
       }
       // the initial state has been read before anything is published
       if (p.inplace) __asm__ volatile("" ::"v"(h) : "memory");
@@ -438,19 +456,20 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NW, bool CUT>
 __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
-  constexpr int kTile = 64 * V, TT = kGlrSegment / NW, ES = (int)sizeof(T);
+  constexpr int kTile = 64 * V, TT = kBwdTokens, kChunk = NW * TT, ES = (int)sizeof(T);
   __shared__ float fA[NW][kTile], fw[NW][kTile], bA[NW][kTile], bw[NW][kTile];
   __shared__ float fcarry[NW][kTile], bcarry[NW][kTile];
   __shared__ int aggcut[NW];
+  __shared__ uint64_t stash[kWindow][kTile];
   const Place pl = take_place(p, true);
   const int len = row_length(p, pl.row);
-  const int t0 = pl.chunk * kGlrSegment;
-  const int last = len > 0 ? (len - 1) / kGlrSegment : 0;
+  const int t0 = pl.chunk * kChunk;
+  const int last = len > 0 ? (len - 1) / kChunk : 0;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lt0 = wave * TT;
-  const int nt = max(0, min(kGlrSegment, len - t0)); // rows that exist
+  const int nt = max(0, min(kChunk, len - t0)); // rows that exist
   const int ntw = max(0, min(TT, nt - lt0));
-  const int ntp = min(kGlrSegment, p.L - t0), ntpw = max(0, min(TT, ntp - lt0)); // rows of the gradients
+  const int ntp = min(kChunk, p.L - t0), ntpw = max(0, min(TT, ntp - lt0)); // rows of the gradients
   const int c0 = pl.tile * kTile + lane * V; // V divides D: all of a lane's channels exist or none
   const uint32_t off = c0 < p.D ? (uint32_t)(c0 * ES) : kNowhere;
   const int64_t prow = ((int64_t)pl.row * p.nchunk + pl.chunk) * 3 * p.D; // row of the partial sums
@@ -509,7 +528,8 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   bool sm = true;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    ch[e] = chan_of(p.A, p.rbias, p.ibias, min(c0 + e, p.D - 1));
+    const int c = min(c0 + e, p.D - 1);
+    ch[e] = chan_of(p.A[c], p.rbias ? p.rbias[c] : 0.f, p.ibias ? p.ibias[c] : 0.f);
     sm = sm && small_decay(ch[e].A2);
   }
 
@@ -522,6 +542,7 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   constexpr int GR = TT < kTogether ? TT : kTogether;
 #pragma unroll
   for (int j0 = 0; j0 < TT; j0 += GR) {
+    if (j0 >= ntw) continue;
 #pragma unroll
     for (int j = j0; j < j0 + GR; ++j) vr[j].pin(), vi[j].pin(), vx[j].pin();
     if (small) {
@@ -555,6 +576,7 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   }
 #pragma unroll
   for (int j = TT - 1; j >= 0; --j) {
+    if (j >= ntw) continue;
     const bool rs = CUT && ((resets >> j) & 1);
 #pragma unroll
     for (int e = 0; e < V; ++e) wb[e] = rs ? 0.f : a[j][e] * (vd[j].get(e) + wb[e]);
@@ -589,7 +611,7 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
         cin = p.dfin ? p.dfin[(int64_t)pl.row * p.D + c] : 0.f;
       } else {
         if (more) publish(word, ccut ? make_word(kFinished, cw) : make_word(decay_bits(cA), cw));
-        cin = look_back(word + p.wstride, p.wstride, last - pl.chunk);
+        cin = look_back(word + p.wstride, p.wstride, last - pl.chunk, &stash[0][tid], kTile);
       }
       const float cend = ccut ? cw : fmaf(cA, cin, cw);
       if (more && !(ccut && pl.chunk != last)) publish(word, make_word(kFinished, cend));
@@ -617,6 +639,7 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
     sA[e] = sr[e] = si[e] = 0.f;
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
+      if (j >= ntw) continue;
       const float n = CUT && ((resets >> j) & 1) ? b[j][e] : fmaf(a[j][e], h, b[j][e]);
       b[j][e] = h;
       h = n;
@@ -702,6 +725,19 @@ __global__ __launch_bounds__(256) void glr_fill_kernel(uint4 *p, int64_t n) {
   for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256) p[k] = v;
 }
 
+// V floats, 16 bytes at a time.
+template <int V> __device__ __forceinline__ void load_f32(const float *p, float *v) {
+  if constexpr (V == 1) {
+    v[0] = p[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(p + e);
+      v[e] = q.x, v[e + 1] = q.y, v[e + 2] = q.z, v[e + 3] = q.w;
+    }
+  }
+}
+
 // One token: V channels per lane; bound by the launch at small batches and by
 // HBM (the fp32 state in and out) at large ones.
 template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_kernel(GlrStepParams p) {
@@ -716,19 +752,16 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
   const bool rs = p.reset && p.reset[row] != 0;
   const float *st = p.state + (int64_t)row * p.D + c0;
   float *ns = p.new_state + (int64_t)row * p.D + c0;
-  float h[V];
-  if constexpr (V > 1) {
+  float h[V], A[V], rb[V], ib[V];
+  load_f32<V>(st, h);
+  load_f32<V>(p.A + c0, A);
 #pragma unroll
-    for (int e = 0; e < V; e += 4) {
-      const float4 v = *reinterpret_cast<const float4 *>(st + e);
-      h[e] = v.x, h[e + 1] = v.y, h[e + 2] = v.z, h[e + 3] = v.w;
-    }
-  } else {
-    h[0] = st[0];
-  }
+  for (int e = 0; e < V; ++e) rb[e] = ib[e] = 0.f;
+  if (p.rbias) load_f32<V>(p.rbias + c0, rb);
+  if (p.ibias) load_f32<V>(p.ibias + c0, ib);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const Chan ch = chan_of(p.A, p.rbias, p.ibias, c0 + e);
+    const Chan ch = chan_of(A[e], rb[e], ib[e]);
     const Gate g = gate_of<false>(ch, vr.get(e));
     const float u = sigmoid1(vi.get(e), ch.nib) * vx.get(e);
     h[e] = rs ? u : fmaf(g.a, h[e], g.beta * u);
@@ -742,15 +775,24 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
   store_row<T, V>(rows_rsrc(p.out, (int64_t)row * p.D, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0, h);
 }
 
-template <typename T, int V> hipError_t scan_launch(bool back, const GlrParams &p, hipStream_t st) {
+template <typename T, int V, int NW> void launch_waves(bool back, const GlrParams &p, hipStream_t st) {
   const dim3 grid((uint32_t)p.b * (uint32_t)p.ntile * (uint32_t)p.nchunk);
   if (p.reset) {
-    if (back) glr_bwd_kernel<T, V, kWaves, true><<<grid, 64 * kWaves, 0, st>>>(p);
-    else glr_fwd_kernel<T, V, kWaves, true><<<grid, 64 * kWaves, 0, st>>>(p);
+    if (back) glr_bwd_kernel<T, V, NW, true><<<grid, 64 * NW, 0, st>>>(p);
+    else glr_fwd_kernel<T, V, NW, true><<<grid, 64 * NW, 0, st>>>(p);
   } else {
-    if (back) glr_bwd_kernel<T, V, kWaves, false><<<grid, 64 * kWaves, 0, st>>>(p);
-    else glr_fwd_kernel<T, V, kWaves, false><<<grid, 64 * kWaves, 0, st>>>(p);
+    if (back) glr_bwd_kernel<T, V, NW, false><<<grid, 64 * NW, 0, st>>>(p);
+    else glr_fwd_kernel<T, V, NW, false><<<grid, 64 * NW, 0, st>>>(p);
   }
+}
+// As many waves as the rows need (b256 L32 D5120 bf16 forward: eight 119 us, four
+// 88; a workgroup has a thread for each of its 128 or 64 channels, so two
+// at least).
+template <typename T, int V> hipError_t scan_launch(bool back, const GlrParams &p, hipStream_t st) {
+  const int need = (p.L + (back ? kBwdTokens : kFwdTokens) - 1) / (back ? kBwdTokens : kFwdTokens);
+  if (need <= 2) launch_waves<T, V, 2>(back, p, st);
+  else if (need <= 4) launch_waves<T, V, 4>(back, p, st);
+  else launch_waves<T, V, kWaves>(back, p, st);
   return hipGetLastError();
 }
 

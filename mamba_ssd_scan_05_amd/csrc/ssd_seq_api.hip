@@ -464,8 +464,8 @@ int ssd_glr_step(const ssd_tensor *state, const ssd_tensor *x, const ssd_tensor 
   p.new_state = fptr_out(new_state);
   p.out = out->data;
   p.b = (int)b; p.D = (int)D;
-  const bool vec = rows16(x) && rows16(r) && rows16(i) && rows16(out) && (uintptr_t)state->data % 16 == 0 &&
-                   (uintptr_t)new_state->data % 16 == 0;
+  const bool vec = rows16(x) && rows16(r) && rows16(i) && rows16(out) && rows16(state) && rows16(new_state) &&
+                   rows16(A) && (!r_bias || rows16(r_bias)) && (!i_bias || rows16(i_bias));
   const hipError_t e = launch_glr_step(x->dtype, vec, p, (hipStream_t)stream);
   return e == hipSuccess ? SSD_OK : hip_fail(e, "gated recurrence step launch");
 }

@@ -399,7 +399,7 @@ def ssd_glr_fwd(x, r, i, A, r_bias=None, i_bias=None, *, reset=None, lengths=Non
     int32; ``states`` (see ssd_glr_states) is filled for ssd_glr_bwd.  Returns
     (out, final_state or None); tokens behind a row's length are not written."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if final_state is None and return_final_state:
         final_state = torch.empty((x.shape[0], x.shape[-1]), dtype=torch.float32, device=x.device)
     with _on_device(x):
@@ -424,7 +424,7 @@ def ssd_glr_bwd(x, r, i, A, r_bias=None, i_bias=None, *, reset=None, lengths=Non
     g = dict(out or {})
     for k in ("dx", "dr", "di"):
         if g.get(k) is None:
-            g[k] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            g[k] = torch.empty_like(x, memory_format=torch.contiguous_format)
     small = dict(dA=(D,), dr_bias=(D,) if want_bias else None, di_bias=(D,) if want_bias else None,
                  dinit=(x.shape[0], D) if want_init else None)
     for k, shp in small.items():
@@ -448,7 +448,7 @@ def ssd_glr_step(state, x, r, i, A, r_bias=None, i_bias=None, *, reset=None, out
     """One token of the gated linear recurrence for every row: state [b, D] is
     updated in place (or written to ``new_state``); returns out [b, D]."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     with _on_device(state):
         st = _stream(stream, state)
         keep, d = _descs(state, x, r, i, A, r_bias, i_bias, reset,
@@ -465,9 +465,9 @@ def ssd_norm_rotate_fwd(q, k, q_weight=None, k_weight=None, freqs=None, position
     elements by position * freqs; positions [b, L] int32 or int64 (default
     0..L-1).  Returns (q_out, k_out)."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     with _on_device(q):
         st = _stream(stream, q)
         keep, d = _descs(q, k, q_weight, k_weight, freqs, positions, q_out, k_out)
@@ -485,7 +485,7 @@ def ssd_norm_rotate_bwd(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_o
     g = dict(out or {})
     for n, t in (("dq", q), ("dk", k)):
         if g.get(n) is None:
-            g[n] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            g[n] = torch.empty_like(t, memory_format=torch.contiguous_format)
     for n in ("dq_weight", "dk_weight"):
         if not want_weights:
             g[n] = None

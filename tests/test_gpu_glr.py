@@ -64,6 +64,10 @@ SHAPES = [
     (1, 1, 64, "dense", 0, None, False),
     (2, 2, 72, "fused", 0.5, [0, 2], True),
     (3, 5, 3, "dense", 0, None, True),
+    (3, 16, 200, "dense", 0.05, [16, 9, 1], True),
+    (2, 33, 130, "fused", 0, None, True),
+    (2, 64, 128, "fused", 0.02, [64, 33], False),
+    (3, 65, 40, "offset", 0, None, True),
     (2, 127, 40, "dense", 0.02, None, True),
     (1, 128, 130, "dense", 0, None, True),
     (2, 129, 64, "offset", 0.01, [129, 128], True),
