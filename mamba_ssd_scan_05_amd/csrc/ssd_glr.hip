@@ -28,7 +28,7 @@
 // a workgroup waits only for lower tickets, which were handed to workgroups
 // that already run, so every wait ends.
 #include "ssd_device.h"
-#include "ssd_internal.h"
+#include "ssd_seq.h"
 
 namespace ssd {
 namespace {

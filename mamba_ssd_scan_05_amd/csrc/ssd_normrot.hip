@@ -17,7 +17,7 @@
 // in 64 bits, reduced to a fraction of a turn there: exact to fp32 at any
 // position.  Bound by HBM: x in, y out (backward: x and dy in, dx out).
 #include "ssd_device.h"
-#include "ssd_internal.h"
+#include "ssd_seq.h"
 
 namespace ssd {
 namespace {

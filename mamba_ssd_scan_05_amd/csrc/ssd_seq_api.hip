@@ -7,7 +7,7 @@
 
 #include "ssd.h"
 #include "ssd_check.h"
-#include "ssd_internal.h"
+#include "ssd_seq.h"
 
 using namespace ssd;
 
