@@ -382,7 +382,9 @@ int ssd_scan_bwd_gated(const ssd_tensor *x, const ssd_tensor *dt,
  *     h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * sigmoid(i_t + i_bias) * x_t
  *
  * for every batch row and channel; out_t = h_t.  The factor sqrt(1 - a^2)
- * keeps the variance of h at that of its input (taken as 0 where a > 1).
+ * keeps the variance of h at that of its input.  A is meant to be finite and at
+ * most 0: where a > 1 the factor is taken as 0, and the decays of 128
+ * successive tokens multiplied must stay within fp32's range.
  *
  * Packed and padded batches.  reset [b, L] marks (nonzero) the first token of
  * each document: it starts from a zero state (a_t = 0, so the factor is 1).
@@ -394,7 +396,7 @@ int ssd_scan_bwd_gated(const ssd_tensor *x, const ssd_tensor *dt,
  *
  * Layout: x, r, i and dout may be strided views (slices of a fused
  * projection, broadcast batches): the last dimension contiguous, other
- * strides >= 0, the token stride at most 2^21 elements.  All other tensors are
+ * strides >= 0, the token stride at most 2^22 elements.  All other tensors are
  * dense row-major.  Pointers need the alignment of their element; bf16
  * rows of odd width, stride or alignment are moved two bytes at a time.
  *
@@ -496,15 +498,14 @@ int ssd_glr_step(const ssd_tensor *state, const ssd_tensor *x,
  * other (shared keys: Hk < Hq).
  *
  *   q, k         f32 or bf16, one dtype; views allowed: the last dimension
- *                contiguous, other strides >= 0, token and head strides at
- *                most 2^21 elements                           required
+ *                contiguous, other strides >= 0                required
  *   q_weight, k_weight [N]  f32                               NULL => 1
  *   freqs        [npair]    f32                               NULL => none
- *   positions    [b, L]     i32 or i64, any value             NULL => 0..L-1
+ *   positions    [b, L]     i32 or i64, up to 2^53 either way NULL => 0..L-1
  *   q_out, k_out dtype and shape of q and k, dense, written
  *
  * Supported: N a multiple of 8 up to 256, npair a multiple of 4 up to N / 2,
- * L at most 2^24, Hq and Hk at most 2^16, b * L * (Hq + Hk) at most 2^26.
+ * L at most 2^24, b * L at most 2^25, Hq and Hk at most 2^16.
  * Arithmetic: fp32, angles reduced to a turn in 64 bits; results are rounded
  * once.  Results do not vary from run to run.  No output may overlap any other
  * argument.  Nothing is allocated; the calls may be captured into a HIP graph.

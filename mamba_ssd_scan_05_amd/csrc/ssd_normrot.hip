@@ -120,11 +120,11 @@ __device__ __forceinline__ Turn angles(const NormRotParams &p, const Slot &sl, i
 }
 
 // The lane's weights, in pair order.
-template <bool INTER> __device__ __forceinline__ void load_weight(const float *w, const Slot &sl, float *v) {
+template <bool VEC, bool INTER> __device__ __forceinline__ void load_weight(const float *w, const Slot &sl, float *v) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = 1.f;
   if (!w || !sl.in) return;
-  Raw<float, false> r;
+  Raw<float, VEC> r;
   r.load(w + sl.lo, w + sl.hi);
   r.template pairs<INTER>(v);
 }
@@ -136,17 +136,18 @@ struct Item {
   int t, row, head, hend;
   bool live;
 };
-template <int LH> __device__ __forceinline__ Item item_of(const NormRotParams &p, int64_t item) {
+template <int LH> __device__ __forceinline__ Item item_of(const NormRotParams &p, uint32_t item) {
   constexpr int HPW = 64 / LH;
   const int g = (threadIdx.x & 63) / LH;
   const int tpw = HPW >> p.hg_log;
   Item it;
-  const int64_t group = item / p.split;
-  const int slice = (int)(item - group * p.split);
-  it.tok = group * tpw + (g >> p.hg_log);
+  const uint32_t group = item / (uint32_t)p.split;
+  const int slice = (int)(item - group * (uint32_t)p.split);
+  const uint32_t tok = group * (uint32_t)tpw + (uint32_t)(g >> p.hg_log);
+  it.tok = tok;
   it.live = it.tok < p.ntok;
-  it.row = (int)(it.tok / p.L);
-  it.t = (int)(it.tok - (int64_t)it.row * p.L);
+  it.row = (int)(tok / (uint32_t)p.L);
+  it.t = (int)(tok - (uint32_t)it.row * (uint32_t)p.L);
   it.head = slice * p.per + (g & ((1 << p.hg_log) - 1));
   it.hend = min(p.Hq + p.Hk, (slice + 1) * p.per);
   return it;
@@ -191,7 +192,7 @@ template <typename T, bool BACK> struct Walk {
 template <typename T, int LH, bool VEC, bool INTER>
 __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams p) {
   const int lane = threadIdx.x & 63;
-  const Item it = item_of<LH>(p, (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6));
+  const Item it = item_of<LH>(p, __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)));
   if (!it.live || it.head >= it.hend) return;
   const Slot sl = lane_slot<INTER>(p, lane % LH);
   const int step = 1 << p.hg_log, gap = sl.hi - sl.lo;
@@ -207,7 +208,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
   for (;;) {
     if (fresh) {
       float w[8];
-      load_weight<INTER>(cur.isq ? p.qw : p.kw, sl, w);
+      load_weight<VEC, INTER>(cur.isq ? p.qw : p.kw, sl, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         ci[e] = an.c[e] * w[e], si[e] = an.s[e] * w[e];
@@ -247,15 +248,15 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
 // TB/s); three and the next head loaded ahead, as in the forward, 64 us.
 template <typename T, int LH, bool VEC, bool INTER>
 __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotParams p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Slot sl = lane_slot<INTER>(p, lane % LH);
   const int step = 1 << p.hg_log, gap = sl.hi - sl.lo;
   const float invn = 1.f / (float)p.N;
   float aq[8], ak[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
-  for (int64_t item = (int64_t)blockIdx.x * (kThreads / 64) + wave; item < p.nitem;
-       item += (int64_t)gridDim.x * (kThreads / 64)) {
+  for (uint32_t item = blockIdx.x * (kThreads / 64) + wave; item < (uint32_t)p.nitem;
+       item += gridDim.x * (kThreads / 64)) {
     const Item it = item_of<LH>(p, item);
     if (!it.live || it.head >= it.hend) continue;
     Walk<T, true> cur;
@@ -269,7 +270,7 @@ __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotPar
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
     bool fresh = true;
     for (;;) {
-      if (fresh) load_weight<INTER>(cur.isq ? p.qw : p.kw, sl, w);
+      if (fresh) load_weight<VEC, INTER>(cur.isq ? p.qw : p.kw, sl, w);
       Walk<T, true> nxt = cur;
       nxt.next(p, it, sl, step);
       fresh = nxt.isq != cur.isq;

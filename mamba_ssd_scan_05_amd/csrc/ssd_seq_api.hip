@@ -17,12 +17,10 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;
 constexpr int64_t kMaxWidth = (int64_t)1 << 20;  // channels of the recurrence
-constexpr int64_t kMaxStride = (int64_t)1 << 21; // token stride: 256 fp32 rows within 2^31 bytes
-constexpr int64_t kMaxOuter = (int64_t)1 << 36;  // batch stride
+constexpr int64_t kMaxStride = (int64_t)1 << 22; // token stride of the recurrence: 128 fp32 rows within 2^31 bytes
+constexpr int64_t kMaxOuter = (int64_t)1 << 36;  // other strides
 constexpr int64_t kMaxHeads = (int64_t)1 << 16;
-// head vectors of the norm: there are at least two to a token, so that a launch
-// has at most 2^25 waves
-constexpr int64_t kMaxVectors = (int64_t)1 << 26;
+constexpr int64_t kMaxBatchTokens = (int64_t)1 << 25; // tokens of the norm: at most as many waves in one launch
 constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // workgroups of 512 threads in one launch
 
 const char *dtype_name(int d) {
@@ -48,8 +46,10 @@ Range span_of(const ssd_tensor *t) {
 }
 
 // Presence, dtype, rank, shape, and the alignment of one element; dense
-// row-major, or (view) a contiguous last dimension with other strides >= 0.
-int check_arg(const ssd_tensor *t, const char *name, int dtype, int ndim, const int64_t *shape, bool view = false) {
+// row-major, or (view) a contiguous last dimension with other strides >= 0,
+// those behind the batch at most max_stride.
+int check_arg(const ssd_tensor *t, const char *name, int dtype, int ndim, const int64_t *shape, bool view = false,
+              int64_t max_stride = kMaxOuter) {
   if (!t) return fail(SSD_ERR_NULL, "%s: descriptor is NULL", name);
   if (!t->data) return fail(SSD_ERR_NULL, "%s: data pointer is NULL", name);
   if (t->dtype != dtype)
@@ -66,7 +66,7 @@ int check_arg(const ssd_tensor *t, const char *name, int dtype, int ndim, const 
       if ((!view || i == ndim - 1) && st != dense)
         return fail(SSD_ERR_LAYOUT, "%s: stride of dim %d is %lld, expected %lld", name, i, (long long)st,
                     (long long)dense);
-      if (view && (st < 0 || st > (i == 0 ? kMaxOuter : kMaxStride)))
+      if (view && (st < 0 || st > (i == 0 ? kMaxOuter : max_stride)))
         return fail(st < 0 ? SSD_ERR_LAYOUT : SSD_ERR_UNSUPPORTED, "%s: stride of dim %d is %lld", name, i,
                     (long long)st);
     }
@@ -174,9 +174,9 @@ int validate_glr(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, 
                 (long long)D);
   SSD_CHECK(act_dtype(x, "x"));
   const int64_t sx[3] = {b, L, D}, sd[1] = {D}, sr[2] = {b, L}, sl[1] = {b}, ss[2] = {b, D};
-  SSD_CHECK(check_arg(x, "x", x->dtype, 3, sx, true));
-  SSD_CHECK(check_arg(r, "r", x->dtype, 3, sx, true));
-  SSD_CHECK(check_arg(i, "i", x->dtype, 3, sx, true));
+  SSD_CHECK(check_arg(x, "x", x->dtype, 3, sx, true, kMaxStride));
+  SSD_CHECK(check_arg(r, "r", x->dtype, 3, sx, true, kMaxStride));
+  SSD_CHECK(check_arg(i, "i", x->dtype, 3, sx, true, kMaxStride));
   SSD_CHECK(check_arg(A, "A", SSD_F32, 1, sd));
   if (r_bias) SSD_CHECK(check_arg(r_bias, "r_bias", SSD_F32, 1, sd));
   if (i_bias) SSD_CHECK(check_arg(i_bias, "i_bias", SSD_F32, 1, sd));
@@ -264,8 +264,7 @@ int validate_norm_rotate(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
                 (long long)Hq, (long long)Hk, (long long)N);
   if (N % 8 != 0 || N > 256)
     return fail(SSD_ERR_UNSUPPORTED, "N=%lld is not a multiple of 8 up to 256", (long long)N);
-  if (L > kMaxTokens || b > kMaxTokens || Hq > kMaxHeads || Hk > kMaxHeads || b * L > kMaxVectors ||
-      b * L * (Hq + Hk) > kMaxVectors)
+  if (L > kMaxTokens || b > kMaxTokens || b * L > kMaxBatchTokens || Hq > kMaxHeads || Hk > kMaxHeads)
     return fail(SSD_ERR_UNSUPPORTED, "problem too large: b=%lld L=%lld Hq=%lld Hk=%lld", (long long)b, (long long)L,
                 (long long)Hq, (long long)Hk);
   if (!(eps >= 0.f) || eps > 1e30f) return fail(SSD_ERR_UNSUPPORTED, "eps=%g is not a finite number >= 0", (double)eps);
@@ -369,7 +368,7 @@ int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, c
   const int64_t b = x->shape[0], L = x->shape[1], D = x->shape[2];
   const int64_t so[3] = {b, L, D}, sf[2] = {b, D}, ss[3] = {b, plan.nseg, D}, sd[1] = {D};
   if (states) SSD_CHECK(check_arg(states, "states", SSD_F32, 3, ss));
-  SSD_CHECK(check_arg(dout, "dout", x->dtype, 3, so, true));
+  SSD_CHECK(check_arg(dout, "dout", x->dtype, 3, so, true, kMaxStride));
   if (dfinal_state) SSD_CHECK(check_arg(dfinal_state, "dfinal_state", SSD_F32, 2, sf));
   SSD_CHECK(check_arg(dx, "dx", x->dtype, 3, so));
   SSD_CHECK(check_arg(dr, "dr", x->dtype, 3, so));

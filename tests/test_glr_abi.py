@@ -51,7 +51,7 @@ FWD = [
     ("x_transposed", dict(x=torch.zeros(2, 24, 300, dtype=BF).transpose(1, 2)), 4),
     ("out_view", dict(out=torch.zeros(2, 300, 48, dtype=BF)[..., :24]), 4),
     ("reset_view", dict(reset=torch.zeros(2, 600, dtype=torch.uint8)[:, ::2]), 4),
-    ("x_wide_stride", dict(x=lambda: torch.empty(300 * ((1 << 21) + 8), dtype=BF).as_strided((1, 300, 24), (0, (1 << 21) + 8, 1)).expand(2, 300, 24)), 5),
+    ("x_wide_stride", dict(x=lambda: torch.empty(300 * ((1 << 22) + 8), dtype=BF).as_strided((1, 300, 24), (0, (1 << 22) + 8, 1)).expand(2, 300, 24)), 5),
 ]
 
 

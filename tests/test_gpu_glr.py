@@ -28,6 +28,8 @@ def make(b, L, D, dtype, seed, layout="dense", reset=0.0, lengths=None, init=Tru
     elif layout == "offset":  # rows that start between 16-byte boundaries
         proj = n(b, L, 3 * D + 5).to(dtype).to(DEV)
         x, r, i = proj[..., 1:D + 1], proj[..., D + 2:2 * D + 2], proj[..., 2 * D + 3:3 * D + 3]
+    elif layout == "time_major":
+        x, r, i = (n(L, b, D).to(dtype).to(DEV).transpose(0, 1) for _ in range(3))
     elif layout == "broadcast":  # one row of gates for the whole batch
         x = n(b, L, D).to(dtype).to(DEV)
         r, i = n(1, L, D).to(dtype).to(DEV).expand(b, L, D), n(b, 1, D).to(dtype).to(DEV).expand(b, L, D)
@@ -74,6 +76,7 @@ SHAPES = [
     (3, 130, 128, "fused", 0.02, [65, 64, 63], True),
     (2, 200, 256, "dense", 0, [16, 17], True),
     (1, 255, 56, "fused", 0, None, False),
+    (5, 150, 66, "time_major", 0.01, [150, 0, 149, 64, 150], True),
     (2, 256, 8, "dense", 0, None, True),
     (4, 257, 96, "broadcast", 0.01, [257, 256, 1, 0], True),
     (3, 513, 33, "fused", 0.004, [511, 513, 257], True),
@@ -314,6 +317,40 @@ def test_graph_replays_and_streams():
     torch.cuda.synchronize()
     for o, f in res:
         assert torch.equal(o, want) and torch.equal(f, wf)
+
+
+def test_the_default_stream_by_handle_and_two_host_threads():
+    import threading
+    b, L, D = 2, 600, 128
+    t, dout, dfin = make(b, L, D, BF, seed=16, reset=0.002)
+    want, wf = ssd.ssd_glr_fwd(**t)
+    wg = ssd.ssd_glr_bwd(**t, dout=dout, dfinal_state=dfin)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        out, fin = ssd.ssd_glr_fwd(**t, stream=torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(fin, wf)
+    bad = []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    o, f = ssd.ssd_glr_fwd(**t)
+                    g = ssd.ssd_glr_bwd(**t, dout=dout, dfinal_state=dfin)
+                torch.cuda.current_stream().synchronize()
+                if not (torch.equal(o, want) and torch.equal(f, wf) and all(torch.equal(g[k], wg[k]) for k in wg)):
+                    bad.append("differs")
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # reported below
+            bad.append(repr(e))
+
+    th = [threading.Thread(target=work) for _ in range(3)]
+    for x in th:
+        x.start()
+    for x in th:
+        x.join()
+    assert not bad, bad
 
 
 def test_far_offsets():

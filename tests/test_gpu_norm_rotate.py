@@ -172,3 +172,11 @@ def test_far_offsets():
     q.copy_(t["q"])
     got = ssd.ssd_norm_rotate_fwd(**dict(t, q=q))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # heads 2^30 elements apart, as in a heads-first cache of long sequences
+    q = big.as_strided((2, 3, 2, 64), (192, 64, 1 << 30, 1))
+    q.copy_(t["q"])
+    dy = [torch.randn_like(v) for v in want]
+    got = ssd.ssd_norm_rotate_fwd(**dict(t, q=q))
+    wg = ssd.ssd_norm_rotate_bwd(**t, dq_out=dy[0], dk_out=dy[1])
+    g = ssd.ssd_norm_rotate_bwd(**dict(t, q=q), dq_out=dy[0], dk_out=dy[1])
+    assert torch.equal(got[0], want[0]) and all(torch.equal(g[k], wg[k]) for k in wg)

@@ -63,10 +63,16 @@ def test_options_overlaps_and_sizes_refused():
     a.update(q=proj[:, :, :4], k=proj[:, :, 4:6])
     st, msg = call(a)
     assert st == 4 and "device" in msg or "address" in msg, (st, msg)  # the views pass; CPU memory does not
-    q = torch.zeros(1, dtype=BF).as_strided((1, 1, 1, 1), (1, 1, 1, 1)).expand(1, 1 << 23, 7, 32)
+    row = torch.zeros(1, 1, 1, 32, dtype=BF)
     a = args(1, 1, 1, 1)
-    a.update(q=q[..., :32], k=q[:, :, :2, :32])
+    a.update(q=row.expand(1, (1 << 25) + 1, 7, 32), k=row.expand(1, (1 << 25) + 1, 2, 32))
     assert call(a)[0] == 5
+    # heads-first caches: a head stride of 2^23 elements passes the checks
+    far = torch.empty(1 << 24, dtype=BF).as_strided((2, 5, 2, 32), (160, 32, 1 << 23, 1))
+    a = args(Hq=2)
+    a.update(q=far)
+    st, msg = call(a)
+    assert st == 4 and ("device" in msg or "address" in msg), (st, msg)
     assert ssd.lib().ssd_norm_rotate_workspace(12) == -1 and ssd.lib().ssd_norm_rotate_workspace(128) == 1024 * 2 * 128 * 4
 
 
