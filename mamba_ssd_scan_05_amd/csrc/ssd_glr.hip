@@ -109,9 +109,10 @@ __device__ __forceinline__ float look_back(const uint64_t *prev, int64_t step, i
 
 // V elements of one row at byte offset off (per lane) + so (per wave), in one
 // access of 2, 4 or 16 bytes.  A lane without channels passes kNowhere: its
-// reads give zero and its stores are dropped.
+// reads give zero and its stores are dropped.  AUX: the cache policy (0 or
+// kNonTemporal).
 constexpr uint32_t kNowhere = 0xFFFFFF00u; // past every range
-template <typename T, int V> struct Row {
+template <typename T, int V, int AUX> struct Row {
   static constexpr int kBytes = V * (int)sizeof(T);
   static constexpr int W = kBytes < 4 ? 1 : kBytes / 4; // 32-bit words held
   static_assert(kBytes == 2 || kBytes == 4 || kBytes == 16, "one access");
@@ -128,12 +129,12 @@ template <typename T, int V> struct Row {
   }
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off, int so) {
     if constexpr (W == 4) {
-      const i32x4 v = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, so, 0));
+      const i32x4 v = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, so, AUX));
       d[0] = (uint32_t)v[0], d[1] = (uint32_t)v[1], d[2] = (uint32_t)v[2], d[3] = (uint32_t)v[3];
     } else if constexpr (kBytes == 4) {
-      d[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, so, 0);
+      d[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, so, AUX);
     } else {
-      d[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, so, 0);
+      d[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, so, AUX);
     }
   }
   // Makes the value opaque here, so that nothing computed from it is moved
@@ -150,11 +151,11 @@ template <typename T, int V> struct Row {
 };
 
 // Stores V values, rounded once to T.
-template <typename T, int V>
+template <typename T, int V, int AUX>
 __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t off, int so, const float *v) {
-  constexpr int W = Row<T, V>::W;
-  if constexpr (Row<T, V>::kBytes == 2) {
-    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (__bf16)v[0]), r, (int)off, so, 0);
+  constexpr int W = Row<T, V, AUX>::W;
+  if constexpr (Row<T, V, AUX>::kBytes == 2) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (__bf16)v[0]), r, (int)off, so, AUX);
   } else {
     int d[W];
 #pragma unroll
@@ -170,9 +171,9 @@ __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t off
     }
     if constexpr (W == 4) {
       const i32x4 t = {d[0], d[1], d[2], d[3]};
-      __builtin_amdgcn_raw_buffer_store_b128(t, r, (int)off, so, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(t, r, (int)off, so, AUX);
     } else {
-      __builtin_amdgcn_raw_buffer_store_b32(d[0], r, (int)off, so, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(d[0], r, (int)off, so, AUX);
     }
   }
 }
@@ -282,7 +283,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base, in
 // of them.  Bound by HBM (3 tensors read, 1 written) with the vector ALU close
 // behind.
 // ---------------------------------------------------------------------------
-template <typename T, int V, int NW, bool CUT>
+template <typename T, int V, int NW, bool CUT, int AUX>
 __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
   constexpr int kTile = 64 * V, TT = kFwdTokens, kChunk = NW * TT, ES = (int)sizeof(T);
   __shared__ float aggA[NW][kTile], aggw[NW][kTile], carry[NW][kTile];
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
   const __amdgpu_buffer_rsrc_t rx = rows_rsrc(p.x, pl.row * p.xb + (int64_t)t0 * p.xt, p.xt, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t rr = rows_rsrc(p.r, pl.row * p.rb_ + (int64_t)t0 * p.rt, p.rt, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t ri = rows_rsrc(p.i, pl.row * p.ib_ + (int64_t)t0 * p.it, p.it, nt, p.D, ES);
-  Row<T, V> vx[TT], vr[TT], vi[TT];
+  Row<T, V, AUX> vx[TT], vr[TT], vi[TT];
   if (ntw == TT) {
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
@@ -446,7 +447,7 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
       const bool rs = CUT && ((resets >> j) & 1);
 #pragma unroll
       for (int e = 0; e < V; ++e) h[e] = rs ? b[j][e] : fmaf(a[j][e], h[e], b[j][e]);
-      store_row<T, V>(ro, off, (lt0 + j) * p.D * ES, h);
+      store_row<T, V, AUX>(ro, off, (lt0 + j) * p.D * ES, h);
     }
 }
 
@@ -454,7 +455,7 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
 // Backward.  Chunks of kGlrSegment tokens, entering state given; the chain runs
 // from the last chunk to the first.  4 tensors read, 3 written.
 // ---------------------------------------------------------------------------
-template <typename T, int V, int NW, bool CUT>
+template <typename T, int V, int NW, bool CUT, int AUX>
 __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   constexpr int kTile = 64 * V, TT = kBwdTokens, kChunk = NW * TT, ES = (int)sizeof(T);
   __shared__ float fA[NW][kTile], fw[NW][kTile], bA[NW][kTile], bw[NW][kTile];
@@ -483,9 +484,9 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
 
   // behind the row's length: zero gradients
   for (int j = ntw; j < ntpw; ++j) {
-    store_row<T, V>(odx, off, (lt0 + j) * p.D * ES, zero);
-    store_row<T, V>(odr, off, (lt0 + j) * p.D * ES, zero);
-    store_row<T, V>(odi, off, (lt0 + j) * p.D * ES, zero);
+    store_row<T, V, AUX>(odx, off, (lt0 + j) * p.D * ES, zero);
+    store_row<T, V, AUX>(odr, off, (lt0 + j) * p.D * ES, zero);
+    store_row<T, V, AUX>(odi, off, (lt0 + j) * p.D * ES, zero);
   }
   if (pl.chunk > last) {
     for (int k = tid; k < 3 * kTile; k += 64 * NW) {
@@ -499,7 +500,7 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   const __amdgpu_buffer_rsrc_t rr = rows_rsrc(p.r, pl.row * p.rb_ + (int64_t)t0 * p.rt, p.rt, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t ri = rows_rsrc(p.i, pl.row * p.ib_ + (int64_t)t0 * p.it, p.it, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t rd = rows_rsrc(p.dout, pl.row * p.db + (int64_t)t0 * p.dt, p.dt, nt, p.D, ES);
-  Row<T, V> vx[TT], vr[TT], vi[TT], vd[TT];
+  Row<T, V, AUX> vx[TT], vr[TT], vi[TT], vd[TT];
   if (ntw == TT) {
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
@@ -542,7 +543,13 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   constexpr int GR = TT < kTogether ? TT : kTogether;
 #pragma unroll
   for (int j0 = 0; j0 < TT; j0 += GR) {
-    if (j0 >= ntw) continue;
+    if (j0 >= ntw) { // these tokens pass both walks on
+#pragma unroll
+      for (int j = j0; j < j0 + GR; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) a[j][e] = 1.f, be[j][e] = b[j][e] = 0.f;
+      continue;
+    }
 #pragma unroll
     for (int j = j0; j < j0 + GR; ++j) vr[j].pin(), vi[j].pin(), vx[j].pin();
     if (small) {
@@ -576,7 +583,6 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   }
 #pragma unroll
   for (int j = TT - 1; j >= 0; --j) {
-    if (j >= ntw) continue;
     const bool rs = CUT && ((resets >> j) & 1);
 #pragma unroll
     for (int e = 0; e < V; ++e) wb[e] = rs ? 0.f : a[j][e] * (vd[j].get(e) + wb[e]);
@@ -639,7 +645,6 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
     sA[e] = sr[e] = si[e] = 0.f;
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
-      if (j >= ntw) continue;
       const float n = CUT && ((resets >> j) & 1) ? b[j][e] : fmaf(a[j][e], h, b[j][e]);
       b[j][e] = h;
       h = n;
@@ -673,9 +678,9 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
       sr[e] += orr[e];
       si[e] += oi[e];
     }
-    store_row<T, V>(odx, off, (lt0 + j) * p.D * ES, ox);
-    store_row<T, V>(odr, off, (lt0 + j) * p.D * ES, orr);
-    store_row<T, V>(odi, off, (lt0 + j) * p.D * ES, oi);
+    store_row<T, V, AUX>(odx, off, (lt0 + j) * p.D * ES, ox);
+    store_row<T, V, AUX>(odr, off, (lt0 + j) * p.D * ES, orr);
+    store_row<T, V, AUX>(odi, off, (lt0 + j) * p.D * ES, oi);
   }
   // parameter gradients: the waves' sums in a fixed order (fA, fw and bA are
   // read no more once every wave has its carries)
@@ -745,7 +750,7 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
   const int row = (int)(blockIdx.x / (uint32_t)p.nblk);
   const int c0 = ((int)(blockIdx.x - (uint32_t)row * (uint32_t)p.nblk) * 256 + (int)threadIdx.x) * V;
   if (c0 >= p.D) return;
-  Row<T, V> vr, vi, vx;
+  Row<T, V, 0> vr, vi, vx;
   vr.load(rows_rsrc(p.r, row * p.rb_, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0);
   vi.load(rows_rsrc(p.i, row * p.ib_, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0);
   vx.load(rows_rsrc(p.x, row * p.xb, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0);
@@ -772,27 +777,34 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
   } else {
     ns[0] = h[0];
   }
-  store_row<T, V>(rows_rsrc(p.out, (int64_t)row * p.D, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0, h);
+  store_row<T, V, 0>(rows_rsrc(p.out, (int64_t)row * p.D, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0, h);
 }
 
-template <typename T, int V, int NW> void launch_waves(bool back, const GlrParams &p, hipStream_t st) {
+template <typename T, int V, int NW, int AUX> void launch_waves(bool back, const GlrParams &p, hipStream_t st) {
   const dim3 grid((uint32_t)p.b * (uint32_t)p.ntile * (uint32_t)p.nchunk);
   if (p.reset) {
-    if (back) glr_bwd_kernel<T, V, NW, true><<<grid, 64 * NW, 0, st>>>(p);
-    else glr_fwd_kernel<T, V, NW, true><<<grid, 64 * NW, 0, st>>>(p);
+    if (back) glr_bwd_kernel<T, V, NW, true, AUX><<<grid, 64 * NW, 0, st>>>(p);
+    else glr_fwd_kernel<T, V, NW, true, AUX><<<grid, 64 * NW, 0, st>>>(p);
   } else {
-    if (back) glr_bwd_kernel<T, V, NW, false><<<grid, 64 * NW, 0, st>>>(p);
-    else glr_fwd_kernel<T, V, NW, false><<<grid, 64 * NW, 0, st>>>(p);
+    if (back) glr_bwd_kernel<T, V, NW, false, AUX><<<grid, 64 * NW, 0, st>>>(p);
+    else glr_fwd_kernel<T, V, NW, false, AUX><<<grid, 64 * NW, 0, st>>>(p);
   }
 }
+// x, r and i that take half of the 256 MB last-level cache pass it by (b4 L4096
+// D5120 bf16 forward 158 -> 154 us, b4 L2048 forward and backward 244 -> 234);
+// smaller ones find themselves there again (b5 L1009 D1100 f32 forward 24.5 us,
+// passed by 27.8).
+constexpr int64_t kOnceBytes = (int64_t)128 << 20;
+
 // As many waves as the rows need (b256 L32 D5120 bf16 forward: eight 119 us, four
 // 88; a workgroup has a thread for each of its 128 or 64 channels, so two
 // at least).
 template <typename T, int V> hipError_t scan_launch(bool back, const GlrParams &p, hipStream_t st) {
   const int need = (p.L + (back ? kBwdTokens : kFwdTokens) - 1) / (back ? kBwdTokens : kFwdTokens);
-  if (need <= 2) launch_waves<T, V, 2>(back, p, st);
-  else if (need <= 4) launch_waves<T, V, 4>(back, p, st);
-  else launch_waves<T, V, kWaves>(back, p, st);
+  if (need <= 2) launch_waves<T, V, 2, 0>(back, p, st);
+  else if (need <= 4) launch_waves<T, V, 4, 0>(back, p, st);
+  else if ((int64_t)p.b * p.L * p.D * 3 * (int64_t)sizeof(T) < kOnceBytes) launch_waves<T, V, kWaves, 0>(back, p, st);
+  else launch_waves<T, V, kWaves, kNonTemporal>(back, p, st);
   return hipGetLastError();
 }
 

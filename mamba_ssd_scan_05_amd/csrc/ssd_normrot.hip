@@ -24,12 +24,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 // A lane's eight elements of a head vector as they lie in memory: four at lo
 // and four at hi.  VEC: two accesses of four elements, otherwise eight.
 template <typename T, bool VEC> struct Raw {
   static constexpr int W = sizeof(T) == 2 ? (VEC ? 4 : 8) : 8;
   uint32_t d[W];
-  __device__ __forceinline__ void load(const T *lo, const T *hi) {
+  // ONCE: the row is marked as not read again
+  template <bool ONCE = false> __device__ __forceinline__ void load(const T *lo, const T *hi) {
     if constexpr (!VEC) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -41,10 +45,16 @@ template <typename T, bool VEC> struct Raw {
         }
       }
     } else if constexpr (sizeof(T) == 2) {
-      const uint2 a = *reinterpret_cast<const uint2 *>(lo), b = *reinterpret_cast<const uint2 *>(hi);
+      const u32x2 *pa = reinterpret_cast<const u32x2 *>(lo), *pb = reinterpret_cast<const u32x2 *>(hi);
+      u32x2 a, b;
+      if constexpr (ONCE) a = __builtin_nontemporal_load(pa), b = __builtin_nontemporal_load(pb);
+      else a = *pa, b = *pb;
       d[0] = a.x, d[1] = a.y, d[2] = b.x, d[3] = b.y;
     } else {
-      const uint4 a = *reinterpret_cast<const uint4 *>(lo), b = *reinterpret_cast<const uint4 *>(hi);
+      const u32x4 *pa = reinterpret_cast<const u32x4 *>(lo), *pb = reinterpret_cast<const u32x4 *>(hi);
+      u32x4 a, b;
+      if constexpr (ONCE) a = __builtin_nontemporal_load(pa), b = __builtin_nontemporal_load(pb);
+      else a = *pa, b = *pb;
       d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
     }
   }
@@ -189,7 +199,7 @@ template <typename T, bool BACK> struct Walk {
 // n_j (w_j c).  The next head is loaded while one is worked on.
 // b4 L4096 32 + 8 heads N128 bf16: 67 us (5.0 TB/s); addresses, weights and
 // pair order chosen anew for every head kept the vector ALU busy for 73.
-template <typename T, int LH, bool VEC, bool INTER>
+template <typename T, int LH, bool VEC, bool INTER, bool ONCE>
 __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams p) {
   const int lane = threadIdx.x & 63;
   const Item it = item_of<LH>(p, __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)));
@@ -201,7 +211,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
   cur.h = it.head;
   cur.at(p, it, sl);
   Raw<T, VEC> r{};
-  if (sl.in) r.load(cur.src, cur.src + gap);
+  if (sl.in) r.template load<ONCE>(cur.src, cur.src + gap);
   const Turn an = angles(p, sl, it.tok, it.t);
   float ci[4], cj[4], si[4], sj[4];
   bool fresh = true;
@@ -220,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
     fresh = nxt.isq != cur.isq;
     const bool more = nxt.h < it.hend;
     Raw<T, VEC> rn{};
-    if (more && sl.in) rn.load(nxt.src, nxt.src + gap);
+    if (more && sl.in) rn.template load<ONCE>(nxt.src, nxt.src + gap);
     float x[8];
     r.template pairs<INTER>(x);
     float ss = 0.f;
@@ -351,10 +361,19 @@ __global__ __launch_bounds__(1024) void norm_rotate_sum_kernel(const float *part
   }
 }
 
+// A forward whose input takes half of the 256 MB last-level cache reads it past
+// the caches, which leaves them to the outputs (b4 L4096 32 + 8 heads N128 bf16,
+// 168 MB: 67 -> 58 us); a smaller one leaves its input there for the backward
+// (b4 L2048 of the same, 84 MB, forward and backward: 85 us, past the caches 94).
+constexpr int64_t kOnceBytes = (int64_t)128 << 20;
+
 template <typename T, int LH, bool VEC, bool INTER>
 void launch_pair(bool back, const NormRotParams &p, hipStream_t st) {
+  const uint32_t grid = (uint32_t)((p.nitem + 3) / 4);
+  const bool once = VEC && p.ntok * (p.Hq + p.Hk) * p.N * (int64_t)sizeof(T) >= kOnceBytes;
   if (back) norm_rotate_bwd_kernel<T, LH, VEC, INTER><<<(uint32_t)p.nwg, kThreads, 0, st>>>(p);
-  else norm_rotate_fwd_kernel<T, LH, VEC, INTER><<<(uint32_t)((p.nitem + 3) / 4), kThreads, 0, st>>>(p);
+  else if (once) norm_rotate_fwd_kernel<T, LH, VEC, INTER, VEC><<<grid, kThreads, 0, st>>>(p);
+  else norm_rotate_fwd_kernel<T, LH, VEC, INTER, false><<<grid, kThreads, 0, st>>>(p);
 }
 template <typename T, int LH, bool VEC> hipError_t launch_one(bool back, const NormRotParams &p, hipStream_t st) {
   if (p.interleaved) launch_pair<T, LH, VEC, true>(back, p, st);
