@@ -15,7 +15,7 @@
 // exchange between lanes, and what is per token (its existence, a reset, its
 // address) is per wave.  (Measured before: 16 bytes a lane with the token groups
 // of a wave composed by shuffles, b4 L4096 D5120 bf16 forward 265 us against
-// 154.)  The waves' maps are composed through LDS, and the chunks' through
+// 147.)  The waves' maps are composed through LDS, and the chunks' through
 // one 64-bit word per (chunk, channel) in the workspace: a chunk publishes its
 // own map as soon as it is known and the finished state once its
 // predecessor's is; a later chunk looks back over several words at a time.  So
@@ -280,8 +280,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base, in
 
 // ---------------------------------------------------------------------------
 // Forward.  A wave takes TT successive tokens of the tile's channels, a lane V
-// of them.  Bound by HBM (3 tensors read, 1 written) with the vector ALU close
-// behind.
+// of them.  About 40 vector instructions an element, 5 of them transcendental
+// (two issue slots each).  b4 L4096 D5120 bf16: 147 us for 671 MB, 4.6 TB/s
+// where a large copy reaches 5.1; HBM moves 1.06 times the inputs and outputs
+// (the rest are chain words), the vector ALU is busy 54 % of the time.  The
+// same kernel without gates, look back and ticket takes 138: what is left
+// is the wait at the two barriers and the tail of the chain.
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NW, bool CUT, int AUX>
 __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
@@ -453,7 +457,12 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
 
 // ---------------------------------------------------------------------------
 // Backward.  Chunks of kGlrSegment tokens, entering state given; the chain runs
-// from the last chunk to the first.  4 tensors read, 3 written.
+// from the last chunk to the first.  4 tensors read, 3 written.  Only the decay,
+// beta and the state before each token are kept per element; the gates are formed
+// once more for the gradients, which costs less than the registers to keep them
+// (two workgroups a compute unit instead of one: b4 L2048 D5120 bf16 150 us
+// against 227).  587 MB at 3.9 TB/s; the vector ALU is busy 63 % of the time
+// (75 instructions an element).
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NW, bool CUT, int AUX>
 __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
@@ -743,8 +752,9 @@ template <int V> __device__ __forceinline__ void load_f32(const float *p, float 
   }
 }
 
-// One token: V channels per lane; bound by the launch at small batches and by
-// HBM (the fp32 state in and out) at large ones.
+// One token: V channels per lane; bound by the launch at small batches (b1 D2048:
+// 2.4 us) and by latency and HBM (the fp32 state in and out) at large ones (b256
+// D5120 bf16, 21 MB: 6.5 us).
 template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_kernel(GlrStepParams p) {
   constexpr int ES = (int)sizeof(T);
   const int row = (int)(blockIdx.x / (uint32_t)p.nblk);

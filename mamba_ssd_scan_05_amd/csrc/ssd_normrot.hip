@@ -197,8 +197,9 @@ template <typename T, bool BACK> struct Walk {
 // Forward.  The weights are multiplied into the turn's coefficients once per
 // token and kind of head: y_i = n_i (w_i c) - n_j (w_j s), y_j = n_i (w_i s) +
 // n_j (w_j c).  The next head is loaded while one is worked on.
-// b4 L4096 32 + 8 heads N128 bf16: 67 us (5.0 TB/s); addresses, weights and
-// pair order chosen anew for every head kept the vector ALU busy for 73.
+// b4 L4096 32 + 8 heads N128 bf16: 56 us (6.0 TB/s, outputs left in the last-
+// level cache); addresses, weights and pair order chosen anew for every head
+// kept the vector ALU busy for 73.
 template <typename T, int LH, bool VEC, bool INTER, bool ONCE>
 __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams p) {
   const int lane = threadIdx.x & 63;
@@ -254,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
 
 // Backward, persistent: the waves stride over the items, each lane keeps its
 // share of the weights' gradients in registers; one partial row per workgroup.
-// Four waves a SIMD hide the loads: b4 L2048 32 + 8 heads N128 bf16 49 us (5.2
+// Four waves a SIMD hide the loads: b4 L2048 32 + 8 heads N128 bf16 47 us (5.4
 // TB/s); three and the next head loaded ahead, as in the forward, 64 us.
 template <typename T, int LH, bool VEC, bool INTER>
 __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotParams p) {
