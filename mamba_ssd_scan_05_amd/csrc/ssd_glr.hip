@@ -33,7 +33,6 @@
 namespace ssd {
 namespace {
 
-
 // Tokens of a wave, forward and backward, and the tokens whose decays are
 // formed together (two branches, of which a wave takes one; more at a time need
 // more registers than two workgroups a compute unit leave).
@@ -280,10 +279,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base, in
 
 // ---------------------------------------------------------------------------
 // Forward.  A wave takes TT successive tokens of the tile's channels, a lane V
-// of them.  About 40 vector instructions an element, 5 of them transcendental
-// (two issue slots each).  b4 L4096 D5120 bf16: 147 us for 671 MB, 4.6 TB/s
-// where a large copy reaches 5.1; HBM moves 1.06 times the inputs and outputs
-// (the rest are chain words), the vector ALU is busy 54 % of the time.  The
+// of them.  31 vector instructions an element, 5 of them transcendental (two
+// issue slots each).  b4 L4096 D5120 bf16: 147 us for 671 MB, 4.6 TB/s
+// where a large copy reaches 5.1; HBM moves 1.04 times the inputs and outputs
+// (the rest are chain words), the vector ALU is busy 53 % of the time.  The
 // same kernel without gates, look back and ticket takes 138: what is left
 // is the wait at the two barriers and the tail of the chain.
 // ---------------------------------------------------------------------------
@@ -461,8 +460,8 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
 // beta and the state before each token are kept per element; the gates are formed
 // once more for the gradients, which costs less than the registers to keep them
 // (two workgroups a compute unit instead of one: b4 L2048 D5120 bf16 150 us
-// against 227).  587 MB at 3.9 TB/s; the vector ALU is busy 63 % of the time
-// (75 instructions an element).
+// against 227).  587 MB at 3.9 TB/s; the vector ALU is busy 61 % of the time
+// (74 instructions an element).
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NW, bool CUT, int AUX>
 __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
