@@ -420,18 +420,20 @@ def ssd_glr_bwd(x, r, i, A, r_bias=None, i_bias=None, *, reset=None, lengths=Non
     Returns a dict: dx, dr, di (dtype of x), dA and, when asked for, dr_bias,
     di_bias, dinit (fp32).  ``states`` as filled by ssd_glr_fwd saves a pass
     over the inputs.  ``out`` may hold preallocated tensors under those names."""
-    D, dev = x.shape[-1], x.device
     g = dict(out or {})
     for k in ("dx", "dr", "di"):
         if g.get(k) is None:
             g[k] = torch.empty_like(x, memory_format=torch.contiguous_format)
-    small = dict(dA=(D,), dr_bias=(D,) if want_bias else None, di_bias=(D,) if want_bias else None,
-                 dinit=(x.shape[0], D) if want_init else None)
-    for k, shp in small.items():
-        if shp is None:
+    for k, want in (("dA", True), ("dr_bias", want_bias), ("di_bias", want_bias)):
+        if not want:
             g[k] = None
         elif g.get(k) is None:
-            g[k] = torch.empty(shp, dtype=torch.float32, device=dev)
+            g[k] = torch.empty_like(A)  # cheaper than torch.empty
+    if not want_init:
+        g["dinit"] = None
+    elif g.get("dinit") is None:
+        g["dinit"] = (torch.empty((x.shape[0], x.shape[-1]), dtype=torch.float32, device=x.device)
+                      if init_state is None else torch.empty_like(init_state))
     with _on_device(x):
         st = _stream(stream, x)
         ws = _glr_workspace(x, True, st)

@@ -373,3 +373,64 @@ def test_many_rows_and_a_wide_row():
         out, fin = ssd.ssd_glr_fwd(**t)
         check("out", out, f["h"], f["eh"])
         check("final", fin, f["fin"], f["efin"])
+
+
+def test_a_very_long_row():
+    # constant gates and input: h_t = g (1 - a^t) / (1 - a), g the input's share;
+    # 8192 chunks forward, 16384 back, inputs of stride 0 along the row
+    L, D = 1 << 20, 64
+    one = torch.ones(1, 1, D, device=DEV)
+    A = -torch.linspace(1e-4, 0.4, D, device=DEV)
+    x, z = one.expand(1, L, D), torch.zeros(1, 1, D, device=DEV).expand(1, L, D)
+    states = ssd.ssd_glr_states(x)
+    out, fin = ssd.ssd_glr_fwd(x, z, z, A, states=states)
+    a = np.exp(A.cpu().double().numpy() * 0.5)
+    g = np.sqrt(-np.expm1(A.cpu().double().numpy())) * 0.5
+    # The decay is off by ea U (2 + 8 |log a| and 8 for the roundings of a
+    # step) and the input's share by 40 U; to first order in them h moves by
+    # (ea |h| / (1 - a) + 40 |h|) U, as a sum of what every token adds
+    for t in (1, 100, 128, 129, 4096, 500000, L):
+        want = g * -np.expm1(t * np.log(a)) / (1 - a)
+        tol = ((10 + 8 * np.abs(np.log(a))) / (1 - a) + 40) * glr_ref.U * want
+        got = out[0, t - 1].cpu().double().numpy()
+        assert np.all(np.abs(got - want) <= tol), (t, np.max(np.abs(got - want) / tol))
+    # the final state goes by the chunks' maps, the last output by the tokens:
+    # the same bound for either
+    assert np.all(np.abs(fin[0].cpu().double().numpy() - want) <= tol)
+    # backward with dout = 1: c_0 = sum over t >= 1 of a^t
+    d = ssd.ssd_glr_bwd(x, z, z, A, dout=x, states=states)
+    want = a * -np.expm1(L * np.log(a)) / (1 - a)
+    tol = ((10 + 8 * np.abs(np.log(a))) / (1 - a) + 40) * glr_ref.U * want
+    assert np.all(np.abs(d["dinit"][0].cpu().double().numpy() - want) <= tol)
+
+
+def test_optional_arguments_and_shared_inputs():
+    b, L, D = 2, 200, 66
+    t, dout, dfin = make(b, L, D, F32, seed=17)
+    h = host(t)
+    # no initial state, no gradient of the final one, no biases
+    bare = dict(t, init_state=None, r_bias=None, i_bias=None)
+    out, fin = ssd.ssd_glr_fwd(**bare, return_final_state=False)
+    assert fin is None
+    ref = dict(h, init=None, rb=None, ib=None)
+    f = glr_ref.forward(**ref)
+    check("out", out, f["h"], f["eh"])
+    pre = dict(dx=torch.empty_like(out), dA=torch.empty(D, device=DEV))
+    g = ssd.ssd_glr_bwd(**bare, dout=dout, want_bias=False, want_init=False, out=pre)
+    assert g["dx"] is pre["dx"] and g["dA"] is pre["dA"] and g["dr_bias"] is None and g["dinit"] is None
+    gr = glr_ref.backward(**ref, dout=dout.cpu().double().numpy())
+    for k in ("dx", "dr", "di", "dA"):
+        check(k, g[k], gr[k], gr["e" + k])
+    # lengths outside [0, L] count as the nearer end; any nonzero byte is a reset
+    ln = torch.tensor([-5, 10 ** 9], dtype=torch.int32, device=DEV)
+    rs = torch.zeros(b, L, dtype=torch.uint8, device=DEV)
+    rs[1, 37] = 255
+    out = torch.zeros_like(t["x"])
+    _, fin = ssd.ssd_glr_fwd(**dict(t, lengths=ln, reset=rs), out=out)
+    f = glr_ref.forward(**dict(h, lengths=np.array([0, L]), reset=rs.cpu().numpy()))
+    check("out", out, f["h"], f["eh"])
+    check("final", fin, f["fin"], f["efin"])
+    # one tensor for the input and both gates
+    out, fin = ssd.ssd_glr_fwd(t["x"], t["x"], t["x"], t["A"])
+    f = glr_ref.forward(h["x"], h["x"], h["x"], h["A"])
+    check("out", out, f["h"], f["eh"])

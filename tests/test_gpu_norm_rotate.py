@@ -180,3 +180,33 @@ def test_far_offsets():
     wg = ssd.ssd_norm_rotate_bwd(**t, dq_out=dy[0], dk_out=dy[1])
     g = ssd.ssd_norm_rotate_bwd(**dict(t, q=q), dq_out=dy[0], dk_out=dy[1])
     assert torch.equal(got[0], want[0]) and all(torch.equal(g[k], wg[k]) for k in wg)
+
+
+def test_one_weight_and_shared_inputs():
+    t, pos, dyq, dyk = make(2, 9, 3, 3, 40, 8, F32)
+    t["q_weight"] = None
+    t["k"] = t["q"]
+    qo, ko = ssd.ssd_norm_rotate_fwd(**t)
+    g = ssd.ssd_norm_rotate_bwd(**t, dq_out=dyq, dk_out=dyk, out=dict(dk_weight=torch.empty(40, device=DEV)))
+    eps = float(np.float32(1e-6))
+    for w, o, dy, dn, wn in ((None, qo, dyq, "dq", "dq_weight"), (t["k_weight"], ko, dyk, "dk", "dk_weight")):
+        y, ey = ref.forward(num(t["q"]), num(w), pos, num(t["freqs"]), eps, False)
+        check("y", o, y, ey)
+        d = ref.backward(num(t["q"]), num(w), pos, num(t["freqs"]), eps, False, num(dy), 140)
+        check(dn, g[dn], d["dx"], d["edx"])
+        check(wn, g[wn], d["dw"], d["edw"])
+
+
+def test_many_tokens_of_few_heads_and_few_tokens_of_many():
+    for b, L, Hq, Hk, N, npair in ((1, 200000, 1, 1, 16, 8), (1, 2, 300, 77, 32, 16), (3, 1, 1, 1, 256, 64)):
+        t, pos, dyq, dyk = make(b, L, Hq, Hk, N, npair, F32)
+        qo, ko = ssd.ssd_norm_rotate_fwd(**t)
+        g = ssd.ssd_norm_rotate_bwd(**t, dq_out=dyq, dk_out=dyk)
+        eps = float(np.float32(1e-6))
+        for x, w, o, dy, dn, wn in ((t["q"], t["q_weight"], qo, dyq, "dq", "dq_weight"),
+                                    (t["k"], t["k_weight"], ko, dyk, "dk", "dk_weight")):
+            y, ey = ref.forward(num(x), num(w), pos, num(t["freqs"]), eps, False)
+            check("y", o, y, ey)
+            d = ref.backward(num(x), num(w), pos, num(t["freqs"]), eps, False, num(dy), 130 + Hq + Hk + b * L * (Hq + Hk) // 1024)
+            check(dn, g[dn], d["dx"], d["edx"])
+            check(wn, g[wn], d["dw"], d["edw"])
