@@ -806,8 +806,8 @@ template <typename T, int V, int NW, int AUX> void launch_waves(bool back, const
 constexpr int64_t kOnceBytes = (int64_t)128 << 20;
 
 // As many waves as the rows need (b256 L32 D5120 bf16 forward: eight 119 us, four
-// 88; a workgroup has a thread for each of its 128 or 64 channels, so two
-// at least).
+// 88, two 84; b64 L17: eight 27, two 16; a workgroup has a thread for each of
+// its 128 or 64 channels, so two at least).
 template <typename T, int V> hipError_t scan_launch(bool back, const GlrParams &p, hipStream_t st) {
   const int need = (p.L + (back ? kBwdTokens : kFwdTokens) - 1) / (back ? kBwdTokens : kFwdTokens);
   if (need <= 2) launch_waves<T, V, 2, 0>(back, p, st);

@@ -393,7 +393,9 @@ template <typename T, bool VEC> hipError_t launch_lh(bool back, const NormRotPar
 
 // Splits the tokens' heads into items.  Fewer than kEnough waves leave compute
 // units idle (a decode step): the heads of a token are then spread over
-// several waves, each forming the angles again.
+// several waves, each forming the angles again (b32 L1 32 + 8 heads N128 bf16
+// forward in a graph: 3.0 us, one wave a token 6.6; b1 L1000 7.2 against 8.0;
+// from L2000 on the two are the same).
 void norm_rotate_plan(NormRotParams *p) {
   constexpr int64_t kEnough = 4096;
   int lh = 2;
