@@ -11,4 +11,4 @@ from .ssd import (SSD_ALGO_AUTO, SSD_ALGO_CHUNKED, SSD_ALGO_FUSED, SSD_ALGO_ROWS
                   ssd_status_string, ssd_step, ssd_version,
                   ssd_release_scratch, ssd_scan_bwd, ssd_scan_bwd_gated,
                   ssd_glr_bwd, ssd_glr_fwd, ssd_glr_states, ssd_glr_step, ssd_glr_workspace,
-                  ssd_norm_rotate_bwd, ssd_norm_rotate_fwd)
+                  ssd_norm_rotate_bwd, ssd_norm_rotate_fwd, ssd_norm_rotate_workspace)

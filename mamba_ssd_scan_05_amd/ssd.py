@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import struct
 from typing import Optional
@@ -167,12 +168,15 @@ except ImportError:
     _descs = _descs_py
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
 def _on_device(t):
     """Make t's device current for the call (the library launches on the
     current device and refuses memory that device cannot address)."""
-    if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+    if t is not None and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
         return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    return _SAME_DEVICE
 
 
 def _stream(stream, t):
@@ -181,7 +185,7 @@ def _stream(stream, t):
     if t is not None and t.is_cuda:
         # torch.cuda.current_stream(t.device).cuda_stream without the Stream
         # object (1.9 us)
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
     return None
 
 
@@ -370,6 +374,7 @@ def _workspace(nbytes: int, t, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
 
 
+@functools.lru_cache(maxsize=1024)
 def ssd_glr_workspace(b: int, L: int, D: int, backward: bool = False) -> int:
     """Workspace bytes of ssd_glr_fwd or ssd_glr_bwd (-1: a shape they refuse)."""
     return int(lib().ssd_glr_workspace(int(b), int(L), int(D), int(backward)))
@@ -460,6 +465,12 @@ def ssd_glr_step(state, x, r, i, A, r_bias=None, i_bias=None, *, reset=None, out
     return out
 
 
+@functools.lru_cache(maxsize=64)
+def ssd_norm_rotate_workspace(N: int) -> int:
+    """Workspace bytes of ssd_norm_rotate_bwd (-1: an N it refuses)."""
+    return int(lib().ssd_norm_rotate_workspace(int(N)))
+
+
 def ssd_norm_rotate_fwd(q, k, q_weight=None, k_weight=None, freqs=None, positions=None, *,
                         eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None, stream=None):
     """Norm of queries q [b, L, Hq, N] and keys k [b, L, Hk, N] (C and B of the
@@ -488,14 +499,15 @@ def ssd_norm_rotate_bwd(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_o
     for n, t in (("dq", q), ("dk", k)):
         if g.get(n) is None:
             g[n] = torch.empty_like(t, memory_format=torch.contiguous_format)
-    for n in ("dq_weight", "dk_weight"):
+    for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
         if not want_weights:
             g[n] = None
         elif g.get(n) is None:
-            g[n] = torch.empty((q.shape[-1],), dtype=torch.float32, device=q.device)
+            g[n] = (torch.empty_like(w) if w is not None else
+                    torch.empty((q.shape[-1],), dtype=torch.float32, device=q.device))
     with _on_device(q):
         st = _stream(stream, q)
-        ws = _workspace(int(lib().ssd_norm_rotate_workspace(q.shape[-1])), q, st)
+        ws = _workspace(ssd_norm_rotate_workspace(q.shape[-1]), q, st)
         keep, d = _descs(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_out, g["dq"], g["dk"],
                          g["dq_weight"], g["dk_weight"])
         status = lib().ssd_norm_rotate_bwd(*d, float(eps), int(interleaved),
