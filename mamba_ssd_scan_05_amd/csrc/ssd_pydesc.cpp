@@ -5,6 +5,7 @@
 // under 1 us).  Marshalling only; nothing is computed here.
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstddef>
 #include <exception>
 
 #include "ssd.h"
@@ -25,10 +26,13 @@ int dtype_code(at::ScalarType t) {
   }
 }
 
-// pack(tensor_or_None, ...) -> tuple of descriptor addresses or None, valid
-// until this thread's next call.
+// pack(tensor_or_None, ...) -> tuple of descriptors or None.  A descriptor is
+// a bytes object, which ctypes passes as the address of its contents: the
+// tuple owns them, so a call made in between (by a signal handler, a
+// finalizer, another thread) leaves them alone.  The contents of a bytes object
+// lie behind a header of whole words, aligned to 8 bytes as ssd_tensor needs.
+static_assert(alignof(ssd_tensor) <= 8 && offsetof(PyBytesObject, ob_sval) % 8 == 0, "descriptors in bytes objects");
 PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  static thread_local ssd_tensor desc[kMaxTensors];
   if (n > kMaxTensors) {
     PyErr_SetString(PyExc_ValueError, "too many tensors in one call");
     return nullptr;
@@ -49,7 +53,7 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n) {
         if (nd > 4) {
           PyErr_SetString(PyExc_ValueError, "ssd tensors have at most 4 dimensions");
         } else {
-          ssd_tensor &d = desc[i];
+          ssd_tensor d;
           d.data = t.numel() ? t.data_ptr() : nullptr;
           d.dtype = dtype_code(t.scalar_type());
           d.ndim = (int32_t)nd;
@@ -57,7 +61,7 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n) {
             d.shape[k] = k < nd ? t.size(k) : 0;
             d.strides[k] = k < nd ? t.stride(k) : 0;
           }
-          item = PyLong_FromVoidPtr(&d);
+          item = PyBytes_FromStringAndSize(reinterpret_cast<const char *>(&d), sizeof d);
         }
       } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -73,7 +77,7 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 PyMethodDef kMethods[] = {
-    {"pack", (PyCFunction)(void (*)(void))pack, METH_FASTCALL, "descriptor addresses of the given tensors"},
+    {"pack", (PyCFunction)(void (*)(void))pack, METH_FASTCALL, "descriptors of the given tensors"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pydesc", "ssd_tensor descriptors of torch tensors", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -154,9 +154,10 @@ def _descs_py(*ts):
 
 
 def _descs_native(*ts):
-    """_descs_py through the module _pydesc; the descriptors live until the
-    thread's next call."""
-    return None, _pydesc.pack(*ts)
+    """_descs_py through the module _pydesc: the descriptors are bytes objects
+    (ctypes passes their addresses), owned by the tuple."""
+    d = _pydesc.pack(*ts)
+    return d, d
 
 
 # Same descriptors either way (a wheel of the plain sources has no _pydesc);

@@ -55,3 +55,22 @@ def test_threads_have_their_own():
     done.set()
     th.join()
     assert mine[0] != got["a"][0] and got["later"] == got["raw"]
+
+
+@pytest.mark.parametrize("descs", [ssd._descs_native, ssd._descs_py], ids=["native", "python"])
+def test_a_call_in_between_leaves_the_descriptors_alone(descs):
+    # a signal handler or a finalizer may call the library between a call's
+    # descriptors and its C call
+    keep, d = descs(torch.zeros(2, 3), None, torch.zeros(4, dtype=torch.bfloat16))
+    before = raw(d)
+    keep2, d2 = descs(torch.zeros(7, 7, 7), torch.zeros(1), torch.zeros(5, 1))
+    assert raw(d) == before and raw(d2) != before
+
+
+def test_the_library_reads_the_descriptors():
+    # shapes and strides as the C side sees them, by what it refuses
+    f = lambda *s: torch.zeros(*s)  # noqa: E731
+    for descs in (ssd._descs_native, ssd._descs_py):
+        keep, d = descs(f(3, 24), f(3, 24), f(3, 24), f(3, 23), f(24), None, None, None, f(3, 24), f(3, 24))
+        assert ssd.lib().ssd_glr_step(*d, None) == 2
+        assert "i: dim 1 is 23, expected 24" in ssd.ssd_last_error()
