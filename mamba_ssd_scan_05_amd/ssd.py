@@ -6,6 +6,12 @@ is not built, loading it raises.
 
     out, final = ssd_scan_fwd(x, dt, dt_bias, A, B, C, D, init_state, chunk=256)
     y = ssd_step(state, x, dt, A, B, C, D)          # state updated in place
+
+``stream`` is a HIP stream's handle (default: torch's current stream).  What a
+call allocates itself, outputs that were not passed in and its workspace,
+belongs to the stream it runs on, as under ``torch.cuda.stream``: the caller
+lets that stream wait for the inputs, and other streams wait for it before
+they use the results (and ``record_stream`` results that they outlive).
 """
 from __future__ import annotations
 
@@ -169,7 +175,7 @@ except ImportError:
     _descs = _descs_py
 
 
-_SAME_DEVICE = contextlib.nullcontext()
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _on_device(t):
@@ -177,7 +183,7 @@ def _on_device(t):
     current device and refuses memory that device cannot address)."""
     if t is not None and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
         return torch.cuda.device(t.device)
-    return _SAME_DEVICE
+    return _NO_CONTEXT
 
 
 def _stream(stream, t):
@@ -190,6 +196,16 @@ def _stream(stream, t):
     return None
 
 
+def _on_stream(stream, t):
+    """Makes the call's stream torch's current one while the call's own tensors
+    are allocated.  A block of another stream's pool may still be in use by
+    that stream's earlier work, and may be handed out to its later work while
+    this call is writing it."""
+    if stream is None or t is None or not t.is_cuda or stream == torch._C._cuda_getCurrentRawStream(t.get_device()):
+        return _NO_CONTEXT
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device))
+
+
 def _check(status: int):
     if status != 0:
         raise SsdError(status, lib().ssd_last_error().decode())
@@ -199,11 +215,12 @@ def ssd_scan_fwd(x, dt, dt_bias, A, B, C, D=None, init_state=None, out=None,
                  final_state=None, chunk: int = 256, stream=None,
                  algo: int = SSD_ALGO_AUTO, return_final_state: bool = True):
     """Forward SSD scan; returns (out, final_state or None)."""
-    if out is None:
-        out = torch.empty_like(x)
-    if final_state is None and return_final_state:
-        final_state = torch.empty((x.shape[0], x.shape[2], x.shape[3], B.shape[3]),
-                                  dtype=torch.float32, device=x.device)
+    with _on_stream(stream, x):
+        if out is None:
+            out = torch.empty_like(x)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((x.shape[0], x.shape[2], x.shape[3], B.shape[3]),
+                                      dtype=torch.float32, device=x.device)
     keep, d = _descs(x, dt, dt_bias, A, B, C, D, init_state, out, final_state)
     with _on_device(x):
         st = _stream(stream, x)
@@ -222,7 +239,8 @@ def ssd_scan_fwd_noalloc(x, dt, dt_bias, A, B, C, D=None, init_state=None, out=N
     library's fixed device array).  out (and final_state, if wanted) should
     be passed in by callers that cannot allocate; returns (out, final_state)."""
     if out is None:
-        out = torch.empty_like(x)
+        with _on_stream(stream, x):
+            out = torch.empty_like(x)
     with _on_device(x):
         st = _stream(stream, x)
         keep, d = _descs(x, dt, dt_bias, A, B, C, D, init_state, out, final_state)
@@ -257,11 +275,12 @@ def ssd_scan_bwd(x, dt, dt_bias, A, B, C, D, init_state, dout, dfinal_state=None
                   ddt_bias=(H,) if want_dt_bias else None, dD=(H,) if want_D else None,
                   dinit=(b, H, P, N) if want_init else None)
     g = dict(out or {})
-    for k, shp in shapes.items():
-        if shp is not None and g.get(k) is None:
-            g[k] = torch.empty(shp, dtype=torch.float32, device=dev)
-        elif shp is None:
-            g[k] = None
+    with _on_stream(stream, x):
+        for k, shp in shapes.items():
+            if shp is not None and g.get(k) is None:
+                g[k] = torch.empty(shp, dtype=torch.float32, device=dev)
+            elif shp is None:
+                g[k] = None
     with _on_device(x):
         st = _stream(stream, x)
         keep, d = _descs(x, dt, dt_bias, A, B, C, D, init_state, dout, dfinal_state,
@@ -283,11 +302,12 @@ def ssd_scan_bwd_gated(x, dt, dt_bias, A, B, C, z, D, init_state, dout, dfinal_s
                   ddt_bias=(H,) if want_dt_bias else None, dD=(H,) if want_D else None,
                   dinit=(b, H, P, N) if want_init else None, dz=(b, L, H, P))
     g = dict(out or {})
-    for k, shp in shapes.items():
-        if shp is not None and g.get(k) is None:
-            g[k] = torch.empty(shp, dtype=torch.float32, device=dev)
-        elif shp is None:
-            g[k] = None
+    with _on_stream(stream, x):
+        for k, shp in shapes.items():
+            if shp is not None and g.get(k) is None:
+                g[k] = torch.empty(shp, dtype=torch.float32, device=dev)
+            elif shp is None:
+                g[k] = None
     with _on_device(x):
         st = _stream(stream, x)
         keep, d = _descs(x, dt, dt_bias, A, B, C, D, z, init_state, dout, dfinal_state,
@@ -303,11 +323,12 @@ def ssd_scan_fwd_gated(x, dt, dt_bias, A, B, C, z, D=None, init_state=None, out=
                        algo: int = SSD_ALGO_AUTO, return_final_state: bool = True):
     """Forward scan with the output gate: out = y * silu(z); returns
     (out, final_state or None)."""
-    if out is None:
-        out = torch.empty_like(x)
-    if final_state is None and return_final_state:
-        final_state = torch.empty((x.shape[0], x.shape[2], x.shape[3], B.shape[3]),
-                                  dtype=torch.float32, device=x.device)
+    with _on_stream(stream, x):
+        if out is None:
+            out = torch.empty_like(x)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((x.shape[0], x.shape[2], x.shape[3], B.shape[3]),
+                                      dtype=torch.float32, device=x.device)
     with _on_device(x):
         st = _stream(stream, x)
         keep, d = _descs(x, dt, dt_bias, A, B, C, D, z, init_state, out, final_state)
@@ -320,11 +341,12 @@ def ssd_scan_fwd_rows(x, dt, dt_bias, A, B, C, D=None, init_state=None, out=None
                       final_state=None, waves: int = 0, stream=None,
                       return_final_state: bool = True):
     """Row-sliced walk with `waves` waves per workgroup (0 = automatic)."""
-    if out is None:
-        out = torch.empty_like(x)
-    if final_state is None and return_final_state:
-        final_state = torch.empty((x.shape[0], x.shape[2], x.shape[3], B.shape[3]),
-                                  dtype=torch.float32, device=x.device)
+    with _on_stream(stream, x):
+        if out is None:
+            out = torch.empty_like(x)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((x.shape[0], x.shape[2], x.shape[3], B.shape[3]),
+                                      dtype=torch.float32, device=x.device)
     with _on_device(x):
         st = _stream(stream, x)
         keep, d = _descs(x, dt, dt_bias, A, B, C, D, init_state, out, final_state)
@@ -338,11 +360,12 @@ def ssd_selective_scan_fwd(x, dt, dt_bias, A, B, C, D=None, init_state=None, out
                            return_final_state: bool = True):
     """Selective scan with a diagonal A [D, N] per (channel, state index);
     x, dt [b, L, D]; returns (out, final_state or None)."""
-    if out is None:
-        out = torch.empty_like(x)
-    if final_state is None and return_final_state:
-        final_state = torch.empty((x.shape[0], x.shape[2], B.shape[3]), dtype=torch.float32,
-                                  device=x.device)
+    with _on_stream(stream, x):
+        if out is None:
+            out = torch.empty_like(x)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((x.shape[0], x.shape[2], B.shape[3]), dtype=torch.float32,
+                                      device=x.device)
     with _on_device(x):
         st = _stream(stream, x)
         keep, d = _descs(x, dt, dt_bias, A, B, C, D, init_state, out, final_state)
@@ -354,7 +377,8 @@ def ssd_selective_scan_fwd(x, dt, dt_bias, A, B, C, D=None, init_state=None, out
 def ssd_step(state, x, dt, A, B, C, D=None, out=None, stream=None):
     """One recurrent step; ``state`` is updated in place; returns out."""
     if out is None:
-        out = torch.empty_like(x)
+        with _on_stream(stream, x):
+            out = torch.empty_like(x)
     with _on_device(state):
         st = _stream(stream, state)
         keep, d = _descs(state, x, dt, A, B, C, D, out)
@@ -363,16 +387,11 @@ def ssd_step(state, x, dt, A, B, C, D=None, out=None, stream=None):
     return out
 
 
-def _workspace(nbytes: int, t, stream):
+def _workspace(nbytes: int, t):
     """Workspace of one call from torch's allocator, on the stream the call
     runs on (so that the memory is handed out again only behind the call;
-    under graph capture it belongs to the graph)."""
-    if nbytes <= 0:
-        return None
-    if stream is None or not t.is_cuda or stream == _stream(None, t):
-        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device)):
-        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    under graph capture it belongs to the graph).  Called under _on_stream."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=t.device) if nbytes > 0 else None
 
 
 @functools.lru_cache(maxsize=1024)
@@ -381,10 +400,10 @@ def ssd_glr_workspace(b: int, L: int, D: int, backward: bool = False) -> int:
     return int(lib().ssd_glr_workspace(int(b), int(L), int(D), int(backward)))
 
 
-def _glr_workspace(x, backward, stream):
+def _glr_workspace(x, backward):
     if x.dim() != 3:
         return None  # refused by the call
-    return _workspace(ssd_glr_workspace(*x.shape, backward), x, stream)
+    return _workspace(ssd_glr_workspace(*x.shape, backward), x)
 
 
 def ssd_glr_states(x):
@@ -404,13 +423,14 @@ def ssd_glr_fwd(x, r, i, A, r_bias=None, i_bias=None, *, reset=None, lengths=Non
     x, r, i [b, L, D] (views allowed), reset [b, L] uint8 or bool, lengths [b]
     int32; ``states`` (see ssd_glr_states) is filled for ssd_glr_bwd.  Returns
     (out, final_state or None); tokens behind a row's length are not written."""
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if final_state is None and return_final_state:
-        final_state = torch.empty((x.shape[0], x.shape[-1]), dtype=torch.float32, device=x.device)
+    with _on_stream(stream, x):
+        if out is None:
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((x.shape[0], x.shape[-1]), dtype=torch.float32, device=x.device)
+        ws = _glr_workspace(x, False)
     with _on_device(x):
         st = _stream(stream, x)
-        ws = _glr_workspace(x, False, st)
         keep, d = _descs(x, r, i, A, r_bias, i_bias, reset, lengths, init_state, out, final_state, states)
         status = lib().ssd_glr_fwd(*d, ws.data_ptr() if ws is not None else None,
                                    ws.numel() if ws is not None else 0, st)
@@ -427,22 +447,23 @@ def ssd_glr_bwd(x, r, i, A, r_bias=None, i_bias=None, *, reset=None, lengths=Non
     di_bias, dinit (fp32).  ``states`` as filled by ssd_glr_fwd saves a pass
     over the inputs.  ``out`` may hold preallocated tensors under those names."""
     g = dict(out or {})
-    for k in ("dx", "dr", "di"):
-        if g.get(k) is None:
-            g[k] = torch.empty_like(x, memory_format=torch.contiguous_format)
-    for k, want in (("dA", True), ("dr_bias", want_bias), ("di_bias", want_bias)):
-        if not want:
-            g[k] = None
-        elif g.get(k) is None:
-            g[k] = torch.empty_like(A)  # cheaper than torch.empty
-    if not want_init:
-        g["dinit"] = None
-    elif g.get("dinit") is None:
-        g["dinit"] = (torch.empty((x.shape[0], x.shape[-1]), dtype=torch.float32, device=x.device)
-                      if init_state is None else torch.empty_like(init_state))
+    with _on_stream(stream, x):
+        for k in ("dx", "dr", "di"):
+            if g.get(k) is None:
+                g[k] = torch.empty_like(x, memory_format=torch.contiguous_format)
+        for k, want in (("dA", True), ("dr_bias", want_bias), ("di_bias", want_bias)):
+            if not want:
+                g[k] = None
+            elif g.get(k) is None:
+                g[k] = torch.empty_like(A)  # cheaper than torch.empty
+        if not want_init:
+            g["dinit"] = None
+        elif g.get("dinit") is None:
+            g["dinit"] = (torch.empty((x.shape[0], x.shape[-1]), dtype=torch.float32, device=x.device)
+                          if init_state is None else torch.empty_like(init_state))
+        ws = _glr_workspace(x, True)
     with _on_device(x):
         st = _stream(stream, x)
-        ws = _glr_workspace(x, True, st)
         keep, d = _descs(x, r, i, A, r_bias, i_bias, reset, lengths, init_state, states, dout, dfinal_state,
                          g["dx"], g["dr"], g["di"], g["dA"], g["dr_bias"], g["di_bias"], g["dinit"])
         status = lib().ssd_glr_bwd(*d, ws.data_ptr() if ws is not None else None,
@@ -456,7 +477,8 @@ def ssd_glr_step(state, x, r, i, A, r_bias=None, i_bias=None, *, reset=None, out
     """One token of the gated linear recurrence for every row: state [b, D] is
     updated in place (or written to ``new_state``); returns out [b, D]."""
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        with _on_stream(stream, x):
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
     with _on_device(state):
         st = _stream(stream, state)
         keep, d = _descs(state, x, r, i, A, r_bias, i_bias, reset,
@@ -478,10 +500,11 @@ def ssd_norm_rotate_fwd(q, k, q_weight=None, k_weight=None, freqs=None, position
     scan) for each head, then the rotation of their first 2 * len(freqs)
     elements by position * freqs; positions [b, L] int32 or int64 (default
     0..L-1).  Returns (q_out, k_out)."""
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if k_out is None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    with _on_stream(stream, q):
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     with _on_device(q):
         st = _stream(stream, q)
         keep, d = _descs(q, k, q_weight, k_weight, freqs, positions, q_out, k_out)
@@ -497,18 +520,19 @@ def ssd_norm_rotate_bwd(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_o
     a dict of dq, dk (dtype of q) and, when asked for, dq_weight, dk_weight
     (fp32).  ``out`` may hold preallocated tensors under those names."""
     g = dict(out or {})
-    for n, t in (("dq", q), ("dk", k)):
-        if g.get(n) is None:
-            g[n] = torch.empty_like(t, memory_format=torch.contiguous_format)
-    for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
-        if not want_weights:
-            g[n] = None
-        elif g.get(n) is None:
-            g[n] = (torch.empty_like(w) if w is not None else
-                    torch.empty((q.shape[-1],), dtype=torch.float32, device=q.device))
+    with _on_stream(stream, q):
+        for n, t in (("dq", q), ("dk", k)):
+            if g.get(n) is None:
+                g[n] = torch.empty_like(t, memory_format=torch.contiguous_format)
+        for n, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
+            if not want_weights:
+                g[n] = None
+            elif g.get(n) is None:
+                g[n] = (torch.empty_like(w) if w is not None else
+                        torch.empty((q.shape[-1],), dtype=torch.float32, device=q.device))
+        ws = _workspace(ssd_norm_rotate_workspace(q.shape[-1]), q)
     with _on_device(q):
         st = _stream(stream, q)
-        ws = _workspace(ssd_norm_rotate_workspace(q.shape[-1]), q, st)
         keep, d = _descs(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_out, g["dq"], g["dk"],
                          g["dq_weight"], g["dk_weight"])
         status = lib().ssd_norm_rotate_bwd(*d, float(eps), int(interleaved),
