@@ -434,3 +434,37 @@ def test_optional_arguments_and_shared_inputs():
     out, fin = ssd.ssd_glr_fwd(t["x"], t["x"], t["x"], t["A"])
     f = glr_ref.forward(h["x"], h["x"], h["x"], h["A"])
     check("out", out, f["h"], f["eh"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b,L,D,lengths", [(1, 1, 8, None), (2, 17, 40, [17, 4]), (3, 65, 72, [65, 63, 1]),
+                                           (2, 301, 66, [299, 301])])
+def test_tokens_that_do_not_exist_pass_the_state_on(b, L, D, lengths, dtype):
+    # odd row ends with biases of infinity (gates always open or always shut),
+    # for small and for large decays
+    for amin, amax in ((0.001, 0.4), (0.6, 3.0)):
+        t, dout, dfin = make(b, L, D, dtype, seed=18 + L, lengths=lengths, reset=0.01 if L > 100 else 0,
+                             amin=amin, amax=amax)
+        t["r_bias"][::3] = float("inf")
+        t["i_bias"][1::4] = float("inf")
+        h = host(t)
+        out = torch.zeros(b, L, D, dtype=dtype, device=DEV)
+        _, fin = ssd.ssd_glr_fwd(**t, out=out)
+        f = glr_ref.forward(**h)
+        check("out", out, f["h"], f["eh"])
+        check("final", fin, f["fin"], f["efin"])
+        g = ssd.ssd_glr_bwd(**t, dout=dout, dfinal_state=dfin)
+        ref = glr_ref.backward(**h, dout=dout.float().cpu().double().numpy(), dfin=dfin.cpu().double().numpy())
+        for k in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dinit"):
+            check(k, g[k], ref[k], ref["e" + k])
+        # an r of -infinity outweighs a bias of +infinity
+        one = dict(t, lengths=torch.ones(b, dtype=torch.int32, device=DEV))
+        one["r"] = torch.full_like(t["r"], float("-inf"))
+        one["r_bias"] = torch.full_like(t["r_bias"], float("inf"))
+        _, fin = ssd.ssd_glr_fwd(**dict(one, reset=None))
+        assert torch.equal(fin, t["init_state"])
+        # gates always shut: the state stays as it is
+        t["r_bias"][:] = float("-inf")
+        out = torch.zeros(b, L, D, dtype=dtype, device=DEV)
+        _, fin = ssd.ssd_glr_fwd(**dict(t, reset=None), out=out)
+        assert torch.equal(fin, t["init_state"])
