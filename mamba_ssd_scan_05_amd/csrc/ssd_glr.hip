@@ -675,9 +675,9 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float g = vd[j].get(e) + c[e];
-      // capped, so that 1 - s = e s and 1 - gi = e gi stay finite
-      const float er = fminf(hw_exp2(fmaf(vr[j].get(e), -kLog2e, ch[e].nrb)), 0x1p120f);
-      const float ei = fminf(hw_exp2(fmaf(vi[j].get(e), -kLog2e, ch[e].nib)), 0x1p120f);
+      // capped, so that 1 - s = e s and 1 - gi = e gi stay finite (a NaN stays one)
+      const float er = __builtin_elementwise_minimum(hw_exp2(fmaf(vr[j].get(e), -kLog2e, ch[e].nrb)), 0x1p120f);
+      const float ei = __builtin_elementwise_minimum(hw_exp2(fmaf(vi[j].get(e), -kLog2e, ch[e].nib)), 0x1p120f);
       const float sg = __builtin_amdgcn_rcpf(1.f + er), gi = __builtin_amdgcn_rcpf(1.f + ei);
       const float x = vx[j].get(e), ak = a[j][e], beta = be[j][e];
       const float rb = beta > 0.f ? __builtin_amdgcn_rcpf(beta) : 0.f;

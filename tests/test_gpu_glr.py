@@ -468,3 +468,19 @@ def test_tokens_that_do_not_exist_pass_the_state_on(b, L, D, lengths, dtype):
         out = torch.zeros(b, L, D, dtype=dtype, device=DEV)
         _, fin = ssd.ssd_glr_fwd(**dict(t, reset=None), out=out)
         assert torch.equal(fin, t["init_state"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_nan_inputs_show_in_their_gradients(dtype):
+    # a NaN in one token of one channel: the reference's NaNs, no more and no
+    # fewer, for each of the inputs and the output's gradient (finite otherwise)
+    b, L, D = 2, 100, 16
+    for where in ("x", "r", "i", "dout"):
+        t, dout, dfin = make(b, L, D, dtype, seed=19, reset=0.02)
+        (dout if where == "dout" else t[where])[1, 40, 3] = float("nan")
+        g = ssd.ssd_glr_bwd(**t, dout=dout, dfinal_state=dfin)
+        with np.errstate(invalid="ignore"):
+            ref = glr_ref.backward(**host(t), dout=dout.float().cpu().double().numpy(), dfin=dfin.cpu().double().numpy())
+        for k in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dinit"):
+            got = np.isnan(g[k].float().cpu().numpy())
+            assert np.array_equal(got, np.isnan(ref[k])), (where, k, np.argwhere(got != np.isnan(ref[k]))[:4])
