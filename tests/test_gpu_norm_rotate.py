@@ -210,3 +210,53 @@ def test_many_tokens_of_few_heads_and_few_tokens_of_many():
             d = ref.backward(num(x), num(w), pos, num(t["freqs"]), eps, False, num(dy), 130 + Hq + Hk + b * L * (Hq + Hk) // 1024)
             check(dn, g[dn], d["dx"], d["edx"])
             check(wn, g[wn], d["dw"], d["edw"])
+
+
+def inverse_turn():
+    """1 / (2 pi) to 60 digits."""
+    from fractions import Fraction as Q
+
+    def arctan_of_inverse(n):
+        total, term, k = Q(0), Q(1, n), 1
+        while abs(term) > Q(1, 10 ** 62):
+            total, term, k = total + term / k, -term / (n * n), k + 2
+        return total
+
+    return 1 / (8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239)))
+
+
+@pytest.mark.parametrize("i64", [False, True], ids=["i32", "i64"])
+def test_far_positions_against_exact_turns(i64):
+    # angles reduced with rational arithmetic: the fraction of a turn is exact
+    # here, its angle good to 2^-52
+    from fractions import Fraction as Q
+    pos = [0, 1, 105413503, (1 << 24) - 1, (1 << 27) + 1, (1 << 30) - 1, (1 << 31) - 1, -(1 << 31)]
+    if i64:
+        pos += [(1 << 36) + 12345, (1 << 40) - 7, -(1 << 45) - 1, (1 << 50) + 3, (1 << 52) + 1, (1 << 53) - 1, 1 << 53,
+                -(1 << 53)]
+    L, N = len(pos), 32
+    freqs = torch.tensor([1.0, 0.75, 0.1, 10000.0 ** -0.25, 1e-4, 3.1415927, 100.0, 2.0 ** -30], dtype=torch.float32)
+    t, _, _, _ = make(1, L, 2, 1, N, 8, F32, weights=False, explicit=False)
+    t.update(freqs=freqs.to(DEV), positions=torch.tensor([pos], dtype=torch.int64 if i64 else torch.int32, device=DEV))
+    turn = inverse_turn()
+    ang = np.array([[float((p * Q(float(f)) * turn) % 1) * 2 * np.pi for f in freqs] for p in pos])
+    c, s = np.cos(ang)[None, :, None], np.sin(ang)[None, :, None]
+    eps = float(np.float32(1e-6))
+    for inter in (False, True):
+        qo, ko = ssd.ssd_norm_rotate_fwd(**t, interleaved=inter)
+        for x, o in ((t["q"], qo), (t["k"], ko)):
+            x = num(x)
+            u = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+            a, b = (u[..., 0:16:2], u[..., 1:16:2]) if inter else (u[..., :8], u[..., 8:16])
+            y = u.copy()
+            if inter:
+                y[..., 0:16:2], y[..., 1:16:2] = a * c - b * s, a * s + b * c
+            else:
+                y[..., :8], y[..., 8:16] = a * c - b * s, a * s + b * c
+            both = np.abs(u)
+            tot = np.abs(a) + np.abs(b)
+            if inter:
+                both[..., 0:16:2] = both[..., 1:16:2] = tot
+            else:
+                both[..., :8] = both[..., 8:16] = tot
+            check("y", o, y, 23 * ref.U * both)  # the bound of norm_rotate_ref.forward
