@@ -508,7 +508,10 @@ int ssd_glr_step(const ssd_tensor *state, const ssd_tensor *x,
  * Supported: N a multiple of 8 up to 256, npair a multiple of 4 up to N / 2,
  * L at most 2^24, b * L at most 2^25, Hq and Hk at most 2^16.
  * Arithmetic: fp32; angles are reduced to a turn in more than 64 bits, to fp32
- * accuracy at every such position; results are rounded once.  Results do not vary from run to run.  No output may overlap any other
+ * accuracy at every such position; results are rounded once.  Elements up to
+ * 2^59; values below 2^-126 count as 0, but not the squares of larger ones.  The
+ * gradients' products (w dy x summed over a head) have to stay in fp32's range.
+ * Results do not vary from run to run.  No output may overlap any other
  * argument.  Nothing is allocated; the calls may be captured into a HIP graph.
  */
 int ssd_norm_rotate_fwd(const ssd_tensor *q, const ssd_tensor *k,

@@ -15,6 +15,8 @@
 // where a token has fewer) and walks over the rest of the token's heads, so
 // the angles are formed once per token and lane, exact to fp32 at any position
 // (see turn_fraction).  Bound by HBM: x in, y out (backward: x and dy in, dx out).
+#include <float.h>
+
 #include "ssd_device.h"
 #include "ssd_seq.h"
 
@@ -89,6 +91,29 @@ template <int LH> __device__ __forceinline__ float head_sum(float v) {
     v = lane_group_sum<16>(v);
     return v + __shfl_xor(v, 16);
   }
+}
+
+// 1 / sqrt(mean(x^2) + eps) from the lane's eight elements x and the head's sum
+// of squares ss.  SMALL (an eps below kSmallEps, where a mean square may leave
+// fp32's range): a head whose mean square does is summed again with x scaled by
+// a power of two.
+constexpr float kSmallEps = 0x1p-100f;
+template <int LH, bool SMALL>
+__device__ __forceinline__ float rstd_of(const float *x, float ss, float invn, float eps) {
+  const float ms = fmaf(ss, invn, eps);
+  float r = __builtin_amdgcn_rsqf(ms);
+  if constexpr (SMALL) {
+    const bool low = ms < kSmallEps, high = ms > FLT_MAX;
+    if (__builtin_amdgcn_ballot_w64(low || high) != 0) {
+      const float c = low ? 0x1p80f : high ? 0x1p-80f : 1.f;
+      float d = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d = fmaf(x[e] * c, x[e] * c, d);
+      d = head_sum<LH>(d);
+      r = __builtin_amdgcn_rsqf(fmaf(d, invn, eps * c * c)) * c;
+    }
+  }
+  return r;
 }
 
 // A lane's place in a head: its eight elements are [lo, lo + 4) and
@@ -211,7 +236,7 @@ template <typename T, bool BACK> struct Walk {
 // b4 L4096 32 + 8 heads N128 bf16: 56 us (6.0 TB/s, outputs left in the last-
 // level cache); addresses, weights and pair order chosen anew for every head
 // kept the vector ALU busy for 73.
-template <typename T, int LH, bool VEC, bool INTER, bool ONCE>
+template <typename T, int LH, bool VEC, bool INTER, bool ONCE, bool SMALL>
 __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams p) {
   const int lane = threadIdx.x & 63;
   const Item it = item_of<LH>(p, __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)));
@@ -249,7 +274,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
     ss = head_sum<LH>(ss);
-    const float rstd = __builtin_amdgcn_rsqf(fmaf(ss, invn, p.eps));
+    const float rstd = rstd_of<LH, SMALL>(x, ss, invn, p.eps);
     float y[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -268,7 +293,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
 // share of the weights' gradients in registers; one partial row per workgroup.
 // Four waves a SIMD hide the loads: b4 L2048 32 + 8 heads N128 bf16 47 us (5.4
 // TB/s); three and the next head loaded ahead, as in the forward, 64 us.
-template <typename T, int LH, bool VEC, bool INTER>
+template <typename T, int LH, bool VEC, bool INTER, bool SMALL>
 __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotParams p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Slot sl = lane_slot<INTER>(p, lane % LH);
@@ -314,7 +339,7 @@ __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotPar
       }
       ss = head_sum<LH>(ss);
       sv = head_sum<LH>(sv);
-      const float rstd = __builtin_amdgcn_rsqf(fmaf(ss, invn, p.eps));
+      const float rstd = rstd_of<LH, SMALL>(x, ss, invn, p.eps);
       const float m = sv * rstd * invn; // mean(w v n)
       float d[8];
 #pragma unroll
@@ -379,13 +404,20 @@ __global__ __launch_bounds__(1024) void norm_rotate_sum_kernel(const float *part
 // (b4 L2048 of the same, 84 MB, forward and backward: 85 us, past the caches 94).
 constexpr int64_t kOnceBytes = (int64_t)128 << 20;
 
+// A small eps takes kernels of its own: the branch of rstd_of in the forward's
+// walk costs 5 % there (b4 L4096 32 + 8 heads N128 bf16 58.5 -> 61.7 us).
 template <typename T, int LH, bool VEC, bool INTER>
 void launch_pair(bool back, const NormRotParams &p, hipStream_t st) {
-  const uint32_t grid = (uint32_t)((p.nitem + 3) / 4);
+  const uint32_t grid = (uint32_t)((p.nitem + 3) / 4), nwg = (uint32_t)p.nwg;
   const bool once = VEC && p.ntok * (p.Hq + p.Hk) * p.N * (int64_t)sizeof(T) >= kOnceBytes;
-  if (back) norm_rotate_bwd_kernel<T, LH, VEC, INTER><<<(uint32_t)p.nwg, kThreads, 0, st>>>(p);
-  else if (once) norm_rotate_fwd_kernel<T, LH, VEC, INTER, VEC><<<grid, kThreads, 0, st>>>(p);
-  else norm_rotate_fwd_kernel<T, LH, VEC, INTER, false><<<grid, kThreads, 0, st>>>(p);
+  if (p.eps < kSmallEps) {
+    if (back) norm_rotate_bwd_kernel<T, LH, VEC, INTER, true><<<nwg, kThreads, 0, st>>>(p);
+    else norm_rotate_fwd_kernel<T, LH, VEC, INTER, false, true><<<grid, kThreads, 0, st>>>(p);
+  } else {
+    if (back) norm_rotate_bwd_kernel<T, LH, VEC, INTER, false><<<nwg, kThreads, 0, st>>>(p);
+    else if (once) norm_rotate_fwd_kernel<T, LH, VEC, INTER, VEC, false><<<grid, kThreads, 0, st>>>(p);
+    else norm_rotate_fwd_kernel<T, LH, VEC, INTER, false, false><<<grid, kThreads, 0, st>>>(p);
+  }
 }
 template <typename T, int LH, bool VEC> hipError_t launch_one(bool back, const NormRotParams &p, hipStream_t st) {
   if (p.interleaved) launch_pair<T, LH, VEC, true>(back, p, st);

@@ -260,3 +260,28 @@ def test_far_positions_against_exact_turns(i64):
             else:
                 both[..., :8] = both[..., 8:16] = tot
             check("y", o, y, 23 * ref.U * both)  # the bound of norm_rotate_ref.forward
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("N,npair", [(8, 4), (40, 8), (128, 64), (256, 0)])
+def test_mean_squares_outside_the_range_of_fp32(N, npair, dtype):
+    # heads of very small and very large elements beside ordinary ones, no eps
+    t, pos, dyq, dyk = make(2, 6, 3, 1, N, npair, dtype, seed=5)
+    scale = torch.tensor([1e-36, 1e-30, 1e-22, 1.0, 1e18, 1e30], device=DEV).view(1, 6, 1, 1)
+    t["q"], t["k"] = (t["q"].float() * scale).to(dtype), (t["k"].float() * scale.flip(1)).to(dtype)
+    t["q"][0, 3, 1, N // 2] = 1e-25  # one tiny element in an ordinary head
+    qo, ko = ssd.ssd_norm_rotate_fwd(**t, eps=0.0)
+    g = ssd.ssd_norm_rotate_bwd(**t, dq_out=dyq, dk_out=dyk, eps=0.0)
+    for x, w, o, dy, dn, wn in ((t["q"], t["q_weight"], qo, dyq, "dq", "dq_weight"),
+                                (t["k"], t["k_weight"], ko, dyk, "dk", "dk_weight")):
+        y, ey = ref.forward(num(x), num(w), pos, num(t["freqs"]), 0.0, False)
+        check("y", o, y, ey)
+        d = ref.backward(num(x), num(w), pos, num(t["freqs"]), 0.0, False, num(dy), 140)
+        # gradients below 2^-126 count as 0
+        check(dn, g[dn], d["dx"], d["edx"] + 2.0 ** -126)
+        check(wn, g[wn], d["dw"], d["edw"])
+    # the largest element of the contract, with an ordinary eps: 256 squares of
+    # 2^59 sum to 2^126
+    t["q"] = torch.full_like(t["q"], 2.0 ** 59)
+    qo, _ = ssd.ssd_norm_rotate_fwd(t["q"], t["k"], eps=1e-6)
+    assert float((qo.float() - 1).abs().max()) <= 13 * ref.U + torch.finfo(dtype).eps / 2
