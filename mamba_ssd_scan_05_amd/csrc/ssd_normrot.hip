@@ -24,6 +24,7 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFold = 64; // items of a wave summed in registers, backward
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -81,6 +82,17 @@ template <typename T, bool VEC, bool INTER> __device__ __forceinline__ void stor
 #pragma unroll
     for (int e = 0; e < 4; ++e) lo[e] = (T)o[e], hi[e] = (T)o[4 + e];
   }
+}
+
+// Adds a lane's eight sums, in pair order, to its place in LDS.
+template <bool INTER> __device__ __forceinline__ void add8(float *lo, float *hi, const float *v) {
+  float o[8];
+  Raw<float, true> r;
+  r.load(lo, hi);
+  r.template pairs<INTER>(o);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] += v[e];
+  store8<float, true, INTER>(lo, hi, o);
 }
 
 // Sum over aligned groups of LH lanes; every lane gets it.
@@ -290,7 +302,9 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
 }
 
 // Backward, persistent: the waves stride over the items, each lane keeps its
-// share of the weights' gradients in registers; one partial row per workgroup.
+// share of the weights' gradients in registers, and adds it to its place in LDS
+// every kFold items (so that no sum grows by one small term after another
+// however many tokens there are); one partial row per workgroup.
 // Four waves a SIMD hide the loads: b4 L2048 32 + 8 heads N128 bf16 47 us (5.4
 // TB/s); three and the next head loaded ahead, as in the forward, 64 us.
 template <typename T, int LH, bool VEC, bool INTER, bool SMALL>
@@ -299,78 +313,87 @@ __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotPar
   const Slot sl = lane_slot<INTER>(p, lane % LH);
   const int step = 1 << p.hg_log, gap = sl.hi - sl.lo;
   const float invn = 1.f / (float)p.N;
-  float aq[8], ak[8];
+  __shared__ __align__(16) float part[kThreads / LH][2][8 * LH];
+  float *const mine = part[threadIdx.x / LH][0];
+  uint32_t item = blockIdx.x * (kThreads / 64) + wave;
+  bool folded = false;
+  do {
+    float aq[8], ak[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
-  for (uint32_t item = blockIdx.x * (kThreads / 64) + wave; item < (uint32_t)p.nitem;
-       item += gridDim.x * (kThreads / 64)) {
-    const Item it = item_of<LH>(p, item);
-    if (!it.live || it.head >= it.hend) continue;
-    Walk<T, true> cur;
-    cur.h = it.head;
-    cur.at(p, it, sl);
-    Raw<T, VEC> rx{}, rv{};
-    if (sl.in) rx.load(cur.src, cur.src + gap), rv.load(cur.dy, cur.dy + gap);
-    const Turn an = angles(p, sl, it.tok, it.t);
-    float w[8], acc[8];
+    for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
+    for (int k = 0; k < kFold && item < (uint32_t)p.nitem; ++k, item += gridDim.x * (kThreads / 64)) {
+      const Item it = item_of<LH>(p, item);
+      if (!it.live || it.head >= it.hend) continue;
+      Walk<T, true> cur;
+      cur.h = it.head;
+      cur.at(p, it, sl);
+      Raw<T, VEC> rx{}, rv{};
+      if (sl.in) rx.load(cur.src, cur.src + gap), rv.load(cur.dy, cur.dy + gap);
+      const Turn an = angles(p, sl, it.tok, it.t);
+      float w[8], acc[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    bool fresh = true;
-    for (;;) {
-      if (fresh) load_weight<VEC, INTER>(cur.isq ? p.qw : p.kw, sl, w);
-      Walk<T, true> nxt = cur;
-      nxt.next(p, it, sl, step);
-      fresh = nxt.isq != cur.isq;
-      const bool more = nxt.h < it.hend;
-      float x[8], dy[8], v[8], wv[8];
-      rx.template pairs<INTER>(x);
-      rv.template pairs<INTER>(dy);
-      float ss = 0.f, sv = 0.f;
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      bool fresh = true;
+      for (;;) {
+        if (fresh) load_weight<VEC, INTER>(cur.isq ? p.qw : p.kw, sl, w);
+        Walk<T, true> nxt = cur;
+        nxt.next(p, it, sl, step);
+        fresh = nxt.isq != cur.isq;
+        const bool more = nxt.h < it.hend;
+        float x[8], dy[8], v[8], wv[8];
+        rx.template pairs<INTER>(x);
+        rv.template pairs<INTER>(dy);
+        float ss = 0.f, sv = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = fmaf(dy[e], an.c[e], dy[4 + e] * an.s[e]);
-        v[4 + e] = fmaf(dy[4 + e], an.c[e], -(dy[e] * an.s[e]));
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        wv[e] = v[e] * w[e];
-        ss = fmaf(x[e], x[e], ss);
-        sv = fmaf(wv[e], x[e], sv);
-      }
-      ss = head_sum<LH>(ss);
-      sv = head_sum<LH>(sv);
-      const float rstd = rstd_of<LH, SMALL>(x, ss, invn, p.eps);
-      const float m = sv * rstd * invn; // mean(w v n)
-      float d[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = x[e] * rstd;
-        d[e] = rstd * fmaf(-n, m, wv[e]);
-        acc[e] = fmaf(v[e], n, acc[e]);
-      }
-      if (sl.in) store8<T, VEC, INTER>(cur.dst, cur.dst + gap, d);
-      if (fresh || !more) {
-        // the sums of one kind of head
+        for (int e = 0; e < 4; ++e) {
+          v[e] = fmaf(dy[e], an.c[e], dy[4 + e] * an.s[e]);
+          v[4 + e] = fmaf(dy[4 + e], an.c[e], -(dy[e] * an.s[e]));
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          aq[e] += cur.isq ? acc[e] : 0.f;
-          ak[e] += cur.isq ? 0.f : acc[e];
-          acc[e] = 0.f;
+          wv[e] = v[e] * w[e];
+          ss = fmaf(x[e], x[e], ss);
+          sv = fmaf(wv[e], x[e], sv);
         }
+        ss = head_sum<LH>(ss);
+        sv = head_sum<LH>(sv);
+        const float rstd = rstd_of<LH, SMALL>(x, ss, invn, p.eps);
+        const float m = sv * rstd * invn; // mean(w v n)
+        float d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float n = x[e] * rstd;
+          d[e] = rstd * fmaf(-n, m, wv[e]);
+          acc[e] = fmaf(v[e], n, acc[e]);
+        }
+        if (sl.in) store8<T, VEC, INTER>(cur.dst, cur.dst + gap, d);
+        if (fresh || !more) {
+          // the sums of one kind of head
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            aq[e] += cur.isq ? acc[e] : 0.f;
+            ak[e] += cur.isq ? 0.f : acc[e];
+            acc[e] = 0.f;
+          }
+        }
+        if (!more) break;
+        cur = nxt;
+        if (sl.in) rx.load(cur.src, cur.src + gap), rv.load(cur.dy, cur.dy + gap);
       }
-      if (!more) break;
-      cur = nxt;
-      if (sl.in) rx.load(cur.src, cur.src + gap), rv.load(cur.dy, cur.dy + gap);
     }
-  }
-  // lane groups of the workgroup in a fixed order
-  __shared__ __align__(16) float part[kThreads / LH][2][8 * LH];
-  const int g = threadIdx.x / LH;
-  if (sl.in) {
-    store8<float, true, INTER>(&part[g][0][sl.lo], &part[g][0][sl.hi], aq);
-    store8<float, true, INTER>(&part[g][1][sl.lo], &part[g][1][sl.hi], ak);
-  }
+    if (sl.in) {
+      if (folded) {
+        add8<INTER>(mine + sl.lo, mine + sl.hi, aq);
+        add8<INTER>(mine + 8 * LH + sl.lo, mine + 8 * LH + sl.hi, ak);
+      } else {
+        store8<float, true, INTER>(mine + sl.lo, mine + sl.hi, aq);
+        store8<float, true, INTER>(mine + 8 * LH + sl.lo, mine + 8 * LH + sl.hi, ak);
+      }
+    }
+    folded = true;
+  } while (item < (uint32_t)p.nitem);
   __syncthreads();
+  // lane groups of the workgroup in a fixed order
   for (int c = threadIdx.x; c < 2 * p.N; c += kThreads) {
     const int which = c >= p.N, el = c - which * p.N;
     float s = 0.f;

@@ -285,3 +285,19 @@ def test_mean_squares_outside_the_range_of_fp32(N, npair, dtype):
     t["q"] = torch.full_like(t["q"], 2.0 ** 59)
     qo, _ = ssd.ssd_norm_rotate_fwd(t["q"], t["k"], eps=1e-6)
     assert float((qo.float() - 1).abs().max()) <= 13 * ref.U + torch.finfo(dtype).eps / 2
+
+
+def test_weight_gradients_of_very_many_tokens():
+    # one head vector for all of 2^23 tokens (stride 0): 2048 of them to every
+    # wave.  The sums of equal terms are exact but for fp32's roundings, which
+    # may number a few dozen at each level however many tokens there are (64
+    # items in registers, 32 such sums, 8 lane groups).
+    L, N = 1 << 23, 256
+    t, _, dyq, dyk = make(1, 1, 1, 1, N, 0, BF, seed=6)
+    g = ssd.ssd_norm_rotate_bwd(t["q"].expand(1, L, 1, N), t["k"].expand(1, L, 1, N), t["q_weight"], t["k_weight"], None,
+                                None, dyq.expand(1, L, 1, N), dyk.expand(1, L, 1, N))
+    for x, w, dy, dn, wn in ((t["q"], t["q_weight"], dyq, "dq", "dq_weight"), (t["k"], t["k_weight"], dyk, "dk", "dk_weight")):
+        d = ref.backward(num(x), num(w), np.zeros((1, 1)), None, float(np.float32(1e-6)), False, num(dy), 64 + 32 + 8)
+        check(wn, g[wn], L * d["dw"], L * d["edw"])
+        check(dn, g[dn][:, -1:], d["dx"], d["edx"])
+        assert bool((g[dn] == g[dn][:, :1]).all())
