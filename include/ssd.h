@@ -453,7 +453,8 @@ int ssd_glr_fwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i,
  * <dfinal_state, final state>.  Inputs as for ssd_glr_fwd;
  * states is what ssd_glr_fwd wrote for the same inputs, or NULL: then they
  * are formed again from the inputs (one more pass over x, r and i).
- * dout [b, L, D] has the dtype of x; dfinal_state [b, D] f32 may be NULL.
+ * dout [b, L, D] has the dtype of x or is f32 (as ssd_scan_bwd writes its
+ * gradients); dfinal_state [b, D] f32 may be NULL.
  * Written in full: dx, dr, di [b, L, D] in the dtype of x (zero behind a
  * row's length); dA, dr_bias, di_bias [D] and dinit_state [b, D] f32, each of
  * these four may be NULL.  Where sqrt(1 - a^2) is 0 the gradient through it

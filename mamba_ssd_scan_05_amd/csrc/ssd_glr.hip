@@ -109,14 +109,14 @@ __device__ __forceinline__ float look_back(const uint64_t *prev, int64_t step, i
 }
 
 // V elements of one row at byte offset off (per lane) + so (per wave), in one
-// access of 2, 4 or 16 bytes.  A lane without channels passes kNowhere: its
+// access of 2, 4, 8 or 16 bytes.  A lane without channels passes kNowhere: its
 // reads give zero and its stores are dropped.  AUX: the cache policy (0 or
 // kNonTemporal).
 constexpr uint32_t kNowhere = 0xFFFFFF00u; // past every range
 template <typename T, int V, int AUX> struct Row {
   static constexpr int kBytes = V * (int)sizeof(T);
   static constexpr int W = kBytes < 4 ? 1 : kBytes / 4; // 32-bit words held
-  static_assert(kBytes == 2 || kBytes == 4 || kBytes == 16, "one access");
+  static_assert(kBytes == 2 || kBytes == 4 || kBytes == 8 || kBytes == 16, "one access");
   uint32_t d[W];
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -132,6 +132,9 @@ template <typename T, int V, int AUX> struct Row {
     if constexpr (W == 4) {
       const i32x4 v = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, so, AUX));
       d[0] = (uint32_t)v[0], d[1] = (uint32_t)v[1], d[2] = (uint32_t)v[2], d[3] = (uint32_t)v[3];
+    } else if constexpr (W == 2) {
+      const i32x2 v = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, so, AUX));
+      d[0] = (uint32_t)v[0], d[1] = (uint32_t)v[1];
     } else if constexpr (kBytes == 4) {
       d[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, so, AUX);
     } else {
@@ -468,11 +471,14 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
 // once more for the gradients, which costs less than the registers to keep them
 // (two workgroups a compute unit instead of one: b4 L2048 D5120 bf16 150 us
 // against 227).  587 MB at 3.9 TB/s; the vector ALU is busy 61 % of the time
-// (74 instructions an element).
+// (74 instructions an element).  TD is the type of dout: with bf16 inputs also
+// the fp32 of ssd_scan_bwd's gradients.  That takes eight registers more; held to
+// four waves a SIMD it keeps four to seven in scratch (the same case 177 us, not
+// held 224; a cast to bf16 before costs 50).
 // ---------------------------------------------------------------------------
-template <typename T, int V, int NW, bool CUT, int AUX>
-__global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
-  constexpr int kTile = 64 * V, TT = kBwdTokens, kChunk = NW * TT, ES = (int)sizeof(T);
+template <typename T, typename TD, int V, int NW, bool CUT, int AUX>
+__global__ __launch_bounds__(64 * NW, sizeof(TD) > sizeof(T) ? 4 : 1) void glr_bwd_kernel(GlrParams p) {
+  constexpr int kTile = 64 * V, TT = kBwdTokens, kChunk = NW * TT, ES = (int)sizeof(T), ESD = (int)sizeof(TD);
   __shared__ float fA[NW][kTile], fw[NW][kTile], bA[NW][kTile], bw[NW][kTile];
   __shared__ float fcarry[NW][kTile], bcarry[NW][kTile];
   __shared__ int aggcut[NW];
@@ -488,6 +494,7 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   const int ntp = min(kChunk, p.L - t0), ntpw = max(0, min(TT, ntp - lt0)); // rows of the gradients
   const int c0 = pl.tile * kTile + lane * V; // V divides D: all of a lane's channels exist or none
   const uint32_t off = c0 < p.D ? (uint32_t)(c0 * ES) : kNowhere;
+  const uint32_t offd = c0 < p.D ? (uint32_t)(c0 * ESD) : kNowhere;
   const int64_t prow = ((int64_t)pl.row * p.nchunk + pl.chunk) * 3 * p.D; // row of the partial sums
   const int64_t g0 = ((int64_t)pl.row * p.L + t0) * p.D;
   const __amdgpu_buffer_rsrc_t odx = rows_rsrc(p.dx, g0, p.D, ntp, p.D, ES);
@@ -514,15 +521,16 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
   const __amdgpu_buffer_rsrc_t rx = rows_rsrc(p.x, pl.row * p.xb + (int64_t)t0 * p.xt, p.xt, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t rr = rows_rsrc(p.r, pl.row * p.rb_ + (int64_t)t0 * p.rt, p.rt, nt, p.D, ES);
   const __amdgpu_buffer_rsrc_t ri = rows_rsrc(p.i, pl.row * p.ib_ + (int64_t)t0 * p.it, p.it, nt, p.D, ES);
-  const __amdgpu_buffer_rsrc_t rd = rows_rsrc(p.dout, pl.row * p.db + (int64_t)t0 * p.dt, p.dt, nt, p.D, ES);
-  Row<T, V, AUX> vx[TT], vr[TT], vi[TT], vd[TT];
+  const __amdgpu_buffer_rsrc_t rd = rows_rsrc(p.dout, pl.row * p.db + (int64_t)t0 * p.dt, p.dt, nt, p.D, ESD);
+  Row<T, V, AUX> vx[TT], vr[TT], vi[TT];
+  Row<TD, V, AUX> vd[TT];
   if (ntw == TT) {
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
       vr[j].load(rr, off, (lt0 + j) * p.rt * ES);
       vi[j].load(ri, off, (lt0 + j) * p.it * ES);
       vx[j].load(rx, off, (lt0 + j) * p.xt * ES);
-      vd[j].load(rd, off, (lt0 + j) * p.dt * ES);
+      vd[j].load(rd, offd, (lt0 + j) * p.dt * ESD);
     }
   } else {
 #pragma unroll
@@ -531,7 +539,7 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p) {
         vr[j].load(rr, off, (lt0 + j) * p.rt * ES);
         vi[j].load(ri, off, (lt0 + j) * p.it * ES);
         vx[j].load(rx, off, (lt0 + j) * p.xt * ES);
-        vd[j].load(rd, off, (lt0 + j) * p.dt * ES);
+        vd[j].load(rd, offd, (lt0 + j) * p.dt * ESD);
       } else {
         vr[j].shut(), vi[j].zero(), vx[j].zero(), vd[j].zero();
       }
@@ -796,13 +804,13 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
   store_row<T, V, 0>(rows_rsrc(p.out, (int64_t)row * p.D, 0, 1, p.D, ES), (uint32_t)(c0 * ES), 0, h);
 }
 
-template <typename T, int V, int NW, int AUX> void launch_waves(bool back, const GlrParams &p, hipStream_t st) {
+template <typename T, typename TD, int V, int NW, int AUX> void launch_waves(bool back, const GlrParams &p, hipStream_t st) {
   const dim3 grid((uint32_t)p.b * (uint32_t)p.ntile * (uint32_t)p.nchunk);
-  if (p.reset) {
-    if (back) glr_bwd_kernel<T, V, NW, true, AUX><<<grid, 64 * NW, 0, st>>>(p);
-    else glr_fwd_kernel<T, V, NW, true, AUX><<<grid, 64 * NW, 0, st>>>(p);
+  if (back) {
+    if (p.reset) glr_bwd_kernel<T, TD, V, NW, true, AUX><<<grid, 64 * NW, 0, st>>>(p);
+    else glr_bwd_kernel<T, TD, V, NW, false, AUX><<<grid, 64 * NW, 0, st>>>(p);
   } else {
-    if (back) glr_bwd_kernel<T, V, NW, false, AUX><<<grid, 64 * NW, 0, st>>>(p);
+    if (p.reset) glr_fwd_kernel<T, V, NW, true, AUX><<<grid, 64 * NW, 0, st>>>(p);
     else glr_fwd_kernel<T, V, NW, false, AUX><<<grid, 64 * NW, 0, st>>>(p);
   }
 }
@@ -815,12 +823,12 @@ constexpr int64_t kOnceBytes = (int64_t)128 << 20;
 // As many waves as the rows need (b256 L32 D5120 bf16 forward: eight 119 us, four
 // 88, two 84; b64 L17: eight 27, two 16; a workgroup has a thread for each of
 // its 128 or 64 channels, so two at least).
-template <typename T, int V> hipError_t scan_launch(bool back, const GlrParams &p, hipStream_t st) {
+template <typename T, typename TD, int V> hipError_t scan_launch(bool back, const GlrParams &p, hipStream_t st) {
   const int need = (p.L + (back ? kBwdTokens : kFwdTokens) - 1) / (back ? kBwdTokens : kFwdTokens);
-  if (need <= 2) launch_waves<T, V, 2, 0>(back, p, st);
-  else if (need <= 4) launch_waves<T, V, 4, 0>(back, p, st);
-  else if ((int64_t)p.b * p.L * p.D * 3 * (int64_t)sizeof(T) < kOnceBytes) launch_waves<T, V, kWaves, 0>(back, p, st);
-  else launch_waves<T, V, kWaves, kNonTemporal>(back, p, st);
+  if (need <= 2) launch_waves<T, TD, V, 2, 0>(back, p, st);
+  else if (need <= 4) launch_waves<T, TD, V, 4, 0>(back, p, st);
+  else if ((int64_t)p.b * p.L * p.D * 3 * (int64_t)sizeof(T) < kOnceBytes) launch_waves<T, TD, V, kWaves, 0>(back, p, st);
+  else launch_waves<T, TD, V, kWaves, kNonTemporal>(back, p, st);
   return hipGetLastError();
 }
 
@@ -840,8 +848,9 @@ hipError_t launch_glr(int dtype, bool vec, bool back, const GlrParams &p0, hipSt
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dtype != 1) return scan_launch<float, 1>(back, p, st);
-  return vec ? scan_launch<__bf16, 2>(back, p, st) : scan_launch<__bf16, 1>(back, p, st);
+  if (dtype != 1) return scan_launch<float, float, 1>(back, p, st);
+  if (back && p.dout_f32) return vec ? scan_launch<__bf16, float, 2>(back, p, st) : scan_launch<__bf16, float, 1>(back, p, st);
+  return vec ? scan_launch<__bf16, __bf16, 2>(back, p, st) : scan_launch<__bf16, __bf16, 1>(back, p, st);
 }
 
 hipError_t launch_glr_sum(const float *part, int n, int D, float *dA, float *drb, float *dib, hipStream_t st) {

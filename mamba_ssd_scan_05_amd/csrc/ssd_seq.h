@@ -15,6 +15,7 @@ constexpr int kGlrChunk = 128;
 constexpr int kGlrSegment = 64; // SSD_GLR_SEGMENT
 struct GlrParams {
   const void *x, *r, *i, *dout;          // [b, L, D], last dim contiguous
+  int dout_f32;                          // dout is fp32 whatever x is
   int64_t xb, rb_, ib_, db;              // batch strides, elements
   int xt, rt, it, dt;                    // token strides, elements
   const float *A, *rbias, *ibias;        // [D]; the biases may be null
@@ -39,7 +40,7 @@ struct GlrParams {
 inline int64_t glr_wstride(int64_t D) { return (D + 127) / 128 * 128; }
 inline int64_t glr_chain_bytes(int64_t b, int64_t nchunk, int64_t D) { return b * nchunk * glr_wstride(D) * 8 + 16; }
 // dtype 1 = bf16, 0 = fp32; vec: bf16 widths, strides and pointers allow 4-byte
-// accesses.
+// accesses (of an fp32 dout 8-byte ones).
 hipError_t launch_glr(int dtype, bool vec, bool back, const GlrParams &p, hipStream_t stream);
 // Sums n partial rows [3][D] into dA, d r_bias, d i_bias (each may be null).
 hipError_t launch_glr_sum(const float *part, int n, int D, float *dA, float *drb, float *dib, hipStream_t stream);

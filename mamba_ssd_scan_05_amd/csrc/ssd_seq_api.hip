@@ -83,6 +83,9 @@ int act_dtype(const ssd_tensor *t, const char *name) {
   return SSD_OK;
 }
 
+// The type asked of an output's gradient: f32 or that of x.
+int grad_dtype(const ssd_tensor *t, const ssd_tensor *x) { return t && t->dtype == SSD_F32 ? SSD_F32 : x->dtype; }
+
 // A call's tensors, for the checks over all of them.
 struct Args {
   static constexpr int kMax = 24;
@@ -368,7 +371,7 @@ int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, c
   const int64_t b = x->shape[0], L = x->shape[1], D = x->shape[2];
   const int64_t so[3] = {b, L, D}, sf[2] = {b, D}, ss[3] = {b, plan.nseg, D}, sd[1] = {D};
   if (states) SSD_CHECK(check_arg(states, "states", SSD_F32, 3, ss));
-  SSD_CHECK(check_arg(dout, "dout", x->dtype, 3, so, true, kMaxStride));
+  SSD_CHECK(check_arg(dout, "dout", grad_dtype(dout, x), 3, so, true, kMaxStride));
   if (dfinal_state) SSD_CHECK(check_arg(dfinal_state, "dfinal_state", SSD_F32, 2, sf));
   SSD_CHECK(check_arg(dx, "dx", x->dtype, 3, so));
   SSD_CHECK(check_arg(dr, "dr", x->dtype, 3, so));
@@ -407,11 +410,12 @@ int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, c
   p.dout = dout->data;
   p.db = b == 1 ? 0 : dout->strides[0];
   p.dt = L == 1 ? 0 : (int)dout->strides[1];
+  p.dout_f32 = dout->dtype == SSD_F32;
   p.dfin = fptr(dfinal_state);
   p.dx = dx->data; p.dr = dr->data; p.di = di->data;
   p.dinit = fptr_out(dinit_state);
   set_chain(&p, plan.nseg, ws);
-  e = launch_glr(x->dtype, vec && rows4b(dout) && rows4b(dx) && rows4b(dr) && rows4b(di), true, p, st);
+  e = launch_glr(x->dtype, vec && rows_of(dout, 2 * elem_size(dout->dtype)) && rows4b(dx) && rows4b(dr) && rows4b(di), true, p, st);
   if (e != hipSuccess) return hip_fail(e, "gated recurrence backward launch");
   e = launch_glr_sum(p.part, (int)(b * plan.nseg), (int)D, fptr_out(dA), fptr_out(dr_bias), fptr_out(di_bias), st);
   return e == hipSuccess ? SSD_OK : hip_fail(e, "gated recurrence parameter sums launch");

@@ -443,8 +443,9 @@ def ssd_glr_bwd(x, r, i, A, r_bias=None, i_bias=None, *, reset=None, lengths=Non
                 out: dict = None, stream=None):
     """Gradients of ssd_glr_fwd for <dout, out> + <dfinal_state, final state>.
 
-    Returns a dict: dx, dr, di (dtype of x), dA and, when asked for, dr_bias,
-    di_bias, dinit (fp32).  ``states`` as filled by ssd_glr_fwd saves a pass
+    ``dout`` in the dtype of x or fp32 (what ssd_scan_bwd returns).  Returns a
+    dict: dx, dr, di (dtype of x), dA and, when asked for, dr_bias, di_bias,
+    dinit (fp32).  ``states`` as filled by ssd_glr_fwd saves a pass
     over the inputs.  ``out`` may hold preallocated tensors under those names."""
     g = dict(out or {})
     with _on_stream(stream, x):

@@ -235,3 +235,23 @@ def test_reference_bound_holds_for_a_plain_fp32_evaluation():
         assert np.all(err <= f["eh"][:, k])
         worst = max(worst, float((err / np.maximum(f["eh"][:, k], 1e-30)).max()))
     assert 0.003 < worst <= 1.0, worst
+
+
+def test_backward_takes_fp32_output_gradients():
+    # f32 dout with bf16 inputs passes the checks (only the CPU memory is
+    # refused); bf16 with f32 inputs does not, nor any other mixture
+    a = bwd_args()
+    a["dout"] = torch.zeros(2, 300, 24)
+    st, msg = call_bwd(a)
+    assert st == 4 and ("device" in msg or "address" in msg), (st, msg)
+    a = bwd_args(dtype=F32)
+    a["dout"] = torch.zeros(2, 300, 24, dtype=BF)
+    st, msg = call_bwd(a)
+    assert st == 3 and "dout" in msg, (st, msg)
+    for k in ("r", "dx", "di"):
+        a = bwd_args()
+        a[k] = torch.zeros(2, 300, 24)
+        assert call_bwd(a)[0] == 3, k
+    a = bwd_args()
+    a["dout"] = torch.zeros(2, 300, 24, dtype=torch.float16)
+    assert call_bwd(a)[0] == 3

@@ -484,3 +484,48 @@ def test_nan_inputs_show_in_their_gradients(dtype):
         for k in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dinit"):
             got = np.isnan(g[k].float().cpu().numpy())
             assert np.array_equal(got, np.isnan(ref[k])), (where, k, np.argwhere(got != np.isnan(ref[k]))[:4])
+
+
+@pytest.mark.parametrize("case", SHAPES, ids=["b%d_L%d_D%d_%s" % c[:4] for c in SHAPES])
+def test_gradients_from_fp32_output_gradients(case):
+    # bf16 inputs and the fp32 gradient of a later fp32 stage, as a strided view
+    # where the case has one
+    b, L, D, layout, reset, lengths, init = case
+    t, _, dfin = make(b, L, D, BF, seed=2 * L + D, layout=layout, reset=reset, lengths=lengths, init=init)
+    g = torch.Generator().manual_seed(L)
+    dout = torch.randn(b, L, D + (3 if layout == "offset" else 0), generator=g).to(DEV)[..., :D]
+    if layout == "time_major":
+        dout = dout.transpose(0, 1).contiguous().transpose(0, 1)
+    if layout == "broadcast":
+        dout = dout[:, :1].expand(b, L, D)
+    states = ssd.ssd_glr_states(t["x"])
+    ssd.ssd_glr_fwd(**t, states=states)
+    ref = glr_ref.backward(**host(t), dout=dout.cpu().double().numpy(), dfin=dfin.cpu().double().numpy())
+    for saved in (states, None):
+        got = ssd.ssd_glr_bwd(**t, dout=dout, dfinal_state=dfin, states=saved)
+        assert got["dx"].dtype == BF and got["dA"].dtype == F32
+        for k in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dinit"):
+            check(k, got[k], ref[k], ref["e" + k])
+
+
+@pytest.mark.parametrize("dtype,ddtype", [(F32, F32), (BF, BF), (BF, F32)], ids=["f32", "bf16", "bf16_f32"])
+def test_inputs_that_pass_the_caches_by(dtype, ddtype):
+    # 64 rows that are views of one: 128 MB and more, every row as the first
+    b, L, D = 64, 512, 700
+    t, dout, dfin = make(1, L, D, dtype, seed=20, reset=0.01, init=False)
+    dout = dout.to(ddtype)
+    w = {k: v.expand(b, *v.shape[1:]) if k in ("x", "r", "i") else v for k, v in t.items()}
+    w["reset"] = t["reset"].expand(b, L).contiguous()
+    out, fin = ssd.ssd_glr_fwd(**w)
+    g = ssd.ssd_glr_bwd(**w, dout=dout.expand(b, L, D), dfinal_state=dfin.expand(b, D).contiguous())
+    h = host(t)
+    f = glr_ref.forward(**h)
+    ref = glr_ref.backward(**h, dout=dout.float().cpu().double().numpy(), dfin=dfin.cpu().double().numpy())
+    check("out", out[:1], f["h"], f["eh"])
+    check("final", fin[:1], f["fin"], f["efin"])
+    for v in (out, fin, *(g[k] for k in ("dx", "dr", "di", "dinit"))):
+        assert bool((v == v[:1]).all())
+    for k in ("dx", "dr", "di", "dinit"):
+        check(k, g[k][:1], ref[k], ref["e" + k])
+    for k in ("dA", "dr_bias", "di_bias"):
+        check(k, g[k], b * ref[k], b * ref["e" + k])
