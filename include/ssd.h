@@ -527,7 +527,8 @@ int64_t ssd_norm_rotate_workspace(int64_t N);
 
 /*
  * ssd_norm_rotate_bwd -- gradients for <dq_out, q_out> + <dk_out, k_out>.
- * dq_out, dk_out: dtype and shape of q and k, views allowed.  Written in full:
+ * dq_out, dk_out: shape of q and k, dtype of q or both f32 (as ssd_scan_bwd writes
+ * its gradients), views allowed.  Written in full:
  * dq, dk (dtype of q, dense) and dq_weight, dk_weight [N] f32, each of these
  * two may be NULL.  Nothing of the forward is needed but its inputs.
  */

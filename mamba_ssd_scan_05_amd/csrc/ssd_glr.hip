@@ -473,8 +473,8 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
 // against 227).  587 MB at 3.9 TB/s; the vector ALU is busy 61 % of the time
 // (74 instructions an element).  TD is the type of dout: with bf16 inputs also
 // the fp32 of ssd_scan_bwd's gradients.  That takes eight registers more; held to
-// four waves a SIMD it keeps four to seven in scratch (the same case 177 us, not
-// held 224; a cast to bf16 before costs 50).
+// four waves a SIMD it keeps four to seven in scratch (the same case 178 us, not
+// held 224, with a cast to bf16 before 185).
 // ---------------------------------------------------------------------------
 template <typename T, typename TD, int V, int NW, bool CUT, int AUX>
 __global__ __launch_bounds__(64 * NW, sizeof(TD) > sizeof(T) ? 4 : 1) void glr_bwd_kernel(GlrParams p) {

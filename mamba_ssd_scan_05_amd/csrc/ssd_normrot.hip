@@ -213,8 +213,10 @@ template <int LH> __device__ __forceinline__ Item item_of(const NormRotParams &p
 
 // The lane group's walk over its heads: queries first, then keys.  Where a
 // head lies is formed at the first one of either kind and advanced from there.
-template <typename T, bool BACK> struct Walk {
-  const T *src, *dy;
+// TD: the type of the outputs' gradients.
+template <typename T, bool BACK, typename TD = T> struct Walk {
+  const T *src;
+  const TD *dy;
   T *dst;
   int h;
   bool isq;
@@ -224,8 +226,8 @@ template <typename T, bool BACK> struct Walk {
     src = isq ? (const T *)p.q + it.row * p.qb + it.t * p.qt + h * p.qh
               : (const T *)p.k + it.row * p.kb + it.t * p.kt + hk * p.kh;
     if constexpr (BACK)
-      dy = isq ? (const T *)p.dyq + it.row * p.dqb + it.t * p.dqt + h * p.dqh
-               : (const T *)p.dyk + it.row * p.dkb + it.t * p.dkt + hk * p.dkh;
+      dy = isq ? (const TD *)p.dyq + it.row * p.dqb + it.t * p.dqt + h * p.dqh
+               : (const TD *)p.dyk + it.row * p.dkb + it.t * p.dkt + hk * p.dkh;
     dst = isq ? (T *)p.oq + (it.tok * p.Hq + h) * p.N : (T *)p.ok + (it.tok * p.Hk + hk) * p.N;
     src += sl.lo, dst += sl.lo;
     if constexpr (BACK) dy += sl.lo;
@@ -306,8 +308,12 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams
 // every kFold items (so that no sum grows by one small term after another
 // however many tokens there are); one partial row per workgroup.
 // Four waves a SIMD hide the loads: b4 L2048 32 + 8 heads N128 bf16 47 us (5.4
-// TB/s); three and the next head loaded ahead, as in the forward, 64 us.
-template <typename T, int LH, bool VEC, bool INTER, bool SMALL>
+// TB/s); three and the next head loaded ahead, as in the forward, 64 us.  128
+// registers do not hold every variant: the fp32 ones with pairs in halves keep six
+// to eight in scratch, those moved element by element two to five, some others two
+// or three.  TD is the type of the outputs' gradients: fp32 with bf16 inputs is
+// what ssd_scan_bwd writes (the same case 67 us, with casts to bf16 before 92).
+template <typename T, typename TD, int LH, bool VEC, bool INTER, bool SMALL>
 __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotParams p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Slot sl = lane_slot<INTER>(p, lane % LH);
@@ -324,10 +330,11 @@ __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotPar
     for (int k = 0; k < kFold && item < (uint32_t)p.nitem; ++k, item += gridDim.x * (kThreads / 64)) {
       const Item it = item_of<LH>(p, item);
       if (!it.live || it.head >= it.hend) continue;
-      Walk<T, true> cur;
+      Walk<T, true, TD> cur;
       cur.h = it.head;
       cur.at(p, it, sl);
-      Raw<T, VEC> rx{}, rv{};
+      Raw<T, VEC> rx{};
+      Raw<TD, VEC> rv{};
       if (sl.in) rx.load(cur.src, cur.src + gap), rv.load(cur.dy, cur.dy + gap);
       const Turn an = angles(p, sl, it.tok, it.t);
       float w[8], acc[8];
@@ -336,7 +343,7 @@ __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotPar
       bool fresh = true;
       for (;;) {
         if (fresh) load_weight<VEC, INTER>(cur.isq ? p.qw : p.kw, sl, w);
-        Walk<T, true> nxt = cur;
+        Walk<T, true, TD> nxt = cur;
         nxt.next(p, it, sl, step);
         fresh = nxt.isq != cur.isq;
         const bool more = nxt.h < it.hend;
@@ -427,18 +434,24 @@ __global__ __launch_bounds__(1024) void norm_rotate_sum_kernel(const float *part
 // (b4 L2048 of the same, 84 MB, forward and backward: 85 us, past the caches 94).
 constexpr int64_t kOnceBytes = (int64_t)128 << 20;
 
+template <typename T, typename TD, int LH, bool VEC, bool INTER>
+void launch_back(const NormRotParams &p, uint32_t nwg, hipStream_t st) {
+  if (p.eps < kSmallEps) norm_rotate_bwd_kernel<T, TD, LH, VEC, INTER, true><<<nwg, kThreads, 0, st>>>(p);
+  else norm_rotate_bwd_kernel<T, TD, LH, VEC, INTER, false><<<nwg, kThreads, 0, st>>>(p);
+}
 // A small eps takes kernels of its own: the branch of rstd_of in the forward's
 // walk costs 5 % there (b4 L4096 32 + 8 heads N128 bf16 58.5 -> 61.7 us).
 template <typename T, int LH, bool VEC, bool INTER>
 void launch_pair(bool back, const NormRotParams &p, hipStream_t st) {
   const uint32_t grid = (uint32_t)((p.nitem + 3) / 4), nwg = (uint32_t)p.nwg;
   const bool once = VEC && p.ntok * (p.Hq + p.Hk) * p.N * (int64_t)sizeof(T) >= kOnceBytes;
-  if (p.eps < kSmallEps) {
-    if (back) norm_rotate_bwd_kernel<T, LH, VEC, INTER, true><<<nwg, kThreads, 0, st>>>(p);
-    else norm_rotate_fwd_kernel<T, LH, VEC, INTER, false, true><<<grid, kThreads, 0, st>>>(p);
+  if (back) {
+    if (p.dy_f32) launch_back<T, float, LH, VEC, INTER>(p, nwg, st);
+    else launch_back<T, T, LH, VEC, INTER>(p, nwg, st);
+  } else if (p.eps < kSmallEps) {
+    norm_rotate_fwd_kernel<T, LH, VEC, INTER, false, true><<<grid, kThreads, 0, st>>>(p);
   } else {
-    if (back) norm_rotate_bwd_kernel<T, LH, VEC, INTER, false><<<nwg, kThreads, 0, st>>>(p);
-    else if (once) norm_rotate_fwd_kernel<T, LH, VEC, INTER, VEC, false><<<grid, kThreads, 0, st>>>(p);
+    if (once) norm_rotate_fwd_kernel<T, LH, VEC, INTER, VEC, false><<<grid, kThreads, 0, st>>>(p);
     else norm_rotate_fwd_kernel<T, LH, VEC, INTER, false, false><<<grid, kThreads, 0, st>>>(p);
   }
 }

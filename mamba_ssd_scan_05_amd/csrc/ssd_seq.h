@@ -63,6 +63,7 @@ struct NormRotParams {
   int64_t qb, qt, qh, kb, kt, kh;         // strides, elements
   const void *dyq, *dyk;                  // gradients at the outputs (backward)
   int64_t dqb, dqt, dqh, dkb, dkt, dkh;
+  int dy_f32;                             // both are fp32 whatever q is
   const float *qw, *kw;                   // [N] or null
   const float *freqs;                     // [npair]
   const int32_t *pos32;                   // [b, L], or

@@ -504,8 +504,8 @@ int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k, const ssd_tens
   NormRotParams p{};
   Args args;
   SSD_CHECK(validate_norm_rotate(q, k, q_weight, k_weight, freqs, positions, eps, interleaved, &p, &args));
-  SSD_CHECK(check_arg(dq_out, "dq_out", q->dtype, 4, q->shape, true));
-  SSD_CHECK(check_arg(dk_out, "dk_out", q->dtype, 4, k->shape, true));
+  SSD_CHECK(check_arg(dq_out, "dq_out", grad_dtype(dq_out, q), 4, q->shape, true));
+  SSD_CHECK(check_arg(dk_out, "dk_out", dq_out->dtype, 4, k->shape, true));
   SSD_CHECK(check_arg(dq, "dq", q->dtype, 4, q->shape));
   SSD_CHECK(check_arg(dk, "dk", q->dtype, 4, k->shape));
   const int64_t sw[1] = {q->shape[3]};
@@ -522,6 +522,7 @@ int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k, const ssd_tens
   SSD_CHECK(args.addressable(workspace));
   p.dyq = dq_out->data;
   p.dyk = dk_out->data;
+  p.dy_f32 = dq_out->dtype == SSD_F32;
   p.dqb = dq_out->strides[0]; p.dqt = dq_out->strides[1]; p.dqh = dq_out->strides[2];
   p.dkb = dk_out->strides[0]; p.dkt = dk_out->strides[1]; p.dkh = dk_out->strides[2];
   p.oq = dq->data;

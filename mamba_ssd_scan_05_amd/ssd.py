@@ -517,8 +517,9 @@ def ssd_norm_rotate_fwd(q, k, q_weight=None, k_weight=None, freqs=None, position
 def ssd_norm_rotate_bwd(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_out, *,
                         eps: float = 1e-6, interleaved: bool = False, want_weights: bool = True,
                         out: dict = None, stream=None):
-    """Gradients of ssd_norm_rotate_fwd for <dq_out, q_out> + <dk_out, k_out>:
-    a dict of dq, dk (dtype of q) and, when asked for, dq_weight, dk_weight
+    """Gradients of ssd_norm_rotate_fwd for <dq_out, q_out> + <dk_out, k_out>
+    (both in the dtype of q, or both fp32 as ssd_scan_bwd returns them): a dict of
+    dq, dk (dtype of q) and, when asked for, dq_weight, dk_weight
     (fp32).  ``out`` may hold preallocated tensors under those names."""
     g = dict(out or {})
     with _on_stream(stream, q):

@@ -116,3 +116,58 @@ def test_prefill_then_decode():
         close(yk, y[:, k], "token %d" % k)
     close(hf, f["fin"], "recurrent state")
     close(Sg, S, "scan state")
+
+
+def within(got, ref, bound, what):
+    """Within the reference's bound and half a step of got's type."""
+    half = torch.finfo(got.dtype).eps / 2
+    got = got.double().cpu().numpy()
+    tol = bound + half * (np.abs(ref) + bound) + 1e-37
+    assert np.all(np.abs(got - ref) <= tol), "%s: worst %.3g of the bound" % (what, np.max(np.abs(got - ref) / tol))
+
+
+@pytest.mark.parametrize("b,L,H,P,G,N", [(2, 150, 4, 16, 2, 32), (1, 300, 2, 64, 1, 128)])
+def test_bf16_training(b, L, H, P, G, N):
+    # bf16 activations through all three and back, without a cast: the scan's
+    # fp32 gradients go into the other two as they are.  Each stage against its
+    # reference on what it was given; the scan's bound for bf16 is
+    # 2e-2 * (1 + |ref|), as in its own tests.
+    bf = torch.bfloat16
+    t = layer(b, L, H, P, G, N, seed=L + 1)
+    d = {k: v.to(DEV).to(bf) if k in ("x", "r", "i", "q", "k") else v.to(DEV) for k, v in t.items()}
+    a = {k: v.double().cpu().numpy() for k, v in d.items()}
+    pos, eps = np.arange(L)[None].repeat(b, 0), float(np.float32(1e-6))
+    gates = (d["x"], d["r"], d["i"], d["A"], d["rb"], d["ib"])
+    ref_gates = tuple(a[k] for k in ("x", "r", "i", "A", "rb", "ib")) + (None, None, a["h0"])
+    states = ssd.ssd_glr_states(d["x"])
+    h, hf = ssd.ssd_glr_fwd(*gates, init_state=d["h0"], states=states)
+    C, B = ssd.ssd_norm_rotate_fwd(d["q"], d["k"], d["qw"], d["kw"], d["freqs"])
+    hs = h.view(b, L, H, P)
+    scan = (d["dt"], d["dtb"], d["As"], B, C, d["Ds"], d["S0"])
+    out, fin = ssd.ssd_scan_fwd(hs, *scan)
+    f = glr_ref.forward(*ref_gates)
+    within(h, f["h"], f["eh"], "h")
+    for y, x, w in ((C, "q", "qw"), (B, "k", "kw")):
+        within(y, *norm_rotate_ref.forward(a[x], a[w], pos, a["freqs"], eps, False), x)
+    num = lambda v: v.double().cpu().numpy()  # noqa: E731
+    ref_scan = (num(hs), a["dt"], a["dtb"], a["As"], num(B), num(C), a["Ds"], a["S0"])
+    y, S = oracle.scan(*ref_scan)
+    close(out, y, "y", 2e-2 * (1 + np.abs(y)))
+    close(fin, S, "state", 2e-2 * (1 + np.abs(S)))
+    g = torch.Generator().manual_seed(8)
+    dy, dS = torch.randn((b, L, H, P), generator=g).to(bf), torch.randn((b, H, P, N), generator=g)
+    gs = ssd.ssd_scan_bwd(hs, *scan, dy.to(DEV), dS.to(DEV))
+    rs = oracle.scan_bwd(*ref_scan, dy.double().numpy(), dS.double().numpy())
+    for k in ("dx", "dB", "dC"):
+        close(gs[k], rs[k], k, 2e-2 * (1 + np.abs(rs[k])))
+    gn = ssd.ssd_norm_rotate_bwd(d["q"], d["k"], d["qw"], d["kw"], d["freqs"], None, gs["dC"], gs["dB"])
+    gr = ssd.ssd_glr_bwd(*gates, init_state=d["h0"], states=states, dout=gs["dx"].view(b, L, H * P))
+    for x, w, dn, wn, dy in (("q", "qw", "dq", "dq_weight", gs["dC"]), ("k", "kw", "dk", "dk_weight", gs["dB"])):
+        ref = norm_rotate_ref.backward(a[x], a[w], pos, a["freqs"], eps, False, num(dy), 200)
+        assert gn[dn].dtype == bf
+        within(gn[dn], ref["dx"], ref["edx"], dn)
+        within(gn[wn], ref["dw"], ref["edw"], wn)
+    ref = glr_ref.backward(*ref_gates, dout=num(gs["dx"]).reshape(b, L, H * P), dfin=None)
+    for k in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dinit"):
+        assert gr[k].dtype == (bf if k in ("dx", "dr", "di") else torch.float32)
+        within(gr[k], ref[k], ref["e" + k], k)

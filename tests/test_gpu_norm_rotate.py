@@ -301,3 +301,21 @@ def test_weight_gradients_of_very_many_tokens():
         check(wn, g[wn], L * d["dw"], L * d["edw"])
         check(dn, g[dn][:, -1:], d["dx"], d["edx"])
         assert bool((g[dn] == g[dn][:, :1]).all())
+
+
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "adjacent"])
+@pytest.mark.parametrize("case", CASES, ids=["b%d_L%d_Hq%d_Hk%d_N%d_p%d_%s" % c[:7] for c in CASES])
+def test_gradients_from_fp32_output_gradients(case, interleaved):
+    b, L, Hq, Hk, N, npair, layout, far, i64 = case
+    t, pos, _, _ = make(b, L, Hq, Hk, N, npair, BF, layout, far, i64, explicit=far > 0 or i64)
+    g = torch.Generator().manual_seed(7)
+    pad = 1 if layout == "offset" else 0  # rows between 16-byte boundaries
+    dyq, dyk = (torch.randn(b, L, H, N + pad, generator=g).to(DEV)[..., pad:] for H in (Hq, Hk))
+    got = ssd.ssd_norm_rotate_bwd(**t, dq_out=dyq, dk_out=dyk, eps=1e-5, interleaved=interleaved)
+    rows = b * L * (Hq + Hk)
+    for x, w, dy, dn, wn in ((t["q"], t["q_weight"], dyq, "dq", "dq_weight"), (t["k"], t["k_weight"], dyk, "dk", "dk_weight")):
+        assert got[dn].dtype == BF
+        d = ref.backward(num(x), num(w), pos, num(t["freqs"]), float(np.float32(1e-5)), interleaved, num(dy),
+                         130 + Hq + Hk + rows // 1024)
+        check(dn, got[dn], d["dx"], d["edx"])
+        check(wn, got[wn], d["dw"], d["edw"])

@@ -134,3 +134,20 @@ def test_reference_against_autograd(interleaved, npair):
     d = ref.backward(x, w, pos, freqs, 1e-3, interleaved, dy, 0)
     assert np.allclose(d["dx"], tx.grad.numpy(), rtol=1e-10, atol=1e-12)
     assert np.allclose(d["dw"], tw.grad.numpy(), rtol=1e-10, atol=1e-12)
+
+
+def test_backward_takes_fp32_output_gradients():
+    # both f32 with bf16 q and k: only the CPU memory is refused
+    f32 = lambda a, k: torch.zeros_like(a[k], dtype=torch.float32)  # noqa: E731
+    a = bwd_args()
+    a.update(dq_out=f32(a, "dq_out"), dk_out=f32(a, "dk_out"))
+    st, msg = call_bwd(a)
+    assert st == 4 and ("device" in msg or "address" in msg), (st, msg)
+    for k in ("dq_out", "dk_out"):  # one of each
+        a = bwd_args()
+        a[k] = f32(a, k)
+        st, msg = call_bwd(a)
+        assert st == 3 and "dk_out" in msg, (k, st, msg)
+    a = bwd_args()
+    a.update({k: f32(a, k) for k in ("q", "k", "dq", "dk")})  # f32 q and bf16 gradients
+    assert call_bwd(a)[0] == 3
