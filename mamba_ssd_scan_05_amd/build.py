@@ -5,12 +5,13 @@
 Each .hip source is compiled to an object by hipcc in parallel, then the
 objects are linked into a shared library with a C ABI (include/ssd.h).  The
 CPython module _pydesc (tensor descriptors for the Python binding) is built
-beside it by g++ against torch's headers.
+beside it by g++ against torch's headers, where both are there.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -48,12 +49,29 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_pydesc() -> None:
-    from torch.utils.cpp_extension import include_paths, library_paths
+def _compile_pydesc() -> bool:
+    """Builds _pydesc where g++, Python's and torch's headers are there.  Where
+    they are not, the binding packs its descriptors in Python; a module of an
+    earlier build is taken out, since it may be of another torch."""
+    cxx = os.environ.get("CXX", "g++")
+    python_h = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    try:
+        from torch.utils.cpp_extension import include_paths, library_paths
+        torch_h = any(os.path.exists(os.path.join(d, "torch", "csrc", "autograd", "python_variable.h"))
+                      for d in include_paths())
+    except ImportError:
+        torch_h = False
+    missing = [n for n, there in ((cxx, shutil.which(cxx)), ("Python.h", os.path.exists(python_h)),
+                                  ("torch's C++ headers", torch_h)) if not there]
+    if missing:
+        print("_pydesc is not built (no %s)" % ", ".join(missing), file=sys.stderr)
+        if os.path.exists(PYDESC):
+            os.remove(PYDESC)
+        return False
     tmp = PYDESC + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-Wall", "-Werror", "-I" + os.path.join(ROOT, "include")]
-    for d in include_paths() + [sysconfig.get_paths()["include"]]:
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-I" + os.path.join(ROOT, "include")]
+    for d in include_paths() + [os.path.dirname(python_h)]:
         cmd += ["-isystem", d]
     cmd += [os.path.join(CSRC, "ssd_pydesc.cpp"), "-o", tmp]
     for d in library_paths():  # torch's, loaded already when the module is imported
@@ -61,8 +79,9 @@ def _compile_pydesc() -> None:
     cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for ssd_pydesc.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr))
+        raise RuntimeError("%s failed for ssd_pydesc.cpp:\n%s\n%s" % (cxx, " ".join(cmd), r.stderr))
     os.replace(tmp, PYDESC)
+    return True
 
 
 def build(verbose: bool = False) -> str:
