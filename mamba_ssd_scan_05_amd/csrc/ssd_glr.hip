@@ -511,7 +511,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(TD) > sizeof(T) ? 4 : 1) void glr_b
     store_row<T, V, AUX>(odi, off, (lt0 + j) * p.D * ES, zero);
   }
   if (pl.chunk > last) {
-    for (int k = tid; k < 3 * kTile; k += 64 * NW) {
+    for (int k = tid; k < 3 * kTile && p.part; k += 64 * NW) {
       const int c = pl.tile * kTile + k % kTile;
       if (c < p.D) p.part[prow + (int64_t)(k / kTile) * p.D + c] = 0.f;
     }
@@ -707,6 +707,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(TD) > sizeof(T) ? 4 : 1) void glr_b
   }
   // parameter gradients: the waves' sums in a fixed order (fA, fw and bA are
   // read no more once every wave has its carries)
+  if (!p.part) return;
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < V; ++e) {

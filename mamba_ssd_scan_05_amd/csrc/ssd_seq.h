@@ -28,7 +28,7 @@ struct GlrParams {
   const float *dfin;                     // [b, D] or null
   void *dx, *dr, *di;                    // [b, L, D] dense
   float *dinit;                          // [b, D] or null
-  float *part;                           // [b, nchunk, 3, D]
+  float *part;                           // [b, nchunk, 3, D], null: no parameter gradients
   uint64_t *words;                       // chain words [b, nchunk, wstride], null if nchunk == 1
   uint32_t *ticket;                      // behind the words
   int64_t wstride;

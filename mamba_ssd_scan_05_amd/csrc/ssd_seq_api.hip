@@ -395,14 +395,16 @@ int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, c
   SSD_CHECK(args.addressable(workspace));
   GlrParams p = glr_params(x, r, i, A, r_bias, i_bias, reset, lengths, init_state, plan);
   char *ws = (char *)workspace;
-  p.part = (float *)(ws + up256(plan.chain_f > plan.chain_b ? plan.chain_f : plan.chain_b));
+  float *part = (float *)(ws + up256(plan.chain_f > plan.chain_b ? plan.chain_f : plan.chain_b));
+  const bool sums = dA || dr_bias || di_bias;
+  p.part = sums ? part : nullptr;
   hipStream_t st = (hipStream_t)stream;
   const bool vec = rows4b(x) && rows4b(r) && rows4b(i);
   hipError_t e;
   if (states) {
     p.states = (float *)states->data;
   } else {
-    p.states = (float *)((char *)p.part + up256(plan.part));
+    p.states = (float *)((char *)part + up256(plan.part));
     set_chain(&p, plan.nfwd, ws);
     e = launch_glr(x->dtype, vec, false, p, st);
     if (e != hipSuccess) return hip_fail(e, "gated recurrence states launch");
@@ -417,7 +419,8 @@ int ssd_glr_bwd(const ssd_tensor *x, const ssd_tensor *r, const ssd_tensor *i, c
   set_chain(&p, plan.nseg, ws);
   e = launch_glr(x->dtype, vec && rows_of(dout, 2 * elem_size(dout->dtype)) && rows4b(dx) && rows4b(dr) && rows4b(di), true, p, st);
   if (e != hipSuccess) return hip_fail(e, "gated recurrence backward launch");
-  e = launch_glr_sum(p.part, (int)(b * plan.nseg), (int)D, fptr_out(dA), fptr_out(dr_bias), fptr_out(di_bias), st);
+  if (!sums) return SSD_OK;
+  e = launch_glr_sum(part, (int)(b * plan.nseg), (int)D, fptr_out(dA), fptr_out(dr_bias), fptr_out(di_bias), st);
   return e == hipSuccess ? SSD_OK : hip_fail(e, "gated recurrence parameter sums launch");
 }
 

@@ -529,3 +529,24 @@ def test_inputs_that_pass_the_caches_by(dtype, ddtype):
         check(k, g[k][:1], ref[k], ref["e" + k])
     for k in ("dA", "dr_bias", "di_bias"):
         check(k, g[k], b * ref[k], b * ref["e" + k])
+
+
+def test_no_parameter_gradients():
+    # none of them wanted: no partial sums are formed, the rest is the same
+    b, L, D = 3, 300, 40
+    t, dout, dfin = make(b, L, D, BF, seed=21, lengths=[300, 70, 0])
+    states = ssd.ssd_glr_states(t["x"])
+    ssd.ssd_glr_fwd(**t, states=states)
+    want = ssd.ssd_glr_bwd(**t, dout=dout, dfinal_state=dfin, states=states)
+    ws = torch.full((ssd.ssd_glr_workspace(b, L, D, True),), 0xA5, dtype=torch.uint8, device=DEV)
+    # behind the chain words [b, segments, 128] of 8 bytes and 16 more
+    chain = b * 5 * 128 * 8 + 16
+    for st in (states, None):
+        out = [torch.empty_like(t["x"]) for _ in range(3)] + [None] * 3 + [torch.empty(b, D, device=DEV)]
+        keep, d = ssd._descs(t["x"], t["r"], t["i"], t["A"], t["r_bias"], t["i_bias"], None, t["lengths"], t["init_state"],
+                             st, dout, dfin, *out)
+        assert ssd.lib().ssd_glr_bwd(*d, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+        for k, v in zip(("dx", "dr", "di", None, None, None, "dinit"), out):
+            assert v is None or torch.equal(v, want[k]), k
+        part = -(-chain // 256) * 256
+        assert bool((ws[part:part + b * 5 * 3 * D * 4] == 0xA5).all())
