@@ -530,7 +530,8 @@ int64_t ssd_norm_rotate_workspace(int64_t N);
  * dq_out, dk_out: shape of q and k, dtype of q or both f32 (as ssd_scan_bwd writes
  * its gradients), views allowed.  Written in full:
  * dq, dk (dtype of q, dense) and dq_weight, dk_weight [N] f32, each of these
- * two may be NULL.  Nothing of the forward is needed but its inputs.
+ * two may be NULL (both: no workspace is needed).  Nothing of the forward is
+ * needed but its inputs.
  */
 int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k,
                         const ssd_tensor *q_weight, const ssd_tensor *k_weight,

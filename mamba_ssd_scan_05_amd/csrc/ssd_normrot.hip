@@ -399,6 +399,7 @@ __global__ __launch_bounds__(kThreads, 4) void norm_rotate_bwd_kernel(NormRotPar
     }
     folded = true;
   } while (item < (uint32_t)p.nitem);
+  if (!p.part) return;
   __syncthreads();
   // lane groups of the workgroup in a fixed order
   for (int c = threadIdx.x; c < 2 * p.N; c += kThreads) {
@@ -499,7 +500,7 @@ hipError_t launch_norm_rotate(int dtype, bool vec, bool back, const NormRotParam
   hipError_t e;
   if (dtype == 1) e = vec ? launch_lh<__bf16, true>(back, p, st) : launch_lh<__bf16, false>(back, p, st);
   else e = vec ? launch_lh<float, true>(back, p, st) : launch_lh<float, false>(back, p, st);
-  if (!back || e != hipSuccess || (!p.dqw && !p.dkw)) return e;
+  if (!back || e != hipSuccess || !p.part) return e;
   norm_rotate_sum_kernel<<<(uint32_t)(2 * p.N / 16), 1024, 0, st>>>(p.part, p.nwg, p.N, p.dqw, p.dkw);
   return hipGetLastError();
 }

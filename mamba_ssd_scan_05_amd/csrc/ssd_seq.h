@@ -69,7 +69,7 @@ struct NormRotParams {
   const int32_t *pos32;                   // [b, L], or
   const int64_t *pos64;                   // [b, L], or both null: 0 .. L-1
   void *oq, *ok;                          // outputs or gradients, dense
-  float *part;                            // [nwg, 2, N] (backward)
+  float *part;                            // [nwg, 2, N] (backward), null: no weight gradients
   float *dqw, *dkw;                       // [N] or null
   float eps;
   int L, Hq, Hk, N, npair, interleaved;

@@ -521,8 +521,9 @@ int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k, const ssd_tens
   args.add(dq_weight, "dq_weight", true);
   args.add(dk_weight, "dk_weight", true);
   SSD_CHECK(args.overlaps(nullptr, nullptr));
-  SSD_CHECK(args.workspace(workspace, workspace_bytes, norm_rotate_bytes(q->shape[3])));
-  SSD_CHECK(args.addressable(workspace));
+  const int64_t need = dq_weight || dk_weight ? norm_rotate_bytes(q->shape[3]) : 0;
+  SSD_CHECK(args.workspace(workspace, workspace_bytes, need));
+  SSD_CHECK(args.addressable(need ? workspace : nullptr));
   p.dyq = dq_out->data;
   p.dyk = dk_out->data;
   p.dy_f32 = dq_out->dtype == SSD_F32;
@@ -532,7 +533,7 @@ int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k, const ssd_tens
   p.ok = dk->data;
   p.dqw = fptr_out(dq_weight);
   p.dkw = fptr_out(dk_weight);
-  p.part = (float *)workspace;
+  p.part = need ? (float *)workspace : nullptr;
   const bool vec = rows4(q) && rows4(k) && rows4(q_weight) && rows4(k_weight) && rows4(dq_out) && rows4(dk_out) &&
                    rows4(dq) && rows4(dk);
   const hipError_t e = launch_norm_rotate(q->dtype, vec, true, p, (hipStream_t)stream);

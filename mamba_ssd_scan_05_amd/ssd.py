@@ -532,7 +532,8 @@ def ssd_norm_rotate_bwd(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_o
             elif g.get(n) is None:
                 g[n] = (torch.empty_like(w) if w is not None else
                         torch.empty((q.shape[-1],), dtype=torch.float32, device=q.device))
-        ws = _workspace(ssd_norm_rotate_workspace(q.shape[-1]), q)
+        ws = (None if g["dq_weight"] is None and g["dk_weight"] is None else
+              _workspace(ssd_norm_rotate_workspace(q.shape[-1]), q))
     with _on_device(q):
         st = _stream(stream, q)
         keep, d = _descs(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_out, g["dq"], g["dk"],

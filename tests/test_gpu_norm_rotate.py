@@ -319,3 +319,17 @@ def test_gradients_from_fp32_output_gradients(case, interleaved):
                          130 + Hq + Hk + rows // 1024)
         check(dn, got[dn], d["dx"], d["edx"])
         check(wn, got[wn], d["dw"], d["edw"])
+
+
+def test_one_weight_gradient_or_none():
+    t, pos, dyq, dyk = make(2, 300, 4, 2, 64, 32, BF)
+    want = ssd.ssd_norm_rotate_bwd(**t, dq_out=dyq, dk_out=dyk)
+    ws = torch.empty(ssd.ssd_norm_rotate_workspace(64), dtype=torch.uint8, device=DEV)
+    for which in ((), ("dq_weight",), ("dk_weight",)):
+        out = {k: torch.empty_like(want[k]) if k in which or k in ("dq", "dk") else None for k in ("dq", "dk", "dq_weight", "dk_weight")}
+        keep, d = ssd._descs(*t.values(), dyq, dyk, *out.values())
+        st = ssd.lib().ssd_norm_rotate_bwd(*d, 1e-6, 0, ws.data_ptr() if which else None, ws.numel() if which else 0,
+                                           torch.cuda.current_stream().cuda_stream)
+        assert st == 0, ssd.ssd_last_error()
+        for k, v in out.items():
+            assert v is None or torch.equal(v, want[k]), (which, k)

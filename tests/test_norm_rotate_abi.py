@@ -151,3 +151,16 @@ def test_backward_takes_fp32_output_gradients():
     a = bwd_args()
     a.update({k: f32(a, k) for k in ("q", "k", "dq", "dk")})  # f32 q and bf16 gradients
     assert call_bwd(a)[0] == 3
+
+
+def test_no_workspace_without_weight_gradients():
+    a = bwd_args()
+    a.update(dqw=None, dkw=None)
+    keep, d = ssd._descs(*a.values())
+    st = ssd.lib().ssd_norm_rotate_bwd(*d, 1e-6, 0, None, 0, None)
+    assert st == 4 and ("device" in ssd.ssd_last_error() or "address" in ssd.ssd_last_error()), ssd.ssd_last_error()
+    for k in ("dqw", "dkw"):  # one of them is wanted
+        a = bwd_args()
+        a[k] = None
+        keep, d = ssd._descs(*a.values())
+        assert ssd.lib().ssd_norm_rotate_bwd(*d, 1e-6, 0, None, 0, None) == 1
