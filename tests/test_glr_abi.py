@@ -255,3 +255,10 @@ def test_backward_takes_fp32_output_gradients():
     a = bwd_args()
     a["dout"] = torch.zeros(2, 300, 24, dtype=torch.float16)
     assert call_bwd(a)[0] == 3
+
+
+def test_the_initial_state_in_place_passes_the_overlap_check():
+    a = fwd_args()
+    a["final_state"] = a["init_state"]
+    st, msg = call_fwd(a)
+    assert st == 4 and ("address" in msg or "device" in msg), (st, msg)  # only the CPU memory is refused

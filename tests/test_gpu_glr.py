@@ -550,3 +550,17 @@ def test_no_parameter_gradients():
             assert v is None or torch.equal(v, want[k]), k
         part = -(-chain // 256) * 256
         assert bool((ws[part:part + b * 5 * 3 * D * 4] == 0xA5).all())
+
+
+@pytest.mark.parametrize("largest", [-0.4, -3.0], ids=["small_decays", "any_decay"])
+def test_gradients_where_the_factor_is_zero(largest):
+    # A of 0 and above: the factor sqrt(1 - a^2) is 0 and so is the gradient
+    # through it, the one through a h_{t-1} stays
+    b, L, D = 2, 200, 10
+    t, dout, dfin = make(b, L, D, F32, seed=22, lengths=[200, 131], reset=0.01)
+    t["A"][:] = torch.tensor([0.0, -0.0, 1e-3, 0.1, 1e-30, -1e-30, -1e-7, -1e-3, -0.2, largest], device=DEV)
+    g = ssd.ssd_glr_bwd(**t, dout=dout, dfinal_state=dfin)
+    ref = glr_ref.backward(**host(t), dout=dout.cpu().double().numpy(), dfin=dfin.cpu().double().numpy())
+    assert np.all(ref["dx"][..., :5][~(host(t)["reset"] != 0)] == 0) and np.all(ref["dA"][:4] != 0)
+    for k in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dinit"):
+        check(k, g[k], ref[k], ref["e" + k])
