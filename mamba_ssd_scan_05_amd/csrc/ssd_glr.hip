@@ -290,11 +290,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base, in
 // ---------------------------------------------------------------------------
 // Forward.  A wave takes TT successive tokens of the tile's channels, a lane V
 // of them.  31 vector instructions an element, 5 of them transcendental (two
-// issue slots each).  b4 L4096 D5120 bf16: 147 us for 671 MB, 4.6 TB/s
-// where a large copy reaches 5.1; HBM moves 1.04 times the inputs and outputs
-// (the rest are chain words), the vector ALU is busy 53 % of the time.  The
-// same kernel without gates, look back and ticket takes 138: what is left
-// is the wait at the two barriers and the tail of the chain.
+// issue slots each).  b4 L4096 D5120 bf16, 671 MB: a call with its fill takes 147
+// us (4.6 TB/s; in a loop over three sets of inputs 155; the kernel alone, under
+// the profiler, 154, at best 144), where a large copy reaches 5.1 TB/s.  HBM moves
+// 1.04 times the inputs and outputs (the rest are chain words), the vector ALU is
+// busy 53 % of the time.  The same kernel without gates, look back and ticket
+// takes 138 of the 147: what is left is the wait at the two barriers and the tail
+// of the chain.
 // ---------------------------------------------------------------------------
 template <typename T, int V, int NW, bool CUT, int AUX>
 __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p) {
@@ -815,10 +817,10 @@ template <typename T, typename TD, int V, int NW, int AUX> void launch_waves(boo
     else glr_fwd_kernel<T, V, NW, false, AUX><<<grid, 64 * NW, 0, st>>>(p);
   }
 }
-// x, r and i that take half of the 256 MB last-level cache pass it by (b4 L4096
-// D5120 bf16 forward 158 -> 154 us, b4 L2048 forward and backward 244 -> 234);
-// smaller ones find themselves there again (b5 L1009 D1100 f32 forward 24.5 us,
-// passed by 27.8).
+// x, r and i that take half of the 256 MB last-level cache pass it by; smaller
+// ones find themselves there again.  In a loop over three sets of inputs, kept
+// in the caches and passed by: b4 L4096 D5120 bf16 forward 159 and 155 us, b4 L2048
+// forward and backward 247 and 239, b5 L1009 D1100 f32 forward 25.5 and 28.6.
 constexpr int64_t kOnceBytes = (int64_t)128 << 20;
 
 // As many waves as the rows need (b256 L32 D5120 bf16 forward: eight 119 us, four

@@ -247,9 +247,9 @@ template <typename T, bool BACK, typename TD = T> struct Walk {
 // Forward.  The weights are multiplied into the turn's coefficients once per
 // token and kind of head: y_i = n_i (w_i c) - n_j (w_j s), y_j = n_i (w_i s) +
 // n_j (w_j c).  The next head is loaded while one is worked on.
-// b4 L4096 32 + 8 heads N128 bf16: 56 us (6.0 TB/s, outputs left in the last-
-// level cache); addresses, weights and pair order chosen anew for every head
-// kept the vector ALU busy for 73.
+// b4 L4096 32 + 8 heads N128 bf16: a call 59 us, the kernel alone 56 (6.0 TB/s,
+// outputs left in the last-level cache); addresses, weights and pair order chosen
+// anew for every head kept the vector ALU busy for 73.
 template <typename T, int LH, bool VEC, bool INTER, bool ONCE, bool SMALL>
 __global__ __launch_bounds__(kThreads) void norm_rotate_fwd_kernel(NormRotParams p) {
   const int lane = threadIdx.x & 63;
@@ -431,8 +431,8 @@ __global__ __launch_bounds__(1024) void norm_rotate_sum_kernel(const float *part
 
 // A forward whose input takes half of the 256 MB last-level cache reads it past
 // the caches, which leaves them to the outputs (b4 L4096 32 + 8 heads N128 bf16,
-// 168 MB: 67 -> 58 us); a smaller one leaves its input there for the backward
-// (b4 L2048 of the same, 84 MB, forward and backward: 85 us, past the caches 94).
+// 168 MB: 67.5 -> 59 us); a smaller one leaves its input there for the backward
+// (b4 L2048 of the same, 84 MB, forward and backward: 85 us, past the caches 92).
 constexpr int64_t kOnceBytes = (int64_t)128 << 20;
 
 template <typename T, typename TD, int LH, bool VEC, bool INTER>
@@ -474,7 +474,7 @@ template <typename T, bool VEC> hipError_t launch_lh(bool back, const NormRotPar
 // Splits the tokens' heads into items.  Fewer than kEnough waves leave compute
 // units idle (a decode step): the heads of a token are then spread over
 // several waves, each forming the angles again (b32 L1 32 + 8 heads N128 bf16
-// forward in a graph: 3.0 us, one wave a token 6.6; b1 L1000 7.2 against 8.0;
+// forward in a graph: 3.1 us, one wave a token 6.6; b1 L1000 7.2 against 8.0;
 // from L2000 on the two are the same).
 void norm_rotate_plan(NormRotParams *p) {
   constexpr int64_t kEnough = 4096;
