@@ -384,8 +384,9 @@ int ssd_scan_bwd_gated(const ssd_tensor *x, const ssd_tensor *dt,
  * for every batch row and channel; out_t = h_t.  The factor sqrt(1 - a^2)
  * keeps the variance of h at that of its input.  A is meant to be finite and at
  * most 0: where a > 1 the factor is taken as 0, and the decays of 128
- * successive tokens multiplied must stay within fp32's range.  An r of -infinity
- * shuts its gate (a_t = 1, the factor 0) whatever r_bias is.
+ * successive tokens multiplied must stay within fp32's range.  An r of -infinity,
+ * or of its type's lowest finite value, shuts its gate (a_t = 1, the factor 0)
+ * whatever r_bias is.
  *
  * Packed and padded batches.  reset [b, L] marks (nonzero) the first token of
  * each document: it starts from a zero state (a_t = 0, so the factor is 1).

@@ -235,11 +235,11 @@ template <bool SMALL> __device__ __forceinline__ Gate gate_of(const Chan &c, flo
   }
   return g;
 }
-// An r_bias of +infinity opens the gate for every finite r all the same as
-// FLT_MAX, and leaves an r of -infinity shut, where inf - inf would be NaN (a NaN
-// bias stays one): a token that does not exist has such an r.  Choosing a = 1,
-// beta = 0 for those tokens instead costs 2 to 4 % of the bf16 backward (b4 L2048
-// D5120 158 to 161 us against 154).
+// An r_bias of +infinity counts as one of 2.4e38: the gate is open for every r
+// above -2^127, and an r of -infinity leaves it shut, where inf - inf would be NaN
+// (a NaN bias stays one): a token that does not exist has such an r.  Choosing a =
+// 1, beta = 0 for those tokens instead costs 2 to 4 % of the bf16 backward (b4
+// L2048 D5120 158 to 161 us against 154).
 __device__ __forceinline__ Chan chan_of(float A, float rbias, float ibias) {
   Chan k;
   k.A2 = A * kLog2e;

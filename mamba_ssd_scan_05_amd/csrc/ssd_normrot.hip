@@ -147,10 +147,11 @@ template <bool INTER> __device__ __forceinline__ Slot lane_slot(const NormRotPar
 
 // The fraction of a turn, in [-1/2, 1/2], of pos * freq / 2 pi, with freq / 2 pi
 // in twice 64 bits (c and the rest of it): whole turns drop out of the product
-// without a rounding (fma).  c alone would be off by 2^-53 of the turns: a third
-// of 2^-24 as an angle at 2^24 turns, whole turns at 2^53 positions; the rest
-// costs nothing at large sizes, up to 3 % of small fp32 calls (b3 L1001 7 + 1
-// heads N80 7.7 -> 7.9 us), and counting it from 2^24 turns on only the same.
+// without a rounding (fma).  c alone is off by about 2^-53 of itself, so by that
+// share of the turns: nothing to fp32 at 2^24 turns, a sixth of a turn at position
+// 2^53 with a freq of 1.  The rest costs nothing at large sizes, up to 3 % of small
+// fp32 calls (b3 L1001 7 + 1 heads N80 7.7 -> 7.9 us), and counting it from 2^24
+// turns on only the same.
 __device__ __forceinline__ float turn_fraction(double pos, double freq) {
   constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnLow = -0x1.6b01ec5417056p-57; // 1 / 2 pi and the rest of it
   const double c = freq * kTurn, rest = fma(freq, kTurn, -c) + freq * kTurnLow;

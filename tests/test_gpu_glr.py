@@ -457,12 +457,16 @@ def test_tokens_that_do_not_exist_pass_the_state_on(b, L, D, lengths, dtype):
         ref = glr_ref.backward(**h, dout=dout.float().cpu().double().numpy(), dfin=dfin.cpu().double().numpy())
         for k in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dinit"):
             check(k, g[k], ref[k], ref["e" + k])
-        # an r of -infinity outweighs a bias of +infinity
+        # an r of -infinity or of the lowest value outweighs a bias of +infinity
         one = dict(t, lengths=torch.ones(b, dtype=torch.int32, device=DEV))
-        one["r"] = torch.full_like(t["r"], float("-inf"))
         one["r_bias"] = torch.full_like(t["r_bias"], float("inf"))
-        _, fin = ssd.ssd_glr_fwd(**dict(one, reset=None))
-        assert torch.equal(fin, t["init_state"])
+        for low in (float("-inf"), torch.finfo(dtype).min):
+            one["r"] = torch.full_like(t["r"], low)
+            _, fin = ssd.ssd_glr_fwd(**dict(one, reset=None))
+            assert torch.equal(fin, t["init_state"])
+            st = t["init_state"].clone()
+            ssd.ssd_glr_step(st, t["x"][:, 0], one["r"][:, 0], t["i"][:, 0], t["A"], one["r_bias"])
+            assert torch.equal(st, t["init_state"])
         # gates always shut: the state stays as it is
         t["r_bias"][:] = float("-inf")
         out = torch.zeros(b, L, D, dtype=dtype, device=DEV)
