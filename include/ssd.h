@@ -65,8 +65,8 @@ extern "C" {
 
 #define SSD_VERSION 100 /* 1.0.0 */
 
-/* Element types.  The integer types are taken by reset, lengths and positions
- * only. */
+/* Element types.  The integer types are taken by reset, lengths, positions,
+ * page_table, start and tokens only. */
 enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_U8 = 2, SSD_I32 = 3, SSD_I64 = 4 };
 
 /* Status codes. */
@@ -541,6 +541,111 @@ int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k,
                         ssd_tensor *dq, ssd_tensor *dk, ssd_tensor *dq_weight,
                         ssd_tensor *dk_weight, float eps, int interleaved,
                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Paged key-value cache and attention over it
+ * -------------------------------------------
+ * Models that mix states by scans and recurrences hold attention layers among
+ * them.  Their cache lies in pages: k_cache and v_cache [pages, page_size, Hk, N]
+ * hold the keys and values of all rows, page_table [b, width] i32 says which page
+ * holds which part of a row: the key at position j of row i is
+ * cache[page_table[i][j / page_size]][j mod page_size].  Any page_size >= 1;
+ * multiples of 16 are faster.
+ *
+ *   start  [b]  i32: the position of the row's first new token, which is the number of
+ *               tokens its cache held before                   required
+ *   tokens [b]  i32: how many of the L tokens of the row there are (values
+ *               outside [0, L] count as the nearer end); those behind are
+ *               not read, their outputs are left as they were  NULL => L
+ *
+ * New token t of row i stands at position p = start[i] + t.  A call of the
+ * append followed by one of the attention with the same start and tokens is a
+ * layer's step; start then grows by tokens.
+ *
+ * What only the device holds is not checked by the host, and bounded there: an
+ * entry of page_table outside [0, pages) (a page not dealt out, or taken back)
+ * holds no keys, and nothing is stored to it; positions below 0 or from
+ * width * page_size on have no place.  Such entries are otherwise allowed.  Rows
+ * may share pages (a common prefix), but tokens that one call stores to the
+ * same place leave any one of them, or a mixture, there.
+ *
+ * Caches may be views: the last dimension contiguous, data and the other strides
+ * (>= 0, that of a page's tokens at most 2^24) multiples of 16 bytes; for the append
+ * no element may be two (strides that overlap), and k_cache and v_cache may lie
+ * in each other's gaps, such as halves of one tensor [pages, 2, page_size, Hk, N].  page_table
+ * may have a batch stride.  Offsets are 64 bits wide.
+ * Supported: f32 or bf16, N a multiple of 8 up to 256, b at most 2^16, L at most 2^24,
+ * b * L at most 2^25, width * page_size at most 2^30 and b times that at most
+ * 2^36.  The calls allocate nothing and may be captured into a HIP graph.
+ */
+
+/*
+ * ssd_kv_append -- keys and values of new tokens into the cache, keys and
+ * queries turned by their positions on the way.
+ *
+ *   q         [b, L, Hq, N]  f32 or bf16                       NULL => keys only
+ *   k, v      [b, L, Hk, N]  dtype of the caches               required
+ *   freqs     [npair]        f32                               NULL => not turned
+ *   q_out     [b, L, Hq, N]  dense, written                    with q
+ *   k_cache, v_cache         written at the new tokens' places
+ *
+ *     k_cache[p] = R(p) k,   v_cache[p] = v,   q_out = R(p) q
+ *
+ * R, freqs, npair and interleaved as for ssd_norm_rotate_fwd, whose angles it
+ * has (fp32, one rounding); values are moved as they are, and what is not
+ * turned as well.  q, k and v may be views (the last dimension contiguous, other
+ * strides >= 0).  q_out is written for tokens without a place in the cache too.
+ * No output may overlap any other argument.
+ */
+int ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *v,
+                  const ssd_tensor *freqs, const ssd_tensor *page_table,
+                  const ssd_tensor *start, const ssd_tensor *tokens,
+                  ssd_tensor *q_out, ssd_tensor *k_cache, ssd_tensor *v_cache,
+                  int interleaved, void *stream);
+
+/* Workspace bytes of ssd_attn_fwd (and, with L = 1, of ssd_attn_step), see
+ * Workspace above; 0 where none is needed, -1 for sizes they refuse.  Host only.
+ * It does not depend on the cache or on the rows' lengths. */
+int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk,
+                           int64_t N);
+
+/*
+ * ssd_attn_fwd -- attention of new tokens over the cache, which holds them
+ * already.  Head h reads the key head floor(h * Hk / Hq); Hq is a multiple of Hk.
+ * The query at position p sees the keys at 0 .. p, with window > 0 the last
+ * `window` of them (its own included):
+ *
+ *     s_j = scale * q . k_j,   lse = log sum_j e^{s_j},   out = sum_j e^{s_j - lse} v_j
+ *
+ *   q    [b, L, Hq, N]  f32 or bf16; views allowed as for ssd_kv_append
+ *   out  [b, L, Hq, N]  dtype of q, dense, 16-byte aligned, written
+ *   lse  [b, L, Hq]     f32, written                           NULL => skip
+ *   scale               finite, not 0 (1 / sqrt(N) is usual); may be negative
+ *   window              0 => all keys
+ *
+ * A query that sees no key, or only scores of -infinity, has out 0 and lse
+ * -infinity.  Keys that a query does not see do not reach it, whatever they hold
+ * (NaN and infinities among it).  One or several new tokens a row, prompts and pieces
+ * of prompts: any L.  Rows of any lengths share the device evenly.
+ * Arithmetic: scores, maxima, sums and outputs in fp32; with bf16 inputs
+ * the weights e^{s - m} are rounded to bf16 for the product with the values (2^-8
+ * of each); out is rounded once.  Results do not vary from run to run; a row's do
+ * depend, to rounding, on the other rows' lengths (which say where it is cut).
+ * out and lse may not overlap any other argument.  b * L * Hq at most 2^27.
+ */
+int ssd_attn_fwd(const ssd_tensor *q, const ssd_tensor *k_cache,
+                 const ssd_tensor *v_cache, const ssd_tensor *page_table,
+                 const ssd_tensor *start, const ssd_tensor *tokens,
+                 ssd_tensor *out, ssd_tensor *lse, float scale, int64_t window,
+                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ssd_attn_step -- one new token for every row (serving): q and out [b, Hq, N],
+ * lse [b, Hq] or NULL, otherwise as ssd_attn_fwd with L = 1. */
+int ssd_attn_step(const ssd_tensor *q, const ssd_tensor *k_cache,
+                  const ssd_tensor *v_cache, const ssd_tensor *page_table,
+                  const ssd_tensor *start, ssd_tensor *out, ssd_tensor *lse,
+                  float scale, int64_t window, void *workspace,
+                  int64_t workspace_bytes, void *stream);
 
 /*
  * ssd_scan_plan -- the plan SSD_ALGO_AUTO uses for a shape on a device with

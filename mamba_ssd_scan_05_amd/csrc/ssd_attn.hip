@@ -1,0 +1,570 @@
+// ssd_attn.hip -- attention of new tokens over a paged key-value cache.  For
+// query vector q of a token at position p, over the keys j in (p - window, p]
+// that the cache holds:
+//
+//   s_j = scale q . k_j,   out = sum_j e^{s_j - m} v_j / l,   l = sum_j e^{s_j - m}
+//
+// in one pass with the running maximum m.  All exponents are base 2 (the scale
+// carries log2 e).
+//
+// Decomposition.  The G query heads that share a key head are rows of one
+// product, so K and V are read once for all of them: 16 rows (token, head) a
+// workgroup, as columns of the products S^T = K Q^T and O^T = V^T P^T.  In that
+// orientation a lane holds scores of one query only (its column), its four
+// accumulator rows are keys, and they are the B operand of the second product
+// as they stand (keys {4g..4g+3, 16+4g..16+4g+3} of lane group g): P does not
+// leave the registers.  The four waves of a workgroup take every fourth tile of
+// keys, each with its own m, l and O, and are joined in LDS at the end.
+// K rows go to registers as A operands; V tiles pass through LDS, a wave's own
+// part of it, written as rows and read transposed (ds_read_b64_tr_b16).
+//
+// Long caches are cut into pieces (see piece_of); attn_join_kernel joins them.
+#include "ssd_cache.h"
+#include "ssd_device.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 256, kWaves = 4;
+
+// Keys of a tile: the K of the second product's matrix instruction (bf16 32,
+// fp32 four times 4).
+template <typename T> constexpr int kKT = sizeof(T) == 2 ? 2 : 1; // groups of 16 keys
+
+// Maximum over the four lane groups of a column.
+__device__ __forceinline__ float col_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float col_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+__device__ __forceinline__ int wave_incl_scan_i(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return v;
+}
+
+// A row of the batch: how many new tokens it has, where the first one stands and
+// the keys that any of them sees, [lo, hi).
+struct Row {
+  int n, lo, hi;
+  int64_t start;
+  // kAttnUnit-key units from lo, rounded down to a unit, to hi; a row with tokens
+  // but no keys has one, in which nothing is seen
+  __device__ __forceinline__ int units() const {
+    if (n == 0) return 0;
+    const int u = (hi + kAttnUnit - 1) / kAttnUnit - lo / kAttnUnit;
+    return max(u, 1);
+  }
+};
+__device__ __forceinline__ Row row_of(const AttnParams &p, int i) {
+  Row r;
+  r.start = p.c.start[i];
+  r.n = p.c.tokens ? min(max(p.c.tokens[i], 0), p.L) : p.L;
+  const int64_t cap = p.c.capacity;
+  const int64_t hi = min(max(r.start + r.n, (int64_t)0), cap);
+  const int64_t lo = p.window ? min(max(r.start + 1 - p.window, (int64_t)0), hi) : 0;
+  r.lo = (int)lo, r.hi = (int)hi;
+  return r;
+}
+
+// A piece: keys [k0, k1) of row i, its `index`th of `count`.
+struct Piece {
+  int i, index, count, first, size; // first: the row's first piece; size: units of a piece
+};
+// The plan, the same in every workgroup: all rows' lengths together are cut into
+// about p.workers pieces of equal size, so that a batch of one long row and many
+// short ones keeps the device as busy as an even one.  Piece `slot` of that list.
+// The sum of the units stays below 2^31 (checked on the host).
+__device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh, Piece *pc) {
+  if (p.workers == 1) {
+    *pc = Piece{slot, 0, 1, slot, INT32_MAX};
+    return slot < p.b;
+  }
+  const int tid = threadIdx.x, lane = tid & 63;
+  constexpr int kMinUnits = 4;
+  if (p.b <= 64) { // every wave by itself
+    const int u = lane < p.b ? row_of(p, lane).units() : 0;
+    const int total = __builtin_amdgcn_readlane(wave_incl_scan_i(u), 63);
+    const int size = max((total + p.workers - 1) / p.workers, kMinUnits);
+    const int cnt = (u + size - 1) / size, end = wave_incl_scan_i(cnt);
+    const uint64_t m = __builtin_amdgcn_ballot_w64(end > slot);
+    if (m == 0) return false;
+    const int i = (int)__builtin_ctzll(m);
+    const int c = __builtin_amdgcn_readlane(cnt, i), f = __builtin_amdgcn_readlane(end, i) - c;
+    *pc = Piece{i, slot - f, c, f, size};
+    return true;
+  }
+  // each thread a run of rows
+  const int per = (p.b + kThreads - 1) / kThreads, i0 = min(tid * per, p.b), i1 = min(i0 + per, p.b);
+  int sum = 0;
+  for (int i = i0; i < i1; ++i) sum += row_of(p, i).units();
+  sum = wave_incl_scan_i(sum);
+  if (lane == 63) sh[tid >> 6] = sum;
+  __syncthreads();
+  const int total = sh[0] + sh[1] + sh[2] + sh[3];
+  __syncthreads();
+  const int size = max((total + p.workers - 1) / p.workers, kMinUnits);
+  int cnt = 0;
+  for (int i = i0; i < i1; ++i) cnt += (row_of(p, i).units() + size - 1) / size;
+  const int incl = wave_incl_scan_i(cnt);
+  if (lane == 63) sh[tid >> 6] = incl;
+  if (tid == 0) sh[4] = -1;
+  __syncthreads();
+  int before = incl - cnt;
+  for (int w = 0; w < (tid >> 6); ++w) before += sh[w];
+  if (slot >= before && slot < before + cnt)
+    for (int i = i0; i < i1; ++i) {
+      const int c = (row_of(p, i).units() + size - 1) / size;
+      if (slot < before + c) {
+        sh[4] = i, sh[5] = before, sh[6] = c;
+        break;
+      }
+      before += c;
+    }
+  __syncthreads();
+  const int i = sh[4], f = sh[5], c = sh[6];
+  __syncthreads();
+  *pc = Piece{i, slot - f, c, f, size};
+  return i >= 0;
+}
+
+// A V tile of a wave in LDS: 16-byte pieces of its rows as they come, but the
+// 16-column units of a row exchanged by its number, so that the rows a transposed
+// read touches at once lie on different banks.
+template <typename T, int NP> struct Swizzle {
+  static constexpr int UB = 16 * sizeof(T), NU = NP / 16; // bytes of a unit, units of a row
+  static constexpr int kAll = 256 / UB;                   // units of all banks: 8 (bf16), 4 (fp32)
+  static constexpr int pow2(int n) { return n % 2 ? 1 : 2 * pow2(n / 2); }
+  static constexpr int U2 = pow2(NU) < kAll ? pow2(NU) : kAll;
+  __device__ static __forceinline__ int at(int row, int unit) { // first element of the unit
+    const int x = sizeof(T) == 2 ? row / (kAll / U2) : row / 4;
+    return row * NP + (unit ^ (x & (U2 - 1))) * 16;
+  }
+};
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ bool odd_values(u32x4 v, __bf16) { // an infinity or a NaN among them
+  bool b = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b |= (v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u;
+  return b;
+}
+__device__ __forceinline__ bool odd_values(u32x4 v, float) {
+  bool b = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b |= (v[e] & 0x7F800000u) == 0x7F800000u;
+  return b;
+}
+
+__device__ __forceinline__ void load_frag(FragBF &f, const __bf16 *p) { f.v = *reinterpret_cast<const bf16x8 *>(p); }
+__device__ __forceinline__ void load_frag(FragF32 &f, const float *p) {
+  const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f.v[e] = a[e], f.v[4 + e] = b[e];
+}
+
+template <typename T> __device__ __forceinline__ typename FragOf<T>::type zero_frag() {
+  const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  return pack8<T>(z);
+}
+
+// UNI: the page size is a multiple of 16, so that 16 keys from a multiple of 16 on
+// lie in one page and their page is looked up once, by the scalar unit; otherwise
+// every lane looks up the rows it loads.
+template <typename T, int NP, bool UNI>
+__global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
+  constexpr int KT = kKT<T>, TK = 16 * KT, ES = sizeof(T);
+  constexpr int KK = NP / 32, ND = NP / 16;    // steps of 32 dims, tiles of 16 dims
+  constexpr int PC = NP * ES / 16, PI = PC / 4; // 16-byte pieces of a row, loads of 16 rows
+  constexpr int LO = NP + 4;                   // row stride of the join's tile
+  using Frag = typename FragOf<T>::type;
+  using SW = Swizzle<T, NP>;
+  constexpr int kTile = TK * NP * ES, kJoin = 16 * LO * 4;
+  __shared__ __align__(16) char lds[kWaves * (kTile > kJoin ? kTile : kJoin)];
+  __shared__ float2 ml[kWaves][16];
+  __shared__ int sh[8];
+
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t id = blockIdx.x;
+  const int tile = (int)(id % (uint32_t)p.tiles);
+  id /= (uint32_t)p.tiles;
+  const int hk = (int)(id % (uint32_t)p.Hk), slot = (int)(id / (uint32_t)p.Hk);
+  Piece pc;
+  if (!piece_of(p, slot, sh, &pc)) return;
+  pc.i = __builtin_amdgcn_readfirstlane(pc.i);
+  pc.index = __builtin_amdgcn_readfirstlane(pc.index);
+  pc.size = __builtin_amdgcn_readfirstlane(pc.size);
+  const Row row = row_of(p, pc.i);
+  if (p.workers > 1 && pc.index == 0 && hk == 0 && tile == 0 && threadIdx.x == 0)
+    p.pieces[pc.i] = make_int2(pc.first, pc.count);
+  const int nrows = row.n * p.G, r0 = tile * kAttnRows;
+  if (r0 >= nrows) return;
+
+  // the tile's tokens and the keys that any and all of its queries see
+  const int t_first = (int)div_by((uint32_t)r0, p.group);
+  const int t_last = (int)div_by((uint32_t)(min(r0 + kAttnRows, nrows) - 1), p.group);
+  const int64_t cap = p.c.capacity;
+  auto last_key = [&](int t) { return (int)min(max(row.start + t + 1, (int64_t)0), cap); };
+  auto first_key = [&](int t) { return p.window ? (int)min(max(row.start + t + 1 - p.window, (int64_t)0), cap) : 0; };
+  int k0 = first_key(t_first), k1 = last_key(t_last);
+  const int all0 = first_key(t_last), all1 = last_key(t_first); // seen by every query: [all0, all1)
+  {
+    const int64_t base = (int64_t)(row.lo / kAttnUnit) * kAttnUnit, size = (int64_t)pc.size * kAttnUnit;
+    const int64_t a = base + pc.index * size;
+    k0 = (int)max((int64_t)k0, a);
+    k1 = (int)min((int64_t)k1, a + size);
+  }
+  // this lane's query
+  const int r = r0 + li;
+  const bool live = r < nrows;
+  const int t = (int)div_by((uint32_t)(live ? r : r0), p.group), h = hk * p.G + (live ? r : r0) - t * p.G;
+  const int q0 = first_key(t), q1 = last_key(t);
+  Frag qf[KK];
+  {
+    const T *src = (const T *)p.q + pc.i * p.qb + t * p.qt + h * p.qh;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      const int d = 32 * k + 8 * lg;
+      qf[k] = zero_frag<T>();
+      if (live && d < p.N) {
+        if (p.qvec) {
+          load_frag(qf[k], src + d);
+        } else {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = to_f(src[d + e]);
+          qf[k] = pack8<T>(v);
+        }
+        if (p.negate) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = -elem(qf[k], e);
+          qf[k] = pack8<T>(v);
+        }
+      }
+    }
+  }
+
+  // the loads of a tile of keys
+  const T *const kc = (const T *)p.c.kc + hk * p.c.kh, *const vc = (const T *)p.c.vc + hk * p.c.vh;
+  const int32_t *const table = p.c.table + pc.i * p.c.tb;
+  // page of a key that may lie outside the cache or on no page (then 0, *ok = false)
+  auto lookup = [&](int key, bool *ok, int *at) {
+    const uint32_t kk = (uint32_t)min(key, p.c.capacity - 1), e = div_by(kk, p.c.page);
+    const int pg = table[e];
+    *ok = key < p.c.capacity && pg >= 0 && pg < p.c.pages;
+    *at = *ok ? (int)(kk - e * p.c.page.d) : 0;
+    return *ok ? pg : 0;
+  };
+  int vrow[PI], vcol[PI]; // of the lane's pieces of 16 rows of V
+#pragma unroll
+  for (int i = 0; i < PI; ++i) {
+    const int x = i * 64 + lane;
+    vrow[i] = x / PC, vcol[i] = x % PC * (16 / ES);
+  }
+  Frag kf[KT][KK];
+  u32x4 vr[KT * PI];
+  uint32_t have_k = 0, have_v = 0; // keys of the tile that lie on a page, one bit each
+  auto load_k = [&](int kb) {
+    have_k = 0;
+#pragma unroll
+    for (int g = 0; g < KT; ++g) {
+      bool ok;
+      int at;
+      const T *src;
+      if constexpr (UNI) {
+        const int pg = lookup(kb + 16 * g, &ok, &at);
+        src = kc + pg * p.c.kp + at * p.c.ks + li * p.c.ks;
+        if (ok) have_k |= 0xFFFFu << (16 * g);
+      } else {
+        const int pg = lookup(kb + 16 * g + li, &ok, &at);
+        src = kc + pg * p.c.kp + at * p.c.ks;
+        have_k |= (uint32_t)(__builtin_amdgcn_ballot_w64(ok) & 0xFFFFu) << (16 * g);
+      }
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        const int d = 32 * k + 8 * lg;
+        if (d < p.N) load_frag(kf[g][k], src + d);
+        else kf[g][k] = zero_frag<T>();
+      }
+    }
+  };
+  auto load_v = [&](int kb) {
+#pragma unroll
+    for (int g = 0; g < KT; ++g) {
+      bool ok;
+      int at, pg = 0;
+      if constexpr (UNI) pg = lookup(kb + 16 * g, &ok, &at);
+#pragma unroll
+      for (int i = 0; i < PI; ++i) {
+        if constexpr (!UNI) pg = lookup(kb + 16 * g + vrow[i], &ok, &at);
+        const T *src = vc + pg * p.c.vp + at * p.c.vs + (UNI ? vrow[i] * p.c.vs : 0);
+        vr[g * PI + i] = *reinterpret_cast<const u32x4 *>(src + (vcol[i] < p.N ? vcol[i] : 0));
+      }
+    }
+  };
+
+  f32x4 o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+  T *const vt = reinterpret_cast<T *>(lds + wave * kTile);
+  int kb = (k0 & ~(TK - 1)) + wave * TK;
+  if (kb < k1) load_k(kb), load_v(kb);
+  for (; kb < k1; kb += kWaves * TK) {
+    const int next = kb + kWaves * TK;
+    // S^T = K Q^T
+    f32x4 s[KT];
+#pragma unroll
+    for (int g = 0; g < KT; ++g) {
+      s[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KK; ++k) s[g] = mma(kf[g][k], qf[k], s[g]);
+    }
+    have_v = have_k;
+    if (next < k1) load_k(next);
+    // the keys of the tile that any query of the workgroup sees, and whether all see them all
+    const uint32_t lo_bits = k0 > kb ? ~0u << min(k0 - kb, 31) : ~0u;
+    const uint32_t hi_bits = k1 - kb < 32 ? (1u << (k1 - kb)) - 1 : ~0u;
+    const uint32_t seen = have_v & lo_bits & hi_bits;
+    const bool full = seen == (TK == 32 ? ~0u : 0xFFFFu) && kb >= all0 && kb + TK <= all1;
+    if (!full) {
+#pragma unroll
+      for (int g = 0; g < KT; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 16 * g + 4 * lg + e;
+          if (!(seen >> j & 1) || kb + j < q0 || kb + j >= q1) s[g][e] = -INFINITY;
+        }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < KT; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, s[g][e]);
+    const float mn = fmaxf(m, col_max(top) * p.scale);
+    const float base = mn == -INFINITY ? 0.f : mn; // nothing seen yet: every weight 0
+    if (__builtin_amdgcn_ballot_w64(mn != m) != 0) {
+      const float a = hw_exp2(m - base);
+      l *= a;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] *= a;
+      m = mn;
+    }
+    float w[8];
+#pragma unroll
+    for (int g = 0; g < KT; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[4 * g + e] = hw_exp2(fmaf(s[g][e], p.scale, -base));
+        l += w[4 * g + e];
+      }
+    // V through LDS; rows that no query sees are zero there, whatever they held
+    bool odd = false;
+#pragma unroll
+    for (int g = 0; g < KT; ++g)
+#pragma unroll
+      for (int i = 0; i < PI; ++i) {
+        u32x4 v = vr[g * PI + i];
+        if (!full) {
+          if (!(seen >> (16 * g + vrow[i]) & 1)) v = u32x4{0, 0, 0, 0};
+          odd |= odd_values(v, T());
+        }
+        const int unit = vcol[i] / 16;
+        *reinterpret_cast<u32x4 *>(vt + SW::at(16 * g + vrow[i], unit) + vcol[i] % 16) = v;
+      }
+    if (next < k1) load_v(next);
+    if (!full && __builtin_amdgcn_ballot_w64(odd) != 0) {
+      // an infinity or a NaN in a value that some queries see and others may not (a
+      // product would carry it to all): key by key
+      for (int j = 0; j < TK; ++j) {
+        const int from = li + 16 * (j % 16 / 4);
+        float pj = 0.f;
+#pragma unroll
+        for (int g = 0; g < KT; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __shfl(w[4 * g + e], from);
+            if (j / 16 == g && j % 4 == e) pj = x;
+          }
+        const bool see = (seen >> j & 1) && kb + j >= q0 && kb + j < q1;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const T *v = vt + SW::at(j, d) + 4 * lg;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (see) o[d][e] = fmaf(pj, to_f(v[e]), o[d][e]);
+        }
+      }
+    } else if constexpr (ES == 2) {
+      // O^T += V^T P^T; P rounded to bf16: half a step of it, 2^-8 of each weight, less
+      // than the output's own rounding where values of one size are averaged
+      const FragBF pf = pack8<__bf16>(w);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        FragBF vf;
+        const auto tr = [&](int row0) {
+          const __bf16 *a = reinterpret_cast<const __bf16 *>(vt) + SW::at(row0 + 4 * lg + (li >> 2), d) + 4 * (li & 3);
+          return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                                                (__attribute__((address_space(3))) lds_bf16x4 *)(a)));
+        };
+        vf.v = __builtin_shufflevector(tr(0), tr(16), 0, 1, 2, 3, 4, 5, 6, 7);
+        o[d] = mma(vf, pf, o[d]);
+      }
+    } else {
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(to_f(vt[SW::at(4 * lg + e, d) + li]), w[e], o[d], 0, 0, 0);
+    }
+  }
+
+  // join the waves
+  l = col_sum(l);
+  __syncthreads();
+  float *const oj = reinterpret_cast<float *>(lds) + wave * 16 * LO;
+#pragma unroll
+  for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(oj + li * LO + 16 * d + 4 * lg) = o[d];
+  if (lg == 0) ml[wave][li] = make_float2(m, l);
+  __syncthreads();
+  const bool whole = pc.count == 1;
+  const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * kAttnRows;
+  for (int x = threadIdx.x; x < 16 * (NP / 4); x += kThreads) {
+    const int q = x / (NP / 4), c = x % (NP / 4) * 4;
+    if (r0 + q >= nrows || c >= p.N) continue;
+    float2 e[kWaves];
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) e[w] = ml[w][q], top = fmaxf(top, e[w].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float a = hw_exp2(e[w].x - base);
+      sum = fmaf(a, e[w].y, sum);
+      acc += a * *reinterpret_cast<const f32x4 *>(reinterpret_cast<float *>(lds) + (w * 16 + q) * LO + c);
+    }
+    if (whole) {
+      const int tq = (int)div_by((uint32_t)(r0 + q), p.group), hq = hk * p.G + r0 + q - tq * p.G;
+      const int64_t at = ((int64_t)pc.i * p.L + tq) * p.Hq + hq;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      st4<T>((T *)p.out + at * p.N + c, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+      if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
+    } else {
+      *reinterpret_cast<f32x4 *>(p.part + (pr + q) * p.N + c) = acc;
+      if (c == 0) p.part_ml[pr + q] = make_float2(top, sum);
+    }
+  }
+}
+
+// Joins the pieces of the rows that have more than one: a workgroup an output
+// vector, N / 4 threads a piece.
+template <typename T> __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnParams p) {
+  __shared__ float red[kThreads / 64], acc_sh[kThreads][4], sum_sh[kThreads];
+  uint32_t id = blockIdx.x;
+  const int h = (int)(id % (uint32_t)p.Hq);
+  id /= (uint32_t)p.Hq;
+  const int t = (int)(id % (uint32_t)p.L), i = (int)(id / (uint32_t)p.L);
+  const int n = p.c.tokens ? min(max(p.c.tokens[i], 0), p.L) : p.L;
+  if (t >= n) return;
+  const int2 pc = p.pieces[i];
+  if (pc.y <= 1) return;
+  const int hk = (int)div_by((uint32_t)h, p.group), r = t * p.G + h - hk * p.G;
+  const int64_t step = (int64_t)p.Hk * p.tiles * kAttnRows;
+  const int64_t first = ((int64_t)pc.x * p.Hk + hk) * p.tiles * kAttnRows + r;
+  const int tid = threadIdx.x;
+  float top = -INFINITY;
+  for (int c = tid; c < pc.y; c += kThreads) top = fmaxf(top, p.part_ml[first + c * step].x);
+#pragma unroll
+  for (int k = 32; k; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
+  if ((tid & 63) == 0) red[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float base = top == -INFINITY ? 0.f : top;
+  const int nv = p.N / 4, lanes = kThreads / nv; // threads of a piece, pieces at once
+  const int g = tid / nv, c4 = (tid - g * nv) * 4;
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+  if (g < lanes) {
+#pragma unroll 4
+    for (int c = g; c < pc.y; c += lanes) {
+      const float2 e = p.part_ml[first + c * step];
+      const float a = hw_exp2(e.x - base);
+      sum = fmaf(a, e.y, sum);
+      acc += a * *reinterpret_cast<const f32x4 *>(p.part + (first + c * step) * p.N + c4);
+    }
+  }
+  *reinterpret_cast<f32x4 *>(acc_sh[tid]) = acc;
+  sum_sh[tid] = sum;
+  __syncthreads();
+  if (tid >= nv) return;
+  for (int k = 1; k < lanes; ++k) {
+    acc += *reinterpret_cast<const f32x4 *>(acc_sh[k * nv + tid]);
+    sum += sum_sh[k * nv + tid];
+  }
+  const int64_t at = ((int64_t)i * p.L + t) * p.Hq + h;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  st4<T>((T *)p.out + at * p.N + c4, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+  if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
+}
+
+template <typename T, int NP> hipError_t launch_np(const AttnParams &p, hipStream_t st) {
+  const uint32_t grid = (uint32_t)((int64_t)p.slots * p.Hk * p.tiles);
+  if (p.c.page.d % 16 == 0) attn_kernel<T, NP, true><<<grid, kThreads, 0, st>>>(p);
+  else attn_kernel<T, NP, false><<<grid, kThreads, 0, st>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.workers == 1) return e;
+  attn_join_kernel<T><<<(uint32_t)((int64_t)p.b * p.L * p.Hq), kThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
+template <typename T> hipError_t launch_t(const AttnParams &p, hipStream_t st) {
+  if (p.N <= 32) return launch_np<T, 32>(p, st);
+  if (p.N <= 64) return launch_np<T, 64>(p, st);
+  if (p.N <= 96) return launch_np<T, 96>(p, st);
+  if (p.N <= 128) return launch_np<T, 128>(p, st);
+  if (p.N <= 192) return launch_np<T, 192>(p, st);
+  return launch_np<T, 256>(p, st);
+}
+
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
+
+} // namespace
+
+int64_t attn_plan(AttnParams *p) {
+  constexpr int64_t kTarget = 1024; // workgroups that fill the device
+  const int64_t tiles = ((int64_t)p->L * p->G + kAttnRows - 1) / kAttnRows, heads = p->Hk * tiles;
+  p->tiles = (int)tiles;
+  p->workers = heads * p->b >= 8 * kTarget ? 1 : (int)((kTarget + heads - 1) / heads);
+  p->slots = p->workers == 1 ? p->b : p->workers + p->b;
+  if (p->slots * heads > kMaxGroups) return -1;
+  if (p->workers == 1) return 0;
+  const int64_t rows = p->slots * heads * kAttnRows;
+  return up256(rows * p->N * 4) + up256(rows * 8) + up256((int64_t)p->b * 8);
+}
+
+void attn_workspace(AttnParams *p, void *workspace) {
+  const int64_t rows = (int64_t)p->slots * p->Hk * p->tiles * kAttnRows;
+  char *w = (char *)workspace;
+  p->part = (float *)w;
+  p->part_ml = (float2 *)(w + up256(rows * p->N * 4));
+  p->pieces = (int2 *)(w + up256(rows * p->N * 4) + up256(rows * 8));
+}
+
+hipError_t launch_attn(int dtype, const AttnParams &p, hipStream_t st) {
+  return dtype == 1 ? launch_t<__bf16>(p, st) : launch_t<float>(p, st);
+}
+
+} // namespace ssd

@@ -106,6 +106,14 @@ def lib():
         L.ssd_norm_rotate_fwd.restype = ctypes.c_int
         L.ssd_norm_rotate_bwd.argtypes = [P] * 12 + [ctypes.c_float, ctypes.c_int, P, I64, P]
         L.ssd_norm_rotate_bwd.restype = ctypes.c_int
+        L.ssd_kv_append.argtypes = [P] * 10 + [ctypes.c_int, P]
+        L.ssd_kv_append.restype = ctypes.c_int
+        L.ssd_attn_workspace.argtypes = [I64] * 5
+        L.ssd_attn_workspace.restype = I64
+        L.ssd_attn_fwd.argtypes = [P] * 8 + [ctypes.c_float, I64, P, I64, P]
+        L.ssd_attn_fwd.restype = ctypes.c_int
+        L.ssd_attn_step.argtypes = [P] * 7 + [ctypes.c_float, I64, P, I64, P]
+        L.ssd_attn_step.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -543,6 +551,80 @@ def ssd_norm_rotate_bwd(q, k, q_weight, k_weight, freqs, positions, dq_out, dk_o
                                            ws.numel() if ws is not None else 0, st)
     _check(status)
     return g
+
+
+def ssd_kv_append(k, v, k_cache, v_cache, page_table, start, *, q=None, freqs=None, tokens=None,
+                  interleaved: bool = False, q_out=None, stream=None):
+    """Keys and values k, v [b, L, Hk, N] of new tokens into the paged caches
+    [pages, page_size, Hk, N], the keys turned by their positions start[i] + t
+    on the way, and queries q [b, L, Hq, N] turned in the same pass (``freqs`` as
+    for ssd_norm_rotate_fwd, None: not turned).  page_table [b, width], start [b]
+    and tokens [b] (None: all L) are int32.  Returns q_out (None without q)."""
+    if q is not None and q_out is None:
+        with _on_stream(stream, k):
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    with _on_device(k):
+        st = _stream(stream, k)
+        keep, d = _descs(q, k, v, freqs, page_table, start, tokens, q_out, k_cache, v_cache)
+        status = lib().ssd_kv_append(*d, int(interleaved), st)
+    _check(status)
+    return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def ssd_attn_workspace(b: int, L: int, Hq: int, Hk: int, N: int) -> int:
+    """Workspace bytes of ssd_attn_fwd, with L = 1 of ssd_attn_step (-1: sizes
+    they refuse)."""
+    return int(lib().ssd_attn_workspace(int(b), int(L), int(Hq), int(Hk), int(N)))
+
+
+def _attn_workspace(q, k_cache):
+    if q.dim() not in (3, 4) or k_cache.dim() != 4:
+        return None  # refused by the call
+    b, L = (q.shape[0], 1) if q.dim() == 3 else q.shape[:2]
+    return _workspace(ssd_attn_workspace(b, L, q.shape[-2], k_cache.shape[2], q.shape[-1]), q)
+
+
+def ssd_attn_fwd(q, k_cache, v_cache, page_table, start, *, tokens=None, scale: float = None, window: int = 0,
+                 out=None, lse=None, return_lse: bool = True, stream=None):
+    """Attention of the new tokens q [b, L, Hq, N], at positions start[i] + t, over
+    the paged caches, which hold them already (see ssd_kv_append): each sees the
+    keys up to its own position, with ``window`` the last ``window`` of them.
+    scale: of the scores (default 1 / sqrt(N)).  Returns (out, lse or None), lse
+    [b, L, Hq] the logarithm of the sum of e^score."""
+    with _on_stream(stream, q):
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if lse is None and return_lse:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        ws = _attn_workspace(q, k_cache)
+    with _on_device(q):
+        st = _stream(stream, q)
+        keep, d = _descs(q, k_cache, v_cache, page_table, start, tokens, out, lse)
+        status = lib().ssd_attn_fwd(*d, q.shape[-1] ** -0.5 if scale is None else scale, int(window),
+                                    ws.data_ptr() if ws is not None else None,
+                                    ws.numel() if ws is not None else 0, st)
+    _check(status)
+    return out, lse
+
+
+def ssd_attn_step(q, k_cache, v_cache, page_table, start, *, scale: float = None, window: int = 0, out=None,
+                  lse=None, stream=None):
+    """Attention of one new token for every row, q [b, Hq, N] at position
+    start[i], over the paged caches (see ssd_attn_fwd); fills ``lse`` [b, Hq] if it is
+    given; returns out."""
+    with _on_stream(stream, q):
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ws = _attn_workspace(q, k_cache)
+    with _on_device(q):
+        st = _stream(stream, q)
+        keep, d = _descs(q, k_cache, v_cache, page_table, start, out, lse)
+        status = lib().ssd_attn_step(*d, q.shape[-1] ** -0.5 if scale is None else scale, int(window),
+                                     ws.data_ptr() if ws is not None else None,
+                                     ws.numel() if ws is not None else 0, st)
+    _check(status)
+    return out
 
 
 def ssd_scan_plan(b, L, H, P, G, N, dtype=torch.bfloat16, cus: int = 256):
