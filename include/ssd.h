@@ -605,7 +605,8 @@ int ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *v,
 
 /* Workspace bytes of ssd_attn_fwd (and, with L = 1, of ssd_attn_step), see
  * Workspace above; 0 where none is needed, -1 for sizes they refuse.  Host only.
- * It does not depend on the cache or on the rows' lengths. */
+ * It does not depend on the cache or on the rows' lengths, and suffices for either
+ * dtype. */
 int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk,
                            int64_t N);
 

@@ -19,13 +19,12 @@
 // part of it, written as rows and read transposed (ds_read_b64_tr_b16).
 //
 // Long caches are cut into pieces (see piece_of); attn_join_kernel joins them.
-#include "ssd_cache.h"
-#include "ssd_device.h"
+#include "ssd_attn_device.h"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 256, kWaves = 4;
+constexpr int kThreads = 256, kWaves = 4, kRows = 16;
 
 // Keys of a tile: the K of the second product's matrix instruction (bf16 32,
 // fp32 four times 4).
@@ -39,137 +38,6 @@ __device__ __forceinline__ float col_max(float v) {
 __device__ __forceinline__ float col_sum(float v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
-}
-
-__device__ __forceinline__ int wave_incl_scan_i(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
-  return v;
-}
-
-// A row of the batch: how many new tokens it has, where the first one stands and
-// the keys that any of them sees, [lo, hi).
-struct Row {
-  int n, lo, hi;
-  int64_t start;
-  // kAttnUnit-key units from lo, rounded down to a unit, to hi; a row with tokens
-  // but no keys has one, in which nothing is seen
-  __device__ __forceinline__ int units() const {
-    if (n == 0) return 0;
-    const int u = (hi + kAttnUnit - 1) / kAttnUnit - lo / kAttnUnit;
-    return max(u, 1);
-  }
-};
-__device__ __forceinline__ Row row_of(const AttnParams &p, int i) {
-  Row r;
-  r.start = p.c.start[i];
-  r.n = p.c.tokens ? min(max(p.c.tokens[i], 0), p.L) : p.L;
-  const int64_t cap = p.c.capacity;
-  const int64_t hi = min(max(r.start + r.n, (int64_t)0), cap);
-  const int64_t lo = p.window ? min(max(r.start + 1 - p.window, (int64_t)0), hi) : 0;
-  r.lo = (int)lo, r.hi = (int)hi;
-  return r;
-}
-
-// A piece: keys [k0, k1) of row i, its `index`th of `count`.
-struct Piece {
-  int i, index, count, first, size; // first: the row's first piece; size: units of a piece
-};
-// The plan, the same in every workgroup: all rows' lengths together are cut into
-// about p.workers pieces of equal size, so that a batch of one long row and many
-// short ones keeps the device as busy as an even one.  Piece `slot` of that list.
-// The sum of the units stays below 2^31 (checked on the host).
-__device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh, Piece *pc) {
-  if (p.workers == 1) {
-    *pc = Piece{slot, 0, 1, slot, INT32_MAX};
-    return slot < p.b;
-  }
-  const int tid = threadIdx.x, lane = tid & 63;
-  constexpr int kMinUnits = 4;
-  if (p.b <= 64) { // every wave by itself
-    const int u = lane < p.b ? row_of(p, lane).units() : 0;
-    const int total = __builtin_amdgcn_readlane(wave_incl_scan_i(u), 63);
-    const int size = max((total + p.workers - 1) / p.workers, kMinUnits);
-    const int cnt = (u + size - 1) / size, end = wave_incl_scan_i(cnt);
-    const uint64_t m = __builtin_amdgcn_ballot_w64(end > slot);
-    if (m == 0) return false;
-    const int i = (int)__builtin_ctzll(m);
-    const int c = __builtin_amdgcn_readlane(cnt, i), f = __builtin_amdgcn_readlane(end, i) - c;
-    *pc = Piece{i, slot - f, c, f, size};
-    return true;
-  }
-  // each thread a run of rows
-  const int per = (p.b + kThreads - 1) / kThreads, i0 = min(tid * per, p.b), i1 = min(i0 + per, p.b);
-  int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += row_of(p, i).units();
-  sum = wave_incl_scan_i(sum);
-  if (lane == 63) sh[tid >> 6] = sum;
-  __syncthreads();
-  const int total = sh[0] + sh[1] + sh[2] + sh[3];
-  __syncthreads();
-  const int size = max((total + p.workers - 1) / p.workers, kMinUnits);
-  int cnt = 0;
-  for (int i = i0; i < i1; ++i) cnt += (row_of(p, i).units() + size - 1) / size;
-  const int incl = wave_incl_scan_i(cnt);
-  if (lane == 63) sh[tid >> 6] = incl;
-  if (tid == 0) sh[4] = -1;
-  __syncthreads();
-  int before = incl - cnt;
-  for (int w = 0; w < (tid >> 6); ++w) before += sh[w];
-  if (slot >= before && slot < before + cnt)
-    for (int i = i0; i < i1; ++i) {
-      const int c = (row_of(p, i).units() + size - 1) / size;
-      if (slot < before + c) {
-        sh[4] = i, sh[5] = before, sh[6] = c;
-        break;
-      }
-      before += c;
-    }
-  __syncthreads();
-  const int i = sh[4], f = sh[5], c = sh[6];
-  __syncthreads();
-  *pc = Piece{i, slot - f, c, f, size};
-  return i >= 0;
-}
-
-// A V tile of a wave in LDS: 16-byte pieces of its rows as they come, but the
-// 16-column units of a row exchanged by its number, so that the rows a transposed
-// read touches at once lie on different banks.
-template <typename T, int NP> struct Swizzle {
-  static constexpr int UB = 16 * sizeof(T), NU = NP / 16; // bytes of a unit, units of a row
-  static constexpr int kAll = 256 / UB;                   // units of all banks: 8 (bf16), 4 (fp32)
-  static constexpr int pow2(int n) { return n % 2 ? 1 : 2 * pow2(n / 2); }
-  static constexpr int U2 = pow2(NU) < kAll ? pow2(NU) : kAll;
-  __device__ static __forceinline__ int at(int row, int unit) { // first element of the unit
-    const int x = sizeof(T) == 2 ? row / (kAll / U2) : row / 4;
-    return row * NP + (unit ^ (x & (U2 - 1))) * 16;
-  }
-};
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ bool odd_values(u32x4 v, __bf16) { // an infinity or a NaN among them
-  bool b = false;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b |= (v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u;
-  return b;
-}
-__device__ __forceinline__ bool odd_values(u32x4 v, float) {
-  bool b = false;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b |= (v[e] & 0x7F800000u) == 0x7F800000u;
-  return b;
-}
-
-__device__ __forceinline__ void load_frag(FragBF &f, const __bf16 *p) { f.v = *reinterpret_cast<const bf16x8 *>(p); }
-__device__ __forceinline__ void load_frag(FragF32 &f, const float *p) {
-  const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) f.v[e] = a[e], f.v[4 + e] = b[e];
 }
 
 template <typename T> __device__ __forceinline__ typename FragOf<T>::type zero_frag() {
@@ -191,7 +59,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
   constexpr int kTile = TK * NP * ES, kJoin = 16 * LO * 4;
   __shared__ __align__(16) char lds[kWaves * (kTile > kJoin ? kTile : kJoin)];
   __shared__ float2 ml[kWaves][16];
-  __shared__ int sh[8];
+  __shared__ int sh[11];
 
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -200,19 +68,19 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
   id /= (uint32_t)p.tiles;
   const int hk = (int)(id % (uint32_t)p.Hk), slot = (int)(id / (uint32_t)p.Hk);
   Piece pc;
-  if (!piece_of(p, slot, sh, &pc)) return;
+  if (!piece_of<kThreads>(p, slot, sh, &pc)) return;
   pc.i = __builtin_amdgcn_readfirstlane(pc.i);
   pc.index = __builtin_amdgcn_readfirstlane(pc.index);
   pc.size = __builtin_amdgcn_readfirstlane(pc.size);
   const Row row = row_of(p, pc.i);
   if (p.workers > 1 && pc.index == 0 && hk == 0 && tile == 0 && threadIdx.x == 0)
     p.pieces[pc.i] = make_int2(pc.first, pc.count);
-  const int nrows = row.n * p.G, r0 = tile * kAttnRows;
+  const int nrows = row.n * p.G, r0 = tile * kRows;
   if (r0 >= nrows) return;
 
   // the tile's tokens and the keys that any and all of its queries see
   const int t_first = (int)div_by((uint32_t)r0, p.group);
-  const int t_last = (int)div_by((uint32_t)(min(r0 + kAttnRows, nrows) - 1), p.group);
+  const int t_last = (int)div_by((uint32_t)(min(r0 + kRows, nrows) - 1), p.group);
   const int64_t cap = p.c.capacity;
   auto last_key = [&](int t) { return (int)min(max(row.start + t + 1, (int64_t)0), cap); };
   auto first_key = [&](int t) { return p.window ? (int)min(max(row.start + t + 1 - p.window, (int64_t)0), cap) : 0; };
@@ -439,7 +307,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
   if (lg == 0) ml[wave][li] = make_float2(m, l);
   __syncthreads();
   const bool whole = pc.count == 1;
-  const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * kAttnRows;
+  const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * kRows;
   for (int x = threadIdx.x; x < 16 * (NP / 4); x += kThreads) {
     const int q = x / (NP / 4), c = x % (NP / 4) * 4;
     if (r0 + q >= nrows || c >= p.N) continue;
@@ -482,8 +350,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void attn_join_kern
   const int2 pc = p.pieces[i];
   if (pc.y <= 1) return;
   const int hk = (int)div_by((uint32_t)h, p.group), r = t * p.G + h - hk * p.G;
-  const int64_t step = (int64_t)p.Hk * p.tiles * kAttnRows;
-  const int64_t first = ((int64_t)pc.x * p.Hk + hk) * p.tiles * kAttnRows + r;
+  const int64_t step = (int64_t)p.Hk * p.tiles * p.rows;
+  const int64_t first = ((int64_t)pc.x * p.Hk + hk) * p.tiles * p.rows + r;
   const int tid = threadIdx.x;
   float top = -INFINITY;
   for (int c = tid; c < pc.y; c += kThreads) top = fmaxf(top, p.part_ml[first + c * step].x);
@@ -520,22 +388,25 @@ template <typename T> __global__ __launch_bounds__(kThreads) void attn_join_kern
   if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
 }
 
-template <typename T, int NP> hipError_t launch_np(const AttnParams &p, hipStream_t st) {
+template <typename T, int NP> void launch_np(const AttnParams &p, hipStream_t st) {
   const uint32_t grid = (uint32_t)((int64_t)p.slots * p.Hk * p.tiles);
   if (p.c.page.d % 16 == 0) attn_kernel<T, NP, true><<<grid, kThreads, 0, st>>>(p);
   else attn_kernel<T, NP, false><<<grid, kThreads, 0, st>>>(p);
-  hipError_t e = hipGetLastError();
+}
+template <typename T> hipError_t launch_t(const AttnParams &p, hipStream_t st) {
+  if (p.rows != kRows) {
+    const hipError_t e = launch_attn_rows(p, st);
+    if (e != hipSuccess) return e;
+  } else if (p.N <= 32) launch_np<T, 32>(p, st);
+  else if (p.N <= 64) launch_np<T, 64>(p, st);
+  else if (p.N <= 96) launch_np<T, 96>(p, st);
+  else if (p.N <= 128) launch_np<T, 128>(p, st);
+  else if (p.N <= 192) launch_np<T, 192>(p, st);
+  else launch_np<T, 256>(p, st);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.workers == 1) return e;
   attn_join_kernel<T><<<(uint32_t)((int64_t)p.b * p.L * p.Hq), kThreads, 0, st>>>(p);
   return hipGetLastError();
-}
-template <typename T> hipError_t launch_t(const AttnParams &p, hipStream_t st) {
-  if (p.N <= 32) return launch_np<T, 32>(p, st);
-  if (p.N <= 64) return launch_np<T, 64>(p, st);
-  if (p.N <= 96) return launch_np<T, 96>(p, st);
-  if (p.N <= 128) return launch_np<T, 128>(p, st);
-  if (p.N <= 192) return launch_np<T, 192>(p, st);
-  return launch_np<T, 256>(p, st);
 }
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -543,20 +414,22 @@ constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
 
 } // namespace
 
-int64_t attn_plan(AttnParams *p) {
-  constexpr int64_t kTarget = 1024; // workgroups that fill the device
-  const int64_t tiles = ((int64_t)p->L * p->G + kAttnRows - 1) / kAttnRows, heads = p->Hk * tiles;
+int64_t attn_plan(AttnParams *p, int dtype) {
+  const int64_t vecs = (int64_t)p->L * p->G;
+  p->rows = dtype == 1 && vecs > 64 ? attn_rows(p->N) : kRows;
+  const int64_t target = p->rows == kRows ? 1024 : 512; // workgroups that fill the device
+  const int64_t tiles = (vecs + p->rows - 1) / p->rows, heads = p->Hk * tiles;
   p->tiles = (int)tiles;
-  p->workers = heads * p->b >= 8 * kTarget ? 1 : (int)((kTarget + heads - 1) / heads);
+  p->workers = heads * p->b >= (p->rows == kRows ? 8 : 1) * target ? 1 : (int)((target + heads - 1) / heads);
   p->slots = p->workers == 1 ? p->b : p->workers + p->b;
   if (p->slots * heads > kMaxGroups) return -1;
   if (p->workers == 1) return 0;
-  const int64_t rows = p->slots * heads * kAttnRows;
+  const int64_t rows = p->slots * heads * p->rows;
   return up256(rows * p->N * 4) + up256(rows * 8) + up256((int64_t)p->b * 8);
 }
 
 void attn_workspace(AttnParams *p, void *workspace) {
-  const int64_t rows = (int64_t)p->slots * p->Hk * p->tiles * kAttnRows;
+  const int64_t rows = (int64_t)p->slots * p->Hk * p->tiles * p->rows;
   char *w = (char *)workspace;
   p->part = (float *)w;
   p->part_ml = (float2 *)(w + up256(rows * p->N * 4));

@@ -1,0 +1,145 @@
+// ssd_attn_device.h -- what the attention kernels share: the rows of the batch and
+// the pieces their lengths are cut into, V tiles in LDS, odd values.
+#pragma once
+
+#include "ssd_cache.h"
+#include "ssd_device.h"
+
+namespace ssd {
+namespace {
+
+__device__ __forceinline__ int wave_incl_scan_i(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return v;
+}
+
+// A row of the batch: how many new tokens it has, where the first one stands and
+// the keys that any of them sees, [lo, hi).
+struct Row {
+  int n, lo, hi;
+  int64_t start;
+  // kAttnUnit-key units from lo, rounded down to a unit, to hi; a row with tokens
+  // but no keys has one, in which nothing is seen
+  __device__ __forceinline__ int units() const {
+    if (n == 0) return 0;
+    const int u = (hi + kAttnUnit - 1) / kAttnUnit - lo / kAttnUnit;
+    return max(u, 1);
+  }
+};
+__device__ __forceinline__ Row row_of(const AttnParams &p, int i) {
+  Row r;
+  r.start = p.c.start[i];
+  r.n = p.c.tokens ? min(max(p.c.tokens[i], 0), p.L) : p.L;
+  const int64_t cap = p.c.capacity;
+  const int64_t hi = min(max(r.start + r.n, (int64_t)0), cap);
+  const int64_t lo = p.window ? min(max(r.start + 1 - p.window, (int64_t)0), hi) : 0;
+  r.lo = (int)lo, r.hi = (int)hi;
+  return r;
+}
+
+// A piece: keys [k0, k1) of row i, its `index`th of `count`.
+struct Piece {
+  int i, index, count, first, size; // first: the row's first piece; size: units of a piece
+};
+// sh: 11 words of LDS.  The plan, the same in every workgroup: all rows' lengths together are cut into
+// about p.workers pieces of equal size, so that a batch of one long row and many
+// short ones keeps the device as busy as an even one.  Piece `slot` of that list.
+// The sum of the units stays below 2^31 (checked on the host).
+template <int THREADS>
+__device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh, Piece *pc) {
+  if (p.workers == 1) {
+    *pc = Piece{slot, 0, 1, slot, INT32_MAX};
+    return slot < p.b;
+  }
+  const int tid = threadIdx.x, lane = tid & 63;
+  constexpr int kMinUnits = 4;
+  if (p.b <= 64) { // every wave by itself
+    const int u = lane < p.b ? row_of(p, lane).units() : 0;
+    const int total = __builtin_amdgcn_readlane(wave_incl_scan_i(u), 63);
+    const int size = max((total + p.workers - 1) / p.workers, kMinUnits);
+    const int cnt = (u + size - 1) / size, end = wave_incl_scan_i(cnt);
+    const uint64_t m = __builtin_amdgcn_ballot_w64(end > slot);
+    if (m == 0) return false;
+    const int i = (int)__builtin_ctzll(m);
+    const int c = __builtin_amdgcn_readlane(cnt, i), f = __builtin_amdgcn_readlane(end, i) - c;
+    *pc = Piece{i, slot - f, c, f, size};
+    return true;
+  }
+  // each thread a run of rows
+  const int per = (p.b + THREADS - 1) / THREADS, i0 = min(tid * per, p.b), i1 = min(i0 + per, p.b);
+  int sum = 0;
+  for (int i = i0; i < i1; ++i) sum += row_of(p, i).units();
+  sum = wave_incl_scan_i(sum);
+  if (lane == 63) sh[tid >> 6] = sum;
+  __syncthreads();
+  int total = 0;
+  for (int w = 0; w < THREADS / 64; ++w) total += sh[w];
+  __syncthreads();
+  const int size = max((total + p.workers - 1) / p.workers, kMinUnits);
+  int cnt = 0;
+  for (int i = i0; i < i1; ++i) cnt += (row_of(p, i).units() + size - 1) / size;
+  const int incl = wave_incl_scan_i(cnt);
+  if (lane == 63) sh[tid >> 6] = incl;
+  if (tid == 0) sh[8] = -1;
+  __syncthreads();
+  int before = incl - cnt;
+  for (int w = 0; w < (tid >> 6); ++w) before += sh[w];
+  if (slot >= before && slot < before + cnt)
+    for (int i = i0; i < i1; ++i) {
+      const int c = (row_of(p, i).units() + size - 1) / size;
+      if (slot < before + c) {
+        sh[8] = i, sh[9] = before, sh[10] = c;
+        break;
+      }
+      before += c;
+    }
+  __syncthreads();
+  const int i = sh[8], f = sh[9], c = sh[10];
+  __syncthreads();
+  *pc = Piece{i, slot - f, c, f, size};
+  return i >= 0;
+}
+
+// A V tile of a wave in LDS: 16-byte pieces of its rows as they come, but the
+// 16-column units of a row exchanged by its number, so that the rows a transposed
+// read touches at once lie on different banks.
+template <typename T, int NP> struct Swizzle {
+  static constexpr int UB = 16 * sizeof(T), NU = NP / 16; // bytes of a unit, units of a row
+  static constexpr int kAll = 256 / UB;                   // units of all banks: 8 (bf16), 4 (fp32)
+  static constexpr int pow2(int n) { return n % 2 ? 1 : 2 * pow2(n / 2); }
+  static constexpr int U2 = pow2(NU) < kAll ? pow2(NU) : kAll;
+  __device__ static __forceinline__ int at(int row, int unit) { // first element of the unit
+    const int x = sizeof(T) == 2 ? row / (kAll / U2) : row / 4;
+    return row * NP + (unit ^ (x & (U2 - 1))) * 16;
+  }
+};
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ bool odd_values(u32x4 v, __bf16) { // an infinity or a NaN among them
+  bool b = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b |= (v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u;
+  return b;
+}
+__device__ __forceinline__ bool odd_values(u32x4 v, float) {
+  bool b = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b |= (v[e] & 0x7F800000u) == 0x7F800000u;
+  return b;
+}
+
+__device__ __forceinline__ void load_frag(FragBF &f, const __bf16 *p) { f.v = *reinterpret_cast<const bf16x8 *>(p); }
+__device__ __forceinline__ void load_frag(FragF32 &f, const float *p) {
+  const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f.v[e] = a[e], f.v[4 + e] = b[e];
+}
+
+} // namespace
+} // namespace ssd

@@ -75,14 +75,16 @@ struct AttnParams {
   // set by attn_plan
   int workers;                      // pieces that the rows' lengths are cut into, over all rows; 1: one piece a row
   int slots;                        // pieces at most
-  int tiles;                        // tiles of kAttnRows query vectors
-  float *part;                      // [slots, Hk, tiles, kAttnRows, N], products' sums
-  float2 *part_ml;                  // [slots, Hk, tiles, kAttnRows], maximum and sum
+  int rows, tiles;                  // query vectors of a tile, tiles of a row and key head
+  float *part;                      // [slots, Hk, tiles, rows, N], products' sums
+  float2 *part_ml;                  // [slots, Hk, tiles, rows], maximum and sum
   int2 *pieces;                     // [b]: a row's first piece and how many
 };
-constexpr int kAttnRows = 16;
-// Fills workers, slots and tiles; workspace bytes, -1 if the call is too large.
-int64_t attn_plan(AttnParams *p);
+// Fills workers, slots, rows and tiles; workspace bytes, -1 if the call is too large.
+int64_t attn_plan(AttnParams *p, int dtype);
+// Many query vectors of a row and key head, bf16 (ssd_attn_rows.hip); query vectors of its tile.
+int attn_rows(int N);
+hipError_t launch_attn_rows(const AttnParams &p, hipStream_t stream);
 void attn_workspace(AttnParams *p, void *workspace);
 hipError_t launch_attn(int dtype, const AttnParams &p, hipStream_t stream);
 } // namespace ssd

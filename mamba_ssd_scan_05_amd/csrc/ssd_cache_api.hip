@@ -141,11 +141,18 @@ bool attn_sizes(int64_t b, int64_t L, int64_t Hq, int64_t Hk, int64_t N) {
          Hq <= kMaxHeads && Hk <= kMaxHeads && Hq % Hk == 0 && b * L * Hq <= (int64_t)1 << 30 && N >= 8 && N <= 256 &&
          N % 8 == 0;
 }
-int64_t attn_setup(AttnParams *p, int64_t b, int64_t L, int64_t Hq, int64_t Hk, int64_t N) {
+int64_t attn_setup(AttnParams *p, int dtype, int64_t b, int64_t L, int64_t Hq, int64_t Hk, int64_t N) {
   p->b = (int)b; p->L = (int)L; p->Hq = (int)Hq; p->Hk = (int)Hk; p->N = (int)N;
   p->G = (int)(Hq / Hk);
   p->group = fast_div((uint32_t)p->G);
-  return attn_plan(p);
+  return attn_plan(p, dtype);
+}
+// Workspace that suffices for either type, -1 if the sizes are refused.
+int64_t attn_bytes(int64_t b, int64_t L, int64_t Hq, int64_t Hk, int64_t N) {
+  if (!attn_sizes(b, L, Hq, Hk, N)) return -1;
+  AttnParams p{};
+  const int64_t f = attn_setup(&p, SSD_F32, b, L, Hq, Hk, N), h = attn_setup(&p, SSD_BF16, b, L, Hq, Hk, N);
+  return f < 0 || h < 0 ? -1 : f > h ? f : h;
 }
 
 // q and out [b, Hq, N] (step) or [b, L, Hq, N].
@@ -166,15 +173,15 @@ int attn(const ssd_tensor *q, const ssd_tensor *k_cache, const ssd_tensor *v_cac
                 (long long)Hq, (long long)Hk, (long long)N);
   SSD_CHECK(check_heads(N));
   if (Hq % Hk != 0) return fail(SSD_ERR_SHAPE, "Hq=%lld is not a multiple of Hk=%lld", (long long)Hq, (long long)Hk);
-  AttnParams p{};
-  const int64_t need = attn_sizes(b, L, Hq, Hk, N) ? attn_setup(&p, b, L, Hq, Hk, N) : -1;
-  if (need < 0)
+  if (attn_bytes(b, L, Hq, Hk, N) < 0)
     return fail(SSD_ERR_UNSUPPORTED, "problem too large: b=%lld L=%lld Hq=%lld", (long long)b, (long long)L,
                 (long long)Hq);
   if (!(fabsf(scale) >= FLT_MIN && fabsf(scale) <= 1e30f))
     return fail(SSD_ERR_UNSUPPORTED, "scale=%g is not a finite number other than 0", (double)scale);
   if (window < 0) return fail(SSD_ERR_UNSUPPORTED, "window=%lld is negative", (long long)window);
   SSD_CHECK(act_dtype(q, "q"));
+  AttnParams p{};
+  const int64_t need = attn_setup(&p, q->dtype, b, L, Hq, Hk, N);
   Args args;
   SSD_CHECK(check_arg(q, "q", q->dtype, nd, q->shape, true));
   args.add(q, "q", false);
@@ -279,8 +286,7 @@ int ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *v,
 }
 
 int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk, int64_t N) {
-  AttnParams p{};
-  return attn_sizes(b, L, Hq, Hk, N) ? attn_setup(&p, b, L, Hq, Hk, N) : -1;
+  return attn_bytes(b, L, Hq, Hk, N);
 }
 
 int ssd_attn_fwd(const ssd_tensor *q, const ssd_tensor *k_cache, const ssd_tensor *v_cache,
