@@ -11,7 +11,8 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTK = 64; // keys of a tile
+// Keys of a tile: with 32 the wide heads' tiles and weights leave room for their sums.
+constexpr int tile_keys(int NP) { return NP <= 128 ? 64 : 32; }
 
 // 16-byte pieces of a K row, exchanged by the row's number so that eight rows
 // read at once lie on different banks.
@@ -30,7 +31,11 @@ __device__ __forceinline__ uint64_t bits(int a, int b) {
   return lo & hi;
 }
 
-template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_kernel(AttnParams p) {
+// UNI: the page size is a multiple of 16; the 64 pieces a wave loads at once lie in
+// 16 rows of one page then, which is found by the scalar unit.
+template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 128 ? 2 : 1) void attn_rows_kernel(AttnParams p) {
+  constexpr int kTK = tile_keys(NP), KG = kTK / 32;       // groups of 32 keys
+  constexpr uint64_t kAll = kTK == 64 ? ~0ull : 0xFFFFFFFFull;
   constexpr int KS = NP / 16, DT = NP / 32;               // steps of 16 dims, tiles of 32 dims
   constexpr int PC = NP / 8, CH = (kTK * PC + 64 * W - 1) / (64 * W); // pieces of a row, of a thread
   constexpr int kRows = 32 * W;
@@ -41,9 +46,14 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
 
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // The tiles of a row and key head read the same keys: they go to one XCD (workgroups
+  // are dealt to the eight in turn) where that gives each the same number of them;
+  // the longest ones first.
   uint32_t id = blockIdx.x;
-  const int tile = p.tiles - 1 - (int)(id % (uint32_t)p.tiles); // the longest ones first
-  id /= (uint32_t)p.tiles;
+  const bool deal = (uint32_t)p.slots * (uint32_t)p.Hk % 8 == 0;
+  const uint32_t n = deal ? id >> 3 : id, group = n / (uint32_t)p.tiles;
+  const int tile = p.tiles - 1 - (int)(n - group * (uint32_t)p.tiles);
+  id = deal ? group * 8 + (id & 7) : group;
   const int hk = (int)(id % (uint32_t)p.Hk), slot = (int)(id / (uint32_t)p.Hk);
   Piece pc;
   if (!piece_of<64 * W>(p, slot, sh, &pc)) return;
@@ -106,20 +116,34 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
   auto page_of = [&](int kb) {
     const int key = kb + lane;
     const int pg = table[div_by((uint32_t)min(key, p.c.capacity - 1), p.c.page)];
-    return key < p.c.capacity && pg < p.c.pages ? max(pg, -1) : -1;
+    return key < p.c.capacity && lane < kTK && pg < p.c.pages ? max(pg, -1) : -1;
   };
   u32x4 kr[CH], vr[CH];
-  auto load = [&](int kb, int pages) { // the thread's pieces of a tile
+  // the thread's pieces of a tile: row and element, places in the LDS tiles, offsets in
+  // bytes from the first of 16 rows
+  int krow[CH], kat[CH], vat[CH];
+  uint32_t koff[CH], voff[CH];
+  bool none[CH]; // behind N: zero for K (nothing is taken there for V)
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int x = c * 64 * W + (int)threadIdx.x, piece = x % PC;
+    krow[c] = min(x / PC, kTK - 1);
+    kat[c] = KW::at(krow[c], piece);
+    vat[c] = VW::at(krow[c], piece / 2) + piece % 2 * 8;
+    none[c] = 8 * piece >= p.N;
+    const int d = none[c] ? 0 : 8 * piece;
+    koff[c] = (uint32_t)(((UNI ? krow[c] % 16 * p.c.ks : 0) + d) * 2);
+    voff[c] = (uint32_t)(((UNI ? krow[c] % 16 * p.c.vs : 0) + d) * 2);
+  }
+  auto load = [&](int kb, int pages) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int x = c * 64 * W + (int)threadIdx.x, krow = min(x / PC, kTK - 1), piece = x % PC;
-      const int pg = __shfl(pages, krow);
-      const uint32_t key = (uint32_t)(kb + krow);
+      const int first = UNI ? __builtin_amdgcn_readfirstlane(krow[c]) & ~15 : krow[c];
+      const int pg = UNI ? __builtin_amdgcn_readlane(pages, first) : __shfl(pages, first);
+      const uint32_t key = (uint32_t)(kb + first);
       const int64_t at = pg < 0 ? 0 : key - div_by(key, p.c.page) * p.c.page.d, page = max(pg, 0);
-      const int d = 8 * piece < p.N ? 8 * piece : 0;
-      kr[c] = *reinterpret_cast<const u32x4 *>(kc + page * p.c.kp + at * p.c.ks + d);
-      vr[c] = *reinterpret_cast<const u32x4 *>(vc + page * p.c.vp + at * p.c.vs + d);
-      if (8 * piece >= p.N) kr[c] = u32x4{0, 0, 0, 0};
+      kr[c] = *reinterpret_cast<const u32x4 *>((const char *)(kc + page * p.c.kp + at * p.c.ks) + koff[c]);
+      vr[c] = *reinterpret_cast<const u32x4 *>((const char *)(vc + page * p.c.vp + at * p.c.vs) + voff[c]);
     }
   };
   // to LDS; rows of V that no query of the workgroup sees are zero there, whatever they
@@ -128,18 +152,24 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
     bool odd = false;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int x = c * 64 * W + (int)threadIdx.x, krow = x / PC, piece = x % PC;
-      if (kTK * PC % (64 * W) != 0 && krow >= kTK) continue;
+      if (kTK * PC % (64 * W) != 0 && c * 64 * W + (int)threadIdx.x >= kTK * PC) continue;
       u32x4 v = vr[c];
       if (edge) {
-        if (!(seen >> krow & 1)) v = u32x4{0, 0, 0, 0};
+        if (!(seen >> krow[c] & 1)) v = u32x4{0, 0, 0, 0};
         odd |= odd_values(v, __bf16());
       }
-      *reinterpret_cast<u32x4 *>(&ktile[buf][KW::at(krow, piece)]) = kr[c];
-      *reinterpret_cast<u32x4 *>(&vtile[buf][VW::at(krow, piece / 2) + piece % 2 * 8]) = v;
+      *reinterpret_cast<u32x4 *>(&ktile[buf][kat[c]]) = none[c] ? u32x4{0, 0, 0, 0} : kr[c];
+      *reinterpret_cast<u32x4 *>(&vtile[buf][vat[c]]) = v;
     }
     return odd;
   };
+
+  // where the lane reads in a tile: both exchanges have a period of rows that divides 16 (K) and 8 (V)
+  int kread[KS], vread[DT];
+#pragma unroll
+  for (int k = 0; k < KS; ++k) kread[k] = KW::at(col, 2 * k + half);
+#pragma unroll
+  for (int d = 0; d < DT; ++d) vread[d] = VW::at(4 * half + (lane >> 2 & 3), 2 * d + (lane >> 4 & 1)) + 4 * (lane & 3);
 
   f32x16 o[DT];
 #pragma unroll
@@ -154,7 +184,7 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
   // a tile's rows to LDS and the barrier behind them
   auto publish = [&](int tile_kb, int b) {
     const uint64_t seen = have & bits(k0 - tile_kb, k1 - tile_kb);
-    const bool edge = seen != ~0ull || tile_kb < all0 || tile_kb + kTK > all1;
+    const bool edge = seen != kAll || tile_kb < all0 || tile_kb + kTK > all1;
     const bool o1 = store(b, seen, edge);
     if (edge) {
       odd = __syncthreads_or(o1);
@@ -180,23 +210,23 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
     }
     if (kb < w1 && next > w0) {
       // S^T = K Q^T
-      f32x16 s[2];
+      f32x16 s[KG];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      for (int g = 0; g < KG; ++g) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[g][e] = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const bf16x8 a = *reinterpret_cast<const bf16x8 *>(&ktile[buf][KW::at(32 * g + col, 2 * k + half)]);
+          const bf16x8 a = *reinterpret_cast<const bf16x8 *>(&ktile[buf][32 * g * NP + kread[k]]);
           s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], s[g], 0, 0, 0);
         }
       }
       const uint64_t seen = here & bits(w0 - kb, w1 - kb);
-      const bool full = seen == ~0ull && kb >= wall0 && next <= wall1;
+      const bool full = seen == kAll && kb >= wall0 && next <= wall1;
       if (!full) {
         const uint64_t mine = seen & bits(q0 - kb, q1 - kb);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < KG; ++g) {
           const uint32_t mg = (uint32_t)(mine >> (32 * g)) >> (4 * half);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -205,7 +235,7 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
       }
       float top = -INFINITY;
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
+      for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[g][e]);
       top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
@@ -219,32 +249,36 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
       }
       const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
+      for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           s[g][e] = hw_exp2(fmaf(s[g][e], p.scale, -base));
           l += s[g][e];
         }
       if (!full && odd) {
-        // an infinity or a NaN in a value that some queries see and others may not: key by key
+        // an infinity or a NaN in a value that some queries see and others may not (a
+        // product would carry it to all): key by key, the scores formed again
         const uint64_t mine = seen & bits(q0 - kb, q1 - kb);
+#pragma unroll 1
         for (int j = 0; j < kTK; ++j) {
-          const int jj = j & 31, src = col + 32 * (jj >> 2 & 1), reg = (jj & 3) + 4 * (jj >> 3);
-          float pj = 0.f;
+          float sj = 0.f;
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+          for (int k = 0; k < KS; ++k) {
+            const bf16x8 a = *reinterpret_cast<const bf16x8 *>(&ktile[buf][KW::at(j, 2 * k + half)]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = __shfl(s[g][e], src);
-              if (j / 32 == g && reg == e) pj = x;
-            }
+            for (int e = 0; e < 8; ++e) sj = fmaf((float)a[e], (float)qf[k][e], sj);
+          }
+          sj += __shfl_xor(sj, 32);
+          const float pj = hw_exp2(fmaf(sj, p.scale, -base));
           if (mine >> j & 1) {
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int dim = 32 * d + 8 * (e / 4) + 4 * half + e % 4;
-                o[d][e] = fmaf(pj, (float)vtile[buf][VW::at(j, dim / 16) + dim % 16], o[d][e]);
+              for (int e = 0; e < 4; ++e) {
+                const int dim = 32 * d + 8 * e + 4 * half;
+                const bf16x4 v = *reinterpret_cast<const bf16x4 *>(&vtile[buf][VW::at(j, dim / 16) + dim % 16]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[d][4 * e + x] = fmaf(pj, (float)v[x], o[d][4 * e + x]);
               }
           }
         }
@@ -252,21 +286,19 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
         // O^T += V^T P^T, 16 keys at a time: eight weights of a lane, rounded to bf16
         // (half a step, 2^-8 of each), against the same keys of V
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < KG; ++g)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             bf16x8 pf;
 #pragma unroll
             for (int e = 0; e < 8; ++e) pf[e] = (__bf16)s[g][8 * u + e];
-            const int row0 = 32 * g + 16 * u + 4 * half + (lane >> 2 & 3);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-              const int unit = 2 * d + (lane >> 4 & 1);
-              const auto tr = [&](int rr) {
+              const auto tr = [&](int row) {
                 return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-                    (__attribute__((address_space(3))) lds_bf16x4 *)(&vtile[buf][VW::at(rr, unit) + 4 * (lane & 3)])));
+                    (__attribute__((address_space(3))) lds_bf16x4 *)(&vtile[buf][row * NP + vread[d]])));
               };
-              const bf16x8 vf = __builtin_shufflevector(tr(row0), tr(row0 + 8), 0, 1, 2, 3, 4, 5, 6, 7);
+              const bf16x8 vf = __builtin_shufflevector(tr(32 * g + 16 * u), tr(32 * g + 16 * u + 8), 0, 1, 2, 3, 4, 5, 6, 7);
               o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
             }
           }
@@ -307,16 +339,23 @@ template <int NP, int W> __global__ __launch_bounds__(64 * W) void attn_rows_ker
 
 } // namespace
 
-int attn_rows(int N) { return N <= 128 ? 256 : 128; }
+#ifndef WV
+#define WV 8
+#endif
+int attn_rows(int N) { return N <= 128 ? 32 * WV : 128; }
 
-hipError_t launch_attn_rows(const AttnParams &p, hipStream_t st) {
+template <int NP, int W> static void launch_np(const AttnParams &p, hipStream_t st) {
   const uint32_t grid = (uint32_t)((int64_t)p.slots * p.Hk * p.tiles);
-  if (p.N <= 32) attn_rows_kernel<32, 8><<<grid, 512, 0, st>>>(p);
-  else if (p.N <= 64) attn_rows_kernel<64, 8><<<grid, 512, 0, st>>>(p);
-  else if (p.N <= 96) attn_rows_kernel<96, 8><<<grid, 512, 0, st>>>(p);
-  else if (p.N <= 128) attn_rows_kernel<128, 8><<<grid, 512, 0, st>>>(p);
-  else if (p.N <= 192) attn_rows_kernel<192, 4><<<grid, 256, 0, st>>>(p);
-  else attn_rows_kernel<256, 4><<<grid, 256, 0, st>>>(p);
+  if (p.c.page.d % 16 == 0) attn_rows_kernel<NP, W, true><<<grid, 64 * W, 0, st>>>(p);
+  else attn_rows_kernel<NP, W, false><<<grid, 64 * W, 0, st>>>(p);
+}
+hipError_t launch_attn_rows(const AttnParams &p, hipStream_t st) {
+  if (p.N <= 32) launch_np<32, WV>(p, st);
+  else if (p.N <= 64) launch_np<64, WV>(p, st);
+  else if (p.N <= 96) launch_np<96, WV>(p, st);
+  else if (p.N <= 128) launch_np<128, WV>(p, st);
+  else if (p.N <= 192) launch_np<192, 4>(p, st);
+  else launch_np<256, 4>(p, st);
   return hipGetLastError();
 }
 
