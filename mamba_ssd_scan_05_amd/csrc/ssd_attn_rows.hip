@@ -180,7 +180,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
 
   int kb = k0 & ~(kTK - 1), buf = 0;
   uint64_t have = 0;
-  int odd = 0, pages = -1;
+  int odd = 0, odd_ever = 0, pages = -1;
   // a tile's rows to LDS and the barrier behind them
   auto publish = [&](int tile_kb, int b) {
     const uint64_t seen = have & bits(k0 - tile_kb, k1 - tile_kb);
@@ -188,6 +188,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     const bool o1 = store(b, seen, edge);
     if (edge) {
       odd = __syncthreads_or(o1);
+      odd_ever |= odd;
     } else {
       odd = 0;
       __syncthreads();
@@ -255,34 +256,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
           s[g][e] = hw_exp2(fmaf(s[g][e], p.scale, -base));
           l += s[g][e];
         }
-      if (!full && odd) {
-        // an infinity or a NaN in a value that some queries see and others may not (a
-        // product would carry it to all): key by key, the scores formed again
-        const uint64_t mine = seen & bits(q0 - kb, q1 - kb);
-#pragma unroll 1
-        for (int j = 0; j < kTK; ++j) {
-          float sj = 0.f;
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const bf16x8 a = *reinterpret_cast<const bf16x8 *>(&ktile[buf][KW::at(j, 2 * k + half)]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sj = fmaf((float)a[e], (float)qf[k][e], sj);
-          }
-          sj += __shfl_xor(sj, 32);
-          const float pj = hw_exp2(fmaf(sj, p.scale, -base));
-          if (mine >> j & 1) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int dim = 32 * d + 8 * e + 4 * half;
-                const bf16x4 v = *reinterpret_cast<const bf16x4 *>(&vtile[buf][VW::at(j, dim / 16) + dim % 16]);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) o[d][4 * e + x] = fmaf(pj, (float)v[x], o[d][4 * e + x]);
-              }
-          }
-        }
-      } else {
+      if (full || !odd) {
         // O^T += V^T P^T, 16 keys at a time: eight weights of a lane, rounded to bf16
         // (half a step, 2^-8 of each), against the same keys of V
 #pragma unroll
@@ -305,6 +279,60 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       }
     }
     if (next < k1) publish(next, buf ^ 1);
+  }
+
+  // The edge tiles with an infinity or a NaN in a value that some queries see and others
+  // may not: a product would have carried it to all.  Key by key, from the cache.
+  if (odd_ever && busy) {
+#pragma unroll 1
+    for (kb = k0 & ~(kTK - 1); kb < k1; kb += kTK) {
+      pages = page_of(kb);
+      have = __builtin_amdgcn_ballot_w64(pages >= 0);
+      const uint64_t any = have & bits(k0 - kb, k1 - kb), seen = have & bits(w0 - kb, w1 - kb);
+      if (seen == 0 || (any == kAll && kb >= all0 && kb + kTK <= all1)) continue;
+      if (seen == kAll && kb >= wall0 && kb + kTK <= wall1) continue;
+      auto value_row = [&](int j, int pg) {
+        const uint32_t key = (uint32_t)(kb + j);
+        return vc + pg * p.c.vp + (int64_t)(key - div_by(key, p.c.page) * p.c.page.d) * p.c.vs;
+      };
+      bool o1 = false;
+#pragma unroll 1
+      for (int x = lane; x < kTK * PC; x += 64) {
+        const int j = x / PC, d = x % PC * 8, pg = __shfl(pages, j);
+        if (d < p.N && (any >> j & 1)) o1 |= odd_values(*reinterpret_cast<const u32x4 *>(value_row(j, pg) + d), __bf16());
+      }
+      if (__builtin_amdgcn_ballot_w64(o1) == 0) continue;
+      const uint64_t mine = seen & bits(q0 - kb, q1 - kb);
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+      for (uint64_t left = seen; left; left &= left - 1) {
+        const int j = (int)__builtin_ctzll(left), pg = __builtin_amdgcn_readlane(pages, j);
+        const uint32_t key = (uint32_t)(kb + j);
+        const __bf16 *kr1 = kc + pg * p.c.kp + (int64_t)(key - div_by(key, p.c.page) * p.c.page.d) * p.c.ks;
+        const __bf16 *vr1 = value_row(j, pg);
+        float sj = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          if (16 * k + 8 * half >= p.N) continue;
+          const bf16x8 a = *reinterpret_cast<const bf16x8 *>(kr1 + 16 * k + 8 * half);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sj = fmaf((float)a[e], (float)qf[k][e], sj);
+        }
+        sj += __shfl_xor(sj, 32);
+        const float pj = hw_exp2(fmaf(sj, p.scale, -base));
+        if (!(mine >> j & 1)) continue;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int dim = 32 * d + 8 * e + 4 * half;
+            if (dim >= p.N) continue;
+            const bf16x4 v = *reinterpret_cast<const bf16x4 *>(vr1 + dim);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[d][4 * e + x] = fmaf(pj, (float)v[x], o[d][4 * e + x]);
+          }
+      }
+    }
   }
 
   if (!live) return;
