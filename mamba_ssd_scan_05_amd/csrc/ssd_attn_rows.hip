@@ -212,16 +212,23 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     if (kb < w1 && next > w0) {
       // S^T = K Q^T
       f32x16 s[KG];
+#ifdef SP
+      __builtin_amdgcn_s_setprio(SP);
+#endif
 #pragma unroll
-      for (int g = 0; g < KG; ++g) {
+      for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[g][e] = 0.f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int g = 0; g < KG; ++g) {
           const bf16x8 a = *reinterpret_cast<const bf16x8 *>(&ktile[buf][32 * g * NP + kread[k]]);
           s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], s[g], 0, 0, 0);
         }
-      }
+#ifdef SP
+      __builtin_amdgcn_s_setprio(0);
+#endif
       const uint64_t seen = here & bits(w0 - kb, w1 - kb);
       const bool full = seen == kAll && kb >= wall0 && next <= wall1;
       if (!full) {
@@ -239,7 +246,8 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[g][e]);
-      top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
+      const Both tops = swap32(top);
+      top = fmaxf(tops.a, tops.b) * p.scale;
       // the weights' reference moves only when some weight would pass 2^8
       if (__builtin_amdgcn_ballot_w64(top > m + 8.f) != 0) {
         const float mn = fmaxf(m, top), a = hw_exp2(m - (mn == -INFINITY ? 0.f : mn));
@@ -249,14 +257,20 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
         m = mn;
       }
       const float base = m == -INFINITY ? 0.f : m;
+      float part[4] = {l, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           s[g][e] = hw_exp2(fmaf(s[g][e], p.scale, -base));
-          l += s[g][e];
+          part[e % 4] += s[g][e];
         }
+      l = (part[0] + part[1]) + (part[2] + part[3]);
+      __asm__ volatile("" : "+v"(l)); // here, beside the exponentials, not behind the products
       if (full || !odd) {
+#ifdef SP2
+      __builtin_amdgcn_s_setprio(SP2);
+#endif
         // O^T += V^T P^T, 16 keys at a time: eight weights of a lane, rounded to bf16
         // (half a step, 2^-8 of each), against the same keys of V
 #pragma unroll
@@ -276,6 +290,9 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
               o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
             }
           }
+#ifdef SP2
+      __builtin_amdgcn_s_setprio(0);
+#endif
       }
     }
     if (next < k1) publish(next, buf ^ 1);

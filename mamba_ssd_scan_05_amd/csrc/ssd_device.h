@@ -251,5 +251,19 @@ template <int NL> __device__ __forceinline__ float lane_group_sum(float v) {
   return v;
 }
 
+// Lanes 32 apart (swap32) and 16 apart (swap16) exchanged without LDS: v and what the
+// other lane holds, in either order.
+struct Both {
+  float a, b;
+};
+__device__ __forceinline__ Both swap32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return Both{__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+__device__ __forceinline__ Both swap16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return Both{__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])};
+}
+
 } // namespace
 } // namespace ssd
