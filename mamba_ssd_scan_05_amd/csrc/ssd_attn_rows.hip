@@ -24,6 +24,16 @@ template <int NP> struct KSwizzle {
   }
 };
 
+// V rows: units of 16 columns two by two, exchanged so that the four rows and two units
+// that half of a wave reads at once lie on different banks.
+template <int NP> struct VSwizzle {
+  static constexpr int pow2(int n) { return n % 2 ? 1 : 2 * pow2(n / 2); }
+  static constexpr int P2 = pow2(NP / 32) < 4 ? pow2(NP / 32) : 4;
+  __device__ static __forceinline__ int at(int row, int unit) { // first element of the unit
+    return row * NP + (unit ^ 2 * (row / (4 / P2) & (P2 - 1))) * 16;
+  }
+};
+
 // Bits [a, b) of 64, the ends anywhere.
 __device__ __forceinline__ uint64_t bits(int a, int b) {
   const uint64_t lo = a <= 0 ? ~0ull : a >= 64 ? 0ull : ~0ull << a;
@@ -40,7 +50,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   constexpr int PC = NP / 8, CH = (kTK * PC + 64 * W - 1) / (64 * W); // pieces of a row, of a thread
   constexpr int kRows = 32 * W;
   using KW = KSwizzle<NP>;
-  using VW = Swizzle<__bf16, NP>;
+  using VW = VSwizzle<NP>;
   __shared__ __align__(16) __bf16 ktile[2][kTK * NP], vtile[2][kTK * NP];
   __shared__ int sh[11];
 
@@ -164,7 +174,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     return odd;
   };
 
-  // where the lane reads in a tile: both exchanges have a period of rows that divides 16 (K) and 8 (V)
+  // where the lane reads in a tile: the exchanges have a period of 16 rows (K) and 4 (V) at most
   int kread[KS], vread[DT];
 #pragma unroll
   for (int k = 0; k < KS; ++k) kread[k] = KW::at(col, 2 * k + half);
@@ -212,9 +222,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     if (kb < w1 && next > w0) {
       // S^T = K Q^T
       f32x16 s[KG];
-#ifdef SP
-      __builtin_amdgcn_s_setprio(SP);
-#endif
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int g = 0; g < KG; ++g)
 #pragma unroll
@@ -226,9 +234,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
           const bf16x8 a = *reinterpret_cast<const bf16x8 *>(&ktile[buf][32 * g * NP + kread[k]]);
           s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], s[g], 0, 0, 0);
         }
-#ifdef SP
       __builtin_amdgcn_s_setprio(0);
-#endif
       const uint64_t seen = here & bits(w0 - kb, w1 - kb);
       const bool full = seen == kAll && kb >= wall0 && next <= wall1;
       if (!full) {
@@ -268,9 +274,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       l = (part[0] + part[1]) + (part[2] + part[3]);
       __asm__ volatile("" : "+v"(l)); // here, beside the exponentials, not behind the products
       if (full || !odd) {
-#ifdef SP2
-      __builtin_amdgcn_s_setprio(SP2);
-#endif
+      __builtin_amdgcn_s_setprio(1);
         // O^T += V^T P^T, 16 keys at a time: eight weights of a lane, rounded to bf16
         // (half a step, 2^-8 of each), against the same keys of V
 #pragma unroll
@@ -290,9 +294,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
               o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
             }
           }
-#ifdef SP2
       __builtin_amdgcn_s_setprio(0);
-#endif
       }
     }
     if (next < k1) publish(next, buf ^ 1);
