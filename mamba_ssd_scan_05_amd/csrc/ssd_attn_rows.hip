@@ -4,6 +4,8 @@
 // query vectors for all keys, W waves share the K and V tiles of 64 keys in LDS, two
 // buffers of them, the next tile's rows on their way to registers while one is
 // worked on.  Bound by the matrix cores together with the exponentials.
+#include <type_traits>
+
 #include "ssd_attn_device.h"
 
 namespace ssd {
@@ -122,15 +124,23 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
 
   const __bf16 *const kc = (const __bf16 *)p.c.kc + hk * p.c.kh, *const vc = (const __bf16 *)p.c.vc + hk * p.c.vh;
   const int32_t *const table = p.c.table + pc.i * p.c.tb;
-  // lane l: the page of key kb + l, -1 for none
-  auto page_of = [&](int kb) {
-    const int key = kb + lane;
-    const int pg = table[div_by((uint32_t)min(key, p.c.capacity - 1), p.c.page)];
-    return key < p.c.capacity && lane < kTK && pg < p.c.pages ? max(pg, -1) : -1;
+  // lane l: the table's entry for key kb + l, and the page, -1 for none
+  auto entry_of = [&](int kb) { return table[div_by((uint32_t)min(kb + lane, p.c.capacity - 1), p.c.page)]; };
+  auto page_of = [&](int kb, int entry) {
+    return kb + lane < p.c.capacity && lane < kTK && entry < p.c.pages ? max(entry, -1) : -1;
   };
-  u32x4 kr[CH], vr[CH];
+  // a lane's key: where its rows lie, elements from the caches' first
+  struct Where {
+    int64_t k, v;
+  };
+  auto where_of = [&](int kb, int page) {
+    const uint32_t key = (uint32_t)(kb + lane);
+    const int64_t at = page < 0 ? 0 : key - div_by(key, p.c.page) * p.c.page.d, pg = max(page, 0);
+    return Where{pg * p.c.kp + at * p.c.ks, pg * p.c.vp + at * p.c.vs};
+  };
   // the thread's pieces of a tile: row and element, places in the LDS tiles, offsets in
   // bytes from the first of 16 rows
+  u32x4 kr[CH], vr[CH];
   int krow[CH], kat[CH], vat[CH];
   uint32_t koff[CH], voff[CH];
   bool none[CH]; // behind N: zero for K (nothing is taken there for V)
@@ -145,35 +155,49 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     koff[c] = (uint32_t)(((UNI ? krow[c] % 16 * p.c.ks : 0) + d) * 2);
     voff[c] = (uint32_t)(((UNI ? krow[c] % 16 * p.c.vs : 0) + d) * 2);
   }
-  auto load = [&](int kb, int pages) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int first = UNI ? __builtin_amdgcn_readfirstlane(krow[c]) & ~15 : krow[c];
-      const int pg = UNI ? __builtin_amdgcn_readlane(pages, first) : __shfl(pages, first);
-      const uint32_t key = (uint32_t)(kb + first);
-      const int64_t at = pg < 0 ? 0 : key - div_by(key, p.c.page) * p.c.page.d, page = max(pg, 0);
-      kr[c] = *reinterpret_cast<const u32x4 *>((const char *)(kc + page * p.c.kp + at * p.c.ks) + koff[c]);
-      vr[c] = *reinterpret_cast<const u32x4 *>((const char *)(vc + page * p.c.vp + at * p.c.vs) + voff[c]);
+  auto from_lane = [&](int64_t x, int c) { // the row's value, with UNI that of the wave's 16 rows
+    const int lo = (int)(uint32_t)x, hi = (int)(x >> 32);
+    if constexpr (UNI) {
+      const int f = __builtin_amdgcn_readfirstlane(krow[c]) & ~15;
+      return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, f) << 32) | (uint32_t)__builtin_amdgcn_readlane(lo, f));
+    } else {
+      return (int64_t)(((uint64_t)(uint32_t)__shfl(hi, krow[c]) << 32) | (uint32_t)__shfl(lo, krow[c]));
     }
   };
-  // to LDS; rows of V that no query of the workgroup sees are zero there, whatever they
-  // held.  An edge tile: true if another row holds an infinity or a NaN.
-  auto store = [&](int buf, uint64_t seen, bool edge) {
+  auto load_k = [&](int64_t at) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      kr[c] = *reinterpret_cast<const u32x4 *>((const char *)(kc + from_lane(at, c)) + koff[c]);
+  };
+  auto load_v = [&](int64_t at) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      vr[c] = *reinterpret_cast<const u32x4 *>((const char *)(vc + from_lane(at, c)) + voff[c]);
+  };
+  constexpr bool kRagged = kTK * PC % (64 * W) != 0; // some threads have no last piece
+  auto store_k = [&](__bf16 *tile) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (kRagged && c * 64 * W + (int)threadIdx.x >= kTK * PC) continue;
+      *reinterpret_cast<u32x4 *>(tile + kat[c]) = none[c] ? u32x4{0, 0, 0, 0} : kr[c];
+    }
+  };
+  // Rows of V that no query of the workgroup sees are zero in LDS, whatever they held.  True
+  // if another row of an edge tile holds an infinity or a NaN.
+  auto store_v = [&](__bf16 *tile, uint64_t seen, bool edge) {
     bool odd = false;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (kTK * PC % (64 * W) != 0 && c * 64 * W + (int)threadIdx.x >= kTK * PC) continue;
+      if (kRagged && c * 64 * W + (int)threadIdx.x >= kTK * PC) continue;
       u32x4 v = vr[c];
       if (edge) {
         if (!(seen >> krow[c] & 1)) v = u32x4{0, 0, 0, 0};
         odd |= odd_values(v, __bf16());
       }
-      *reinterpret_cast<u32x4 *>(&ktile[buf][kat[c]]) = none[c] ? u32x4{0, 0, 0, 0} : kr[c];
-      *reinterpret_cast<u32x4 *>(&vtile[buf][vat[c]]) = v;
+      *reinterpret_cast<u32x4 *>(tile + vat[c]) = v;
     }
     return odd;
   };
-
   // where the lane reads in a tile: the exchanges have a period of 16 rows (K) and 4 (V) at most
   int kread[KS], vread[DT];
 #pragma unroll
@@ -181,64 +205,79 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
 #pragma unroll
   for (int d = 0; d < DT; ++d) vread[d] = VW::at(4 * half + (lane >> 2 & 3), 2 * d + (lane >> 4 & 1)) + 4 * (lane & 3);
 
-  f32x16 o[DT];
+  f32x16 o[DT], s0[KG], s1[KG];
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
   float m = -INFINITY, l = 0.f;
-
-  int kb = k0 & ~(kTK - 1), buf = 0;
-  uint64_t have = 0;
-  int odd = 0, odd_ever = 0, pages = -1;
-  // a tile's rows to LDS and the barrier behind them
-  auto publish = [&](int tile_kb, int b) {
-    const uint64_t seen = have & bits(k0 - tile_kb, k1 - tile_kb);
-    const bool edge = seen != kAll || tile_kb < all0 || tile_kb + kTK > all1;
-    const bool o1 = store(b, seen, edge);
-    if (edge) {
-      odd = __syncthreads_or(o1);
-      odd_ever |= odd;
-    } else {
+  int odd = 0, odd_ever = 0;
+  // S^T = K Q^T
+  auto scores = [&](f32x16 *s, const __bf16 *tile) {
+#pragma unroll
+    for (int g = 0; g < KG; ++g)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[g][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        const bf16x8 a = *reinterpret_cast<const bf16x8 *>(tile + 32 * g * NP + kread[k]);
+        s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], s[g], 0, 0, 0);
+      }
+  };
+  // Tile t's V and tile t + 1's K lie in LDS, tile t's scores in registers.  While t's
+  // weights are formed, the scores of t + 1 run on the matrix cores.
+  int kb = k0 & ~(kTK - 1);
+  uint64_t have0 = 0, have1 = 0; // keys of this tile and of the next that lie on a page
+  int64_t v1 = 0;                // the lane's key of the next tile: its row of V
+  int entry = -1;                // and of the one after that: the table's entry
+  auto publish_v = [&](int tile_kb, uint64_t have, __bf16 *tile) {
+    if (have == kAll && tile_kb >= all0 && tile_kb + kTK <= all1) {
+      store_v(tile, 0, false);
       odd = 0;
       __syncthreads();
+    } else {
+      odd = __syncthreads_or(store_v(tile, have & bits(k0 - tile_kb, k1 - tile_kb), true));
+      odd_ever |= odd;
     }
   };
   if (kb < k1) {
-    const int first = page_of(kb);
-    have = __builtin_amdgcn_ballot_w64(first >= 0);
-    load(kb, first);
-    if (kb + kTK < k1) pages = page_of(kb + kTK);
-    publish(kb, 0);
+    int page = page_of(kb, entry_of(kb));
+    have0 = __builtin_amdgcn_ballot_w64(page >= 0);
+    Where at = where_of(kb, page);
+    load_k(at.k);
+    load_v(at.v);
+    store_k(ktile[0]);
+    page = page_of(kb + kTK, entry_of(kb + kTK));
+    have1 = __builtin_amdgcn_ballot_w64(page >= 0);
+    at = where_of(kb + kTK, page);
+    load_k(at.k);
+    v1 = at.v;
+    store_k(ktile[1]);
+    entry = entry_of(kb + 2 * kTK);
+    publish_v(kb, have0, vtile[0]);
+    if (busy) scores(s0, ktile[0]);
+    __syncthreads(); // its place is written again
   }
-  for (; kb < k1; kb += kTK, buf ^= 1) {
-    const int next = kb + kTK;
-    const uint64_t here = have;
+  auto body = [&](auto par, f32x16 *s, f32x16 *sn) {
+    constexpr int P = decltype(par)::value;
+    const int next = kb + kTK, ahead = kb + 2 * kTK;
+    const uint64_t here = have0;
+    have0 = have1;
     if (next < k1) {
-      have = __builtin_amdgcn_ballot_w64(pages >= 0);
-      load(next, pages);
-      if (next + kTK < k1) pages = page_of(next + kTK);
+      load_v(v1);
+      const int page = page_of(ahead, entry);
+      have1 = __builtin_amdgcn_ballot_w64(page >= 0);
+      const Where at = where_of(ahead, page);
+      load_k(at.k);
+      v1 = at.v;
+      entry = entry_of(ahead + kTK);
     }
-    if (kb < w1 && next > w0) {
-      // S^T = K Q^T
-      f32x16 s[KG];
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int g = 0; g < KG; ++g)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[g][e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int g = 0; g < KG; ++g) {
-          const bf16x8 a = *reinterpret_cast<const bf16x8 *>(&ktile[buf][32 * g * NP + kread[k]]);
-          s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], s[g], 0, 0, 0);
-        }
-      __builtin_amdgcn_s_setprio(0);
-      const uint64_t seen = here & bits(w0 - kb, w1 - kb);
-      const bool full = seen == kAll && kb >= wall0 && next <= wall1;
+    if (busy) {
+      const bool full = here == kAll && kb >= wall0 && next <= wall1;
       if (!full) {
-        const uint64_t mine = seen & bits(q0 - kb, q1 - kb);
+        const uint64_t mine = here & bits(q0 - kb, q1 - kb);
 #pragma unroll
         for (int g = 0; g < KG; ++g) {
           const uint32_t mg = (uint32_t)(mine >> (32 * g)) >> (4 * half);
@@ -263,41 +302,55 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
         m = mn;
       }
       const float base = m == -INFINITY ? 0.f : m;
+      scores(sn, ktile[1 - P]); // behind the last tile: of whatever lies there, not used
       float part[4] = {l, 0.f, 0.f, 0.f};
+      bf16x8 pf[2 * KG];
 #pragma unroll
       for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          s[g][e] = hw_exp2(fmaf(s[g][e], p.scale, -base));
-          part[e % 4] += s[g][e];
+          const float w = hw_exp2(fmaf(s[g][e], p.scale, -base));
+          part[e % 4] += w;
+          // weights rounded to bf16 for the product (half a step, 2^-8 of each)
+          pf[2 * g + e / 8][e % 8] = (__bf16)w;
         }
       l = (part[0] + part[1]) + (part[2] + part[3]);
+#ifdef SG
+#pragma unroll
+      for (int i = 0; i < KS * KG; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, SG, 0);
+      }
+#endif
       __asm__ volatile("" : "+v"(l)); // here, beside the exponentials, not behind the products
       if (full || !odd) {
-      __builtin_amdgcn_s_setprio(1);
-        // O^T += V^T P^T, 16 keys at a time: eight weights of a lane, rounded to bf16
-        // (half a step, 2^-8 of each), against the same keys of V
+        // O^T += V^T P^T, 16 keys at a time: eight weights of a lane against the same keys of V
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int g = 0; g < KG; ++g)
+        for (int u = 0; u < 2 * KG; ++u)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            bf16x8 pf;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) pf[e] = (__bf16)s[g][8 * u + e];
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              const auto tr = [&](int row) {
-                return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-                    (__attribute__((address_space(3))) lds_bf16x4 *)(&vtile[buf][row * NP + vread[d]])));
-              };
-              const bf16x8 vf = __builtin_shufflevector(tr(32 * g + 16 * u), tr(32 * g + 16 * u + 8), 0, 1, 2, 3, 4, 5, 6, 7);
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
-            }
+          for (int d = 0; d < DT; ++d) {
+            const auto tr = [&](int row) {
+              return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                  (__attribute__((address_space(3))) lds_bf16x4 *)(&vtile[P][row * NP + vread[d]])));
+            };
+            const bf16x8 vf = __builtin_shufflevector(tr(16 * u), tr(16 * u + 8), 0, 1, 2, 3, 4, 5, 6, 7);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u], o[d], 0, 0, 0);
           }
-      __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_s_setprio(0);
       }
     }
-    if (next < k1) publish(next, buf ^ 1);
+    if (next < k1) {
+      store_k(ktile[P]);
+      publish_v(next, have0, vtile[1 - P]);
+    }
+    kb = next;
+  };
+  while (kb < k1) {
+    body(std::integral_constant<int, 0>(), s0, s1);
+    if (kb >= k1) break;
+    body(std::integral_constant<int, 1>(), s1, s0);
   }
 
   // The edge tiles with an infinity or a NaN in a value that some queries see and others
@@ -305,8 +358,8 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   if (odd_ever && busy) {
 #pragma unroll 1
     for (kb = k0 & ~(kTK - 1); kb < k1; kb += kTK) {
-      pages = page_of(kb);
-      have = __builtin_amdgcn_ballot_w64(pages >= 0);
+      const int pages = page_of(kb, entry_of(kb));
+      const uint64_t have = __builtin_amdgcn_ballot_w64(pages >= 0);
       const uint64_t any = have & bits(k0 - kb, k1 - kb), seen = have & bits(w0 - kb, w1 - kb);
       if (seen == 0 || (any == kAll && kb >= all0 && kb + kTK <= all1)) continue;
       if (seen == kAll && kb >= wall0 && kb + kTK <= wall1) continue;
