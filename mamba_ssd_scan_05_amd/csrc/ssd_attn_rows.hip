@@ -51,9 +51,13 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   constexpr int KS = NP / 16, DT = NP / 32;               // steps of 16 dims, tiles of 32 dims
   constexpr int PC = NP / 8, CH = (kTK * PC + 64 * W - 1) / (64 * W); // pieces of a row, of a thread
   constexpr int kRows = 32 * W;
+#ifndef AH
+#define AH 2
+#endif
+  constexpr int AHEAD = AH;
   using KW = KSwizzle<NP>;
   using VW = VSwizzle<NP>;
-  __shared__ __align__(16) __bf16 ktile[2][kTK * NP], vtile[2][kTK * NP];
+  __shared__ __align__(16) __bf16 ktile[2][kTK * NP], vtile[3][kTK * NP]; // vtile[2]: zeros
   __shared__ int sh[11];
 
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
@@ -141,45 +145,56 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   // the thread's pieces of a tile: row and element, places in the LDS tiles, offsets in
   // bytes from the first of 16 rows
   u32x4 kr[CH], vr[CH];
-  int krow[CH], kat[CH], vat[CH];
-  uint32_t koff[CH], voff[CH];
-  bool none[CH]; // behind N: zero for K (nothing is taken there for V)
+  // Where pieces of one thread lie whole periods of the exchanges apart, one register holds
+  // each of these for all of them.
+  constexpr int RW = 64 * W / PC;
+  constexpr bool kEven = 64 * W % PC == 0 && RW % 16 == 0;
+  constexpr int CA = kEven ? 1 : CH;
+  int krow_[CA], kat_[CA], vat_[CA];
+  uint32_t koff_[CA], voff_[CA];
+  bool none_[CA]; // behind N: zero for K (nothing is taken there for V)
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
+  for (int c = 0; c < CA; ++c) {
     const int x = c * 64 * W + (int)threadIdx.x, piece = x % PC;
-    krow[c] = min(x / PC, kTK - 1);
-    kat[c] = KW::at(krow[c], piece);
-    vat[c] = VW::at(krow[c], piece / 2) + piece % 2 * 8;
-    none[c] = 8 * piece >= p.N;
-    const int d = none[c] ? 0 : 8 * piece;
-    koff[c] = (uint32_t)(((UNI ? krow[c] % 16 * p.c.ks : 0) + d) * 2);
-    voff[c] = (uint32_t)(((UNI ? krow[c] % 16 * p.c.vs : 0) + d) * 2);
+    krow_[c] = min(x / PC, kTK - 1);
+    kat_[c] = KW::at(krow_[c], piece);
+    vat_[c] = VW::at(krow_[c], piece / 2) + piece % 2 * 8;
+    none_[c] = 8 * piece >= p.N;
+    const int d = none_[c] ? 0 : 8 * piece;
+    koff_[c] = (uint32_t)(((UNI ? krow_[c] % 16 * p.c.ks : 0) + d) * 2);
+    voff_[c] = (uint32_t)(((UNI ? krow_[c] % 16 * p.c.vs : 0) + d) * 2);
   }
+  auto krow = [&](int c) { return kEven ? krow_[0] + c * RW : krow_[c]; };
+  auto kat = [&](int c) { return kEven ? kat_[0] + c * RW * NP : kat_[c]; };
+  auto vat = [&](int c) { return kEven ? vat_[0] + c * RW * NP : vat_[c]; };
+  auto koff = [&](int c) { return koff_[kEven ? 0 : c]; };
+  auto voff = [&](int c) { return voff_[kEven ? 0 : c]; };
+  auto none = [&](int c) { return none_[kEven ? 0 : c]; };
   auto from_lane = [&](int64_t x, int c) { // the row's value, with UNI that of the wave's 16 rows
     const int lo = (int)(uint32_t)x, hi = (int)(x >> 32);
     if constexpr (UNI) {
-      const int f = __builtin_amdgcn_readfirstlane(krow[c]) & ~15;
+      const int f = __builtin_amdgcn_readfirstlane(krow(c)) & ~15;
       return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, f) << 32) | (uint32_t)__builtin_amdgcn_readlane(lo, f));
     } else {
-      return (int64_t)(((uint64_t)(uint32_t)__shfl(hi, krow[c]) << 32) | (uint32_t)__shfl(lo, krow[c]));
+      return (int64_t)(((uint64_t)(uint32_t)__shfl(hi, krow(c)) << 32) | (uint32_t)__shfl(lo, krow(c)));
     }
   };
   auto load_k = [&](int64_t at) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      kr[c] = *reinterpret_cast<const u32x4 *>((const char *)(kc + from_lane(at, c)) + koff[c]);
+      kr[c] = *reinterpret_cast<const u32x4 *>((const char *)(kc + from_lane(at, c)) + koff(c));
   };
   auto load_v = [&](int64_t at) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      vr[c] = *reinterpret_cast<const u32x4 *>((const char *)(vc + from_lane(at, c)) + voff[c]);
+      vr[c] = *reinterpret_cast<const u32x4 *>((const char *)(vc + from_lane(at, c)) + voff(c));
   };
   constexpr bool kRagged = kTK * PC % (64 * W) != 0; // some threads have no last piece
   auto store_k = [&](__bf16 *tile) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (kRagged && c * 64 * W + (int)threadIdx.x >= kTK * PC) continue;
-      *reinterpret_cast<u32x4 *>(tile + kat[c]) = none[c] ? u32x4{0, 0, 0, 0} : kr[c];
+      *reinterpret_cast<u32x4 *>(tile + kat(c)) = none(c) ? u32x4{0, 0, 0, 0} : kr[c];
     }
   };
   // Rows of V that no query of the workgroup sees are zero in LDS, whatever they held.  True
@@ -191,19 +206,19 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       if (kRagged && c * 64 * W + (int)threadIdx.x >= kTK * PC) continue;
       u32x4 v = vr[c];
       if (edge) {
-        if (!(seen >> krow[c] & 1)) v = u32x4{0, 0, 0, 0};
+        if (!(seen >> krow(c) & 1)) v = u32x4{0, 0, 0, 0};
         odd |= odd_values(v, __bf16());
       }
-      *reinterpret_cast<u32x4 *>(tile + vat[c]) = v;
+      *reinterpret_cast<u32x4 *>(tile + vat(c)) = v;
     }
     return odd;
   };
-  // where the lane reads in a tile: the exchanges have a period of 16 rows (K) and 4 (V) at most
-  int kread[KS], vread[DT];
-#pragma unroll
-  for (int k = 0; k < KS; ++k) kread[k] = KW::at(col, 2 * k + half);
-#pragma unroll
-  for (int d = 0; d < DT; ++d) vread[d] = VW::at(4 * half + (lane >> 2 & 3), 2 * d + (lane >> 4 & 1)) + 4 * (lane & 3);
+  // Where the lane reads in a tile: the exchanges have a period of 16 rows (K) and 4 (V) at
+  // most.  The step's place is formed at each read from the first one's (an exclusive or and
+  // an addition): a register for each would leave none for reads ahead.
+  const int kline = col * NP, vline = (4 * half + (lane >> 2 & 3)) * NP + 4 * (lane & 3);
+  int kfirst = KW::at(col, half) - kline;
+  int vfirst = VW::at(4 * half + (lane >> 2 & 3), lane >> 4 & 1) + 4 * (lane & 3) - vline;
 
   f32x16 o[DT], s0[KG], s1[KG];
 #pragma unroll
@@ -212,20 +227,13 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
   float m = -INFINITY, l = 0.f;
   int odd = 0, odd_ever = 0;
-  // S^T = K Q^T
-  auto scores = [&](f32x16 *s, const __bf16 *tile) {
-#pragma unroll
-    for (int g = 0; g < KG; ++g)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[g][e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int g = 0; g < KG; ++g) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8 *>(tile + 32 * g * NP + kread[k]);
-        s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, qf[k], s[g], 0, 0, 0);
-      }
+  // S^T = K Q^T: the operand of product i, keys 32 (i % KG) and on, step i / KG
+  auto key_frag = [&](const __bf16 *tile, int kf, int i) {
+    return *reinterpret_cast<const bf16x8 *>(tile + 32 * (i % KG) * NP + ((kf ^ 16 * (i / KG)) + kline));
   };
+  f32x16 zero;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) zero[e] = 0.f;
   // Tile t's V and tile t + 1's K lie in LDS, tile t's scores in registers.  While t's
   // weights are formed, the scores of t + 1 run on the matrix cores.
   int kb = k0 & ~(kTK - 1);
@@ -242,6 +250,12 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       odd_ever |= odd;
     }
   };
+  // The queries are there from here on: as loads still on their way they would be waited for
+  // at the first product of every tile, and with them the loads of the tile to come.
+#pragma unroll
+  for (int k = 0; k < KS; ++k) __asm__ volatile("" : "+v"(qf[k]));
+  for (int x = threadIdx.x; x < kTK * PC; x += 64 * W)
+    *reinterpret_cast<u32x4 *>(&vtile[2][8 * x]) = u32x4{0, 0, 0, 0};
   if (kb < k1) {
     int page = page_of(kb, entry_of(kb));
     have0 = __builtin_amdgcn_ballot_w64(page >= 0);
@@ -257,7 +271,12 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     store_k(ktile[1]);
     entry = entry_of(kb + 2 * kTK);
     publish_v(kb, have0, vtile[0]);
-    if (busy) scores(s0, ktile[0]);
+    if (busy) {
+#pragma unroll
+      for (int i = 0; i < KS * KG; ++i)
+        s0[i % KG] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(ktile[0], kfirst, i), qf[i / KG],
+                                                             i < KG ? zero : s0[i % KG], 0, 0, 0);
+    }
     __syncthreads(); // its place is written again
   }
   auto body = [&](auto par, f32x16 *s, f32x16 *sn) {
@@ -302,43 +321,49 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
         m = mn;
       }
       const float base = m == -INFINITY ? 0.f : m;
-      scores(sn, ktile[1 - P]); // behind the last tile: of whatever lies there, not used
+      // The order is fixed here, step by step: reads from LDS AHEAD of the product that takes
+      // them, and between two products of the next tile's scores some of this tile's weights
+      // (the compiler's own order reads, waits and multiplies in turn).  Then
+      // O^T += V^T P^T, 16 keys at a time: eight weights of a lane against the same keys of V.
+      // Behind the last tile the scores are of whatever lies there, and not used.
+      const __bf16 *const vt = vtile[full || !odd ? P : 2];
+      int kf = kfirst, vf = vfirst;
+      __asm__ volatile("" : "+v"(kf), "+v"(vf));
+      auto kfrag = [&](int i) { return key_frag(ktile[1 - P], kf, i); };
+      auto vfrag = [&](int j) {
+        const __bf16 *const at = vt + 16 * (j / DT) * NP + ((vf ^ 32 * (j % DT)) + vline);
+        const auto tr = [&](int row) {
+          return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+              (__attribute__((address_space(3))) lds_bf16x4 *)(at + row * NP)));
+        };
+        return __builtin_shufflevector(tr(0), tr(8), 0, 1, 2, 3, 4, 5, 6, 7);
+      };
+      constexpr int NK = KS * KG, NV = 2 * KG * DT, E = 16 * KG; // products of either kind, weights of a lane
+      bf16x8 ka[AHEAD], va[AHEAD], pf[2 * KG];
       float part[4] = {l, 0.f, 0.f, 0.f};
-      bf16x8 pf[2 * KG];
 #pragma unroll
-      for (int g = 0; g < KG; ++g)
+      for (int i = 0; i < AHEAD; ++i) ka[i] = kfrag(i);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float w = hw_exp2(fmaf(s[g][e], p.scale, -base));
-          part[e % 4] += w;
+      for (int i = 0; i < NK; ++i) {
+        sn[i % KG] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ka[i % AHEAD], qf[i / KG], i < KG ? zero : sn[i % KG], 0, 0, 0);
+        if (i + AHEAD < NK) ka[i % AHEAD] = kfrag(i + AHEAD);
+        else va[i + AHEAD - NK] = vfrag(i + AHEAD - NK);
+#pragma unroll
+        for (int x = i * E / NK; x < (i + 1) * E / NK; ++x) {
+          const float w = hw_exp2(fmaf(s[x / 16][x % 16], p.scale, -base));
+          part[x % 4] += w;
           // weights rounded to bf16 for the product (half a step, 2^-8 of each)
-          pf[2 * g + e / 8][e % 8] = (__bf16)w;
+          pf[x / 8][x % 8] = (__bf16)w;
         }
-      l = (part[0] + part[1]) + (part[2] + part[3]);
-#ifdef SG
-#pragma unroll
-      for (int i = 0; i < KS * KG; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, SG, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
-#endif
-      __asm__ volatile("" : "+v"(l)); // here, beside the exponentials, not behind the products
-      if (full || !odd) {
-        // O^T += V^T P^T, 16 keys at a time: eight weights of a lane against the same keys of V
-        __builtin_amdgcn_s_setprio(1);
+      l = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
-        for (int u = 0; u < 2 * KG; ++u)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const auto tr = [&](int row) {
-              return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-                  (__attribute__((address_space(3))) lds_bf16x4 *)(&vtile[P][row * NP + vread[d]])));
-            };
-            const bf16x8 vf = __builtin_shufflevector(tr(16 * u), tr(16 * u + 8), 0, 1, 2, 3, 4, 5, 6, 7);
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u], o[d], 0, 0, 0);
-          }
-        __builtin_amdgcn_s_setprio(0);
+      for (int j = 0; j < NV; ++j) {
+        o[j % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[j % AHEAD], pf[j / DT], o[j % DT], 0, 0, 0);
+        if (j + AHEAD < NV) va[j % AHEAD] = vfrag(j + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (next < k1) {
