@@ -570,7 +570,7 @@ int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k,
  * same place leave any one of them, or a mixture, there.
  *
  * Caches may be views: the last dimension contiguous, data and the other strides
- * (>= 0, that of a page's tokens at most 2^24) multiples of 16 bytes; for the append
+ * (>= 0, that of a page's tokens at most 2^24, of pages below 2^32) multiples of 16 bytes; for the append
  * no element may be two (strides that overlap), and k_cache and v_cache may lie
  * in each other's gaps, such as halves of one tensor [pages, 2, page_size, Hk, N].  page_table
  * may have a batch stride.  Offsets are 64 bits wide.

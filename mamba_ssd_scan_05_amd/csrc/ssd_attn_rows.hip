@@ -133,15 +133,6 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   auto page_of = [&](int kb, int entry) {
     return kb + lane < p.c.capacity && lane < kTK && entry < p.c.pages ? max(entry, -1) : -1;
   };
-  // a lane's key: where its rows lie, elements from the caches' first
-  struct Where {
-    int64_t k, v;
-  };
-  auto where_of = [&](int kb, int page) {
-    const uint32_t key = (uint32_t)(kb + lane);
-    const int64_t at = page < 0 ? 0 : key - div_by(key, p.c.page) * p.c.page.d, pg = max(page, 0);
-    return Where{pg * p.c.kp + at * p.c.ks, pg * p.c.vp + at * p.c.vs};
-  };
   // the thread's pieces of a tile: row and element, places in the LDS tiles, offsets in
   // bytes from the first of 16 rows
   u32x4 kr[CH], vr[CH];
@@ -170,24 +161,31 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   auto koff = [&](int c) { return koff_[kEven ? 0 : c]; };
   auto voff = [&](int c) { return voff_[kEven ? 0 : c]; };
   auto none = [&](int c) { return none_[kEven ? 0 : c]; };
-  auto from_lane = [&](int64_t x, int c) { // the row's value, with UNI that of the wave's 16 rows
-    const int lo = (int)(uint32_t)x, hi = (int)(x >> 32);
+  // Loads of the tile at kb, whose keys lie on `pages` (of the lanes): the row's page and
+  // place in it, with UNI those of the wave's 16 rows.  Strides of pages and tokens are
+  // below 2^32 elements.
+  auto row_at = [&](int kb, int pages, int c, uint32_t ps, uint32_t ts) {
+    int f = krow(c), pg;
     if constexpr (UNI) {
-      const int f = __builtin_amdgcn_readfirstlane(krow(c)) & ~15;
-      return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, f) << 32) | (uint32_t)__builtin_amdgcn_readlane(lo, f));
+      f = __builtin_amdgcn_readfirstlane(f) & ~15;
+      pg = __builtin_amdgcn_readlane(pages, f);
     } else {
-      return (int64_t)(((uint64_t)(uint32_t)__shfl(hi, krow(c)) << 32) | (uint32_t)__shfl(lo, krow(c)));
+      pg = __shfl(pages, f);
     }
+    const uint32_t key = (uint32_t)(kb + f), at = pg < 0 ? 0 : key - div_by(key, p.c.page) * p.c.page.d;
+    return (uint64_t)(uint32_t)max(pg, 0) * ps + (uint64_t)at * ts;
   };
-  auto load_k = [&](int64_t at) {
+  auto load_k = [&](int kb, int pages) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      kr[c] = *reinterpret_cast<const u32x4 *>((const char *)(kc + from_lane(at, c)) + koff(c));
+      kr[c] = *reinterpret_cast<const u32x4 *>(
+          (const char *)(kc + row_at(kb, pages, c, (uint32_t)p.c.kp, (uint32_t)p.c.ks)) + koff(c));
   };
-  auto load_v = [&](int64_t at) {
+  auto load_v = [&](int kb, int pages) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      vr[c] = *reinterpret_cast<const u32x4 *>((const char *)(vc + from_lane(at, c)) + voff(c));
+      vr[c] = *reinterpret_cast<const u32x4 *>(
+          (const char *)(vc + row_at(kb, pages, c, (uint32_t)p.c.vp, (uint32_t)p.c.vs)) + voff(c));
   };
   constexpr bool kRagged = kTK * PC % (64 * W) != 0; // some threads have no last piece
   auto store_k = [&](__bf16 *tile) {
@@ -214,22 +212,34 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     return odd;
   };
   // Where the lane reads in a tile: the exchanges have a period of 16 rows (K) and 4 (V) at
-  // most.  The step's place is formed at each read from the first one's (an exclusive or and
-  // an addition): a register for each would leave none for reads ahead.
-  const int kline = col * NP, vline = (4 * half + (lane >> 2 & 3)) * NP + 4 * (lane & 3);
-  int kfirst = KW::at(col, half) - kline;
-  int vfirst = VW::at(4 * half + (lane >> 2 & 3), lane >> 4 & 1) + 4 * (lane & 3) - vline;
+  // most.  The step's place is formed at each read from the first one's: a register for
+  // each would leave none for reads ahead.  Rows of a power of two: one exclusive or, for the
+  // row's own place has no bits there.
+  constexpr bool kPow2 = (NP & (NP - 1)) == 0;
+  const int krow0 = col * NP, vrow0 = (4 * half + (lane >> 2 & 3)) * NP;
+  const int kfirst = KW::at(col, half) - (kPow2 ? 0 : krow0);
+  const int vfirst = VW::at(4 * half + (lane >> 2 & 3), lane >> 4 & 1) + 4 * (lane & 3) - (kPow2 ? 0 : vrow0);
+  auto k_at = [&](int first, int step) { return kPow2 ? first ^ 16 * step : (first ^ 16 * step) + krow0; };
+  auto v_at = [&](int first, int d) { return kPow2 ? first ^ 32 * d : (first ^ 32 * d) + vrow0; };
 
   f32x16 o[DT], s0[KG], s1[KG];
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, top = -INFINITY; // top: the lane's largest score of the tile
   int odd = 0, odd_ever = 0;
+  auto highest_of = [&](const f32x16 *s) {
+    float x = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < KG; ++g)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x = fmaxf(x, s[g][e]);
+    return x;
+  };
   // S^T = K Q^T: the operand of product i, keys 32 (i % KG) and on, step i / KG
   auto key_frag = [&](const __bf16 *tile, int kf, int i) {
-    return *reinterpret_cast<const bf16x8 *>(tile + 32 * (i % KG) * NP + ((kf ^ 16 * (i / KG)) + kline));
+    return *reinterpret_cast<const bf16x8 *>(tile + 32 * (i % KG) * NP + k_at(kf, i / KG));
   };
   f32x16 zero;
 #pragma unroll
@@ -238,8 +248,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   // weights are formed, the scores of t + 1 run on the matrix cores.
   int kb = k0 & ~(kTK - 1);
   uint64_t have0 = 0, have1 = 0; // keys of this tile and of the next that lie on a page
-  int64_t v1 = 0;                // the lane's key of the next tile: its row of V
-  int entry = -1;                // and of the one after that: the table's entry
+  int page1 = -1, entry = -1;    // of the lane's key: of the next tile the page, of the one after that the table's entry
   auto publish_v = [&](int tile_kb, uint64_t have, __bf16 *tile) {
     if (have == kAll && tile_kb >= all0 && tile_kb + kTK <= all1) {
       store_v(tile, 0, false);
@@ -257,17 +266,14 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   for (int x = threadIdx.x; x < kTK * PC; x += 64 * W)
     *reinterpret_cast<u32x4 *>(&vtile[2][8 * x]) = u32x4{0, 0, 0, 0};
   if (kb < k1) {
-    int page = page_of(kb, entry_of(kb));
-    have0 = __builtin_amdgcn_ballot_w64(page >= 0);
-    Where at = where_of(kb, page);
-    load_k(at.k);
-    load_v(at.v);
+    const int page0 = page_of(kb, entry_of(kb));
+    page1 = page_of(kb + kTK, entry_of(kb + kTK));
+    have0 = __builtin_amdgcn_ballot_w64(page0 >= 0);
+    have1 = __builtin_amdgcn_ballot_w64(page1 >= 0);
+    load_k(kb, page0);
+    load_v(kb, page0);
     store_k(ktile[0]);
-    page = page_of(kb + kTK, entry_of(kb + kTK));
-    have1 = __builtin_amdgcn_ballot_w64(page >= 0);
-    at = where_of(kb + kTK, page);
-    load_k(at.k);
-    v1 = at.v;
+    load_k(kb + kTK, page1);
     store_k(ktile[1]);
     entry = entry_of(kb + 2 * kTK);
     publish_v(kb, have0, vtile[0]);
@@ -276,6 +282,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       for (int i = 0; i < KS * KG; ++i)
         s0[i % KG] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(ktile[0], kfirst, i), qf[i / KG],
                                                              i < KG ? zero : s0[i % KG], 0, 0, 0);
+      top = highest_of(s0);
     }
     __syncthreads(); // its place is written again
   }
@@ -285,12 +292,10 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     const uint64_t here = have0;
     have0 = have1;
     if (next < k1) {
-      load_v(v1);
-      const int page = page_of(ahead, entry);
-      have1 = __builtin_amdgcn_ballot_w64(page >= 0);
-      const Where at = where_of(ahead, page);
-      load_k(at.k);
-      v1 = at.v;
+      load_v(next, page1);
+      page1 = page_of(ahead, entry);
+      have1 = __builtin_amdgcn_ballot_w64(page1 >= 0);
+      load_k(ahead, page1);
       entry = entry_of(ahead + kTK);
     }
     if (busy) {
@@ -304,17 +309,13 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
           for (int e = 0; e < 16; ++e)
             if (!(mg & 1u << (e % 4 + 8 * (e / 4)))) s[g][e] = -INFINITY;
         }
+        top = highest_of(s);
       }
-      float top = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < KG; ++g)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[g][e]);
       const Both tops = swap32(top);
-      top = fmaxf(tops.a, tops.b) * p.scale;
+      const float highest = fmaxf(tops.a, tops.b) * p.scale;
       // the weights' reference moves only when some weight would pass 2^8
-      if (__builtin_amdgcn_ballot_w64(top > m + 8.f) != 0) {
-        const float mn = fmaxf(m, top), a = hw_exp2(m - (mn == -INFINITY ? 0.f : mn));
+      if (__builtin_amdgcn_ballot_w64(highest > m + 8.f) != 0) {
+        const float mn = fmaxf(m, highest), a = hw_exp2(m - (mn == -INFINITY ? 0.f : mn));
         l *= a;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= a;
@@ -331,16 +332,27 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       __asm__ volatile("" : "+v"(kf), "+v"(vf));
       auto kfrag = [&](int i) { return key_frag(ktile[1 - P], kf, i); };
       auto vfrag = [&](int j) {
-        const __bf16 *const at = vt + 16 * (j / DT) * NP + ((vf ^ 32 * (j % DT)) + vline);
+        const __bf16 *const at = vt + 16 * (j / DT) * NP + v_at(vf, j % DT);
         const auto tr = [&](int row) {
           return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
               (__attribute__((address_space(3))) lds_bf16x4 *)(at + row * NP)));
         };
         return __builtin_shufflevector(tr(0), tr(8), 0, 1, 2, 3, 4, 5, 6, 7);
       };
-      constexpr int NK = KS * KG, NV = 2 * KG * DT, E = 16 * KG; // products of either kind, weights of a lane
+      // products of either kind, weights of a lane; of these the first E1 between the scores'
+      // products, the rest between those of the sums, before any that takes them
+      constexpr int NK = KS * KG, NV = 2 * KG * DT, E = 16 * KG, E1 = E * 5 / 8, NE = NV - DT;
       bf16x8 ka[AHEAD], va[AHEAD], pf[2 * KG];
       float part[4] = {l, 0.f, 0.f, 0.f};
+      auto weights = [&](int from, int to) {
+#pragma unroll
+        for (int x = from; x < to; ++x) {
+          const float w = hw_exp2(fmaf(s[x / 16][x % 16], p.scale, -base));
+          part[x % 4] += w;
+          // rounded to bf16 for the product (half a step, 2^-8 of each)
+          pf[x / 8][x % 8] = (__bf16)w;
+        }
+      };
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) ka[i] = kfrag(i);
       __builtin_amdgcn_sched_barrier(0);
@@ -349,22 +361,21 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
         sn[i % KG] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ka[i % AHEAD], qf[i / KG], i < KG ? zero : sn[i % KG], 0, 0, 0);
         if (i + AHEAD < NK) ka[i % AHEAD] = kfrag(i + AHEAD);
         else va[i + AHEAD - NK] = vfrag(i + AHEAD - NK);
-#pragma unroll
-        for (int x = i * E / NK; x < (i + 1) * E / NK; ++x) {
-          const float w = hw_exp2(fmaf(s[x / 16][x % 16], p.scale, -base));
-          part[x % 4] += w;
-          // weights rounded to bf16 for the product (half a step, 2^-8 of each)
-          pf[x / 8][x % 8] = (__bf16)w;
-        }
+        weights(i * E1 / NK, (i + 1) * E1 / NK);
         __builtin_amdgcn_sched_barrier(0);
       }
-      l = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         o[j % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[j % AHEAD], pf[j / DT], o[j % DT], 0, 0, 0);
         if (j + AHEAD < NV) va[j % AHEAD] = vfrag(j + AHEAD);
+        if (j < NE) weights(E1 + j * (E - E1) / NE, E1 + (j + 1) * (E - E1) / NE);
+        if (j == NV / 2 - 1) top = -INFINITY;
+        if (j >= NV / 2) // the largest score of the next tile, if all of it is seen
+#pragma unroll
+          for (int x = (j - NV / 2) * E / (NV / 2); x < (j + 1 - NV / 2) * E / (NV / 2); ++x) top = fmaxf(top, sn[x / 16][x % 16]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      l = (part[0] + part[1]) + (part[2] + part[3]);
     }
     if (next < k1) {
       store_k(ktile[P]);

@@ -21,6 +21,7 @@ constexpr int64_t kMaxBatch = (int64_t)1 << 16;
 constexpr int64_t kMaxBatchTokens = (int64_t)1 << 25; // at most as many waves in one launch
 constexpr int64_t kMaxHeads = (int64_t)1 << 16;
 constexpr int64_t kMaxSlot = (int64_t)1 << 24;        // token stride of a page: 16 fp32 rows within 2^31 bytes
+constexpr int64_t kMaxPage = ((int64_t)1 << 32) - 1;   // page stride
 constexpr int64_t kMaxCapacity = (int64_t)1 << 30;    // tokens of a row
 constexpr int64_t kMaxWindow = (int64_t)1 << 33;      // positions stay below 2^31 + 2^24
 constexpr int64_t kMaxUnits = (int64_t)1 << 30;       // of all rows together
@@ -30,8 +31,9 @@ constexpr int64_t kMaxUnits = (int64_t)1 << 30;       // of all rows together
 int check_cache(const ssd_tensor *t, const char *name, int dtype, const int64_t *shape, bool written) {
   SSD_CHECK(check_arg(t, name, dtype, 4, shape, true));
   if (!rows_of(t, 16)) return fail(SSD_ERR_LAYOUT, "%s: rows are not in 16-byte pieces", name);
-  if (t->shape[1] != 1 && t->strides[1] > kMaxSlot)
-    return fail(SSD_ERR_UNSUPPORTED, "%s: stride of dim 1 is %lld", name, (long long)t->strides[1]);
+  for (int d = 0; d < 2; ++d)
+    if (t->shape[d] != 1 && t->strides[d] > (d == 0 ? kMaxPage : kMaxSlot))
+      return fail(SSD_ERR_UNSUPPORTED, "%s: stride of dim %d is %lld", name, d, (long long)t->strides[d]);
   if (written) {
     // strides from the largest: each holds all of what the smaller ones reach
     int dim[3] = {0, 1, 2};
