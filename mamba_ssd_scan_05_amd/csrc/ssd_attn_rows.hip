@@ -128,11 +128,6 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
 
   const __bf16 *const kc = (const __bf16 *)p.c.kc + hk * p.c.kh, *const vc = (const __bf16 *)p.c.vc + hk * p.c.vh;
   const int32_t *const table = p.c.table + pc.i * p.c.tb;
-  // lane l: the table's entry for key kb + l, and the page, -1 for none
-  auto entry_of = [&](int kb) { return table[div_by((uint32_t)min(kb + lane, p.c.capacity - 1), p.c.page)]; };
-  auto page_of = [&](int kb, int entry) {
-    return kb + lane < p.c.capacity && lane < kTK && entry < p.c.pages ? max(entry, -1) : -1;
-  };
   // the thread's pieces of a tile: row and element, places in the LDS tiles, offsets in
   // bytes from the first of 16 rows
   u32x4 kr[CH], vr[CH];
@@ -161,53 +156,81 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   auto koff = [&](int c) { return koff_[kEven ? 0 : c]; };
   auto voff = [&](int c) { return voff_[kEven ? 0 : c]; };
   auto none = [&](int c) { return none_[kEven ? 0 : c]; };
-  // Loads of the tile at kb, whose keys lie on `pages` (of the lanes): the row's page and
-  // place in it, with UNI those of the wave's 16 rows.  Strides of pages and tokens are
-  // below 2^32 elements.
-  auto row_at = [&](int kb, int pages, int c, uint32_t ps, uint32_t ts) {
-    int f = krow(c), pg;
-    if constexpr (UNI) {
-      f = __builtin_amdgcn_readfirstlane(f) & ~15;
-      pg = __builtin_amdgcn_readlane(pages, f);
-    } else {
-      pg = __shfl(pages, f);
-    }
-    const uint32_t key = (uint32_t)(kb + f), at = pg < 0 ? 0 : key - div_by(key, p.c.page) * p.c.page.d;
-    return (uint64_t)(uint32_t)max(pg, 0) * ps + (uint64_t)at * ts;
+  // Where the rows of a tile lie.  UNI: lane l keeps the page and the places of the l-th 16 keys
+  // of a batch of 16 or 32 tiles, found once for the batch; a wave's loads read their group's
+  // from its lane.  Otherwise lane l finds the page of the tile's l-th key, and each row's
+  // place is formed by the lanes that load it.  Strides of pages and tokens are below 2^32.
+  const int kstart = k0 & ~(kTK - 1);
+  constexpr int kBatch = 64 * 16; // keys
+  uint64_t gk = 0, gv = 0, gok = 0;
+  int page_k = -1, entry = -1; // entry: the table's, of the batch (tile) to come
+  auto entry_of = [&](int kb) {
+    return table[div_by((uint32_t)min(kb + (UNI ? 16 : 1) * lane, p.c.capacity - 1), p.c.page)];
   };
-  auto load_k = [&](int kb, int pages) {
+  auto page_of = [&](int kb, int entry) { // of the lane's key
+    return kb + lane < p.c.capacity && lane < kTK && entry < p.c.pages ? max(entry, -1) : -1;
+  };
+  // Before the loads of the tile at kb: its places, and which of its keys lie on a page.
+  auto locate = [&](int kb) {
+    if constexpr (UNI) {
+      if ((kb - kstart) % kBatch == 0) {
+        const uint32_t key = (uint32_t)(kb + 16 * lane), at = key - div_by(key, p.c.page) * p.c.page.d;
+        const bool ok = (int)key < p.c.capacity && entry >= 0 && entry < p.c.pages;
+        gk = ok ? (uint64_t)(uint32_t)entry * (uint32_t)p.c.kp + (uint64_t)at * (uint32_t)p.c.ks : 0;
+        gv = ok ? (uint64_t)(uint32_t)entry * (uint32_t)p.c.vp + (uint64_t)at * (uint32_t)p.c.vs : 0;
+        gok = __builtin_amdgcn_ballot_w64(ok);
+        if (kb + kBatch < k1) entry = entry_of(kb + kBatch);
+      }
+      const uint32_t b = (uint32_t)(gok >> ((kb - kstart) / 16 % 64)) & ((1u << (kTK / 16)) - 1);
+      if (b == (1u << (kTK / 16)) - 1) return kAll;
+      uint64_t have = 0;
+#pragma unroll
+      for (int g = 0; g < kTK / 16; ++g) have |= b >> g & 1 ? 0xFFFFull << (16 * g) : 0;
+      return have;
+    } else {
+      page_k = page_of(kb, entry);
+      entry = entry_of(kb + kTK);
+      return (uint64_t)__builtin_amdgcn_ballot_w64(page_k >= 0);
+    }
+  };
+  auto row_at = [&](int kb, int c, uint64_t group, int pages, uint32_t ps, uint32_t ts) {
+    if constexpr (UNI) {
+      const int f = (kb - kstart) / 16 % 64 + __builtin_amdgcn_readfirstlane(krow(c)) / 16;
+      return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(group >> 32), f) << 32 |
+             (uint32_t)__builtin_amdgcn_readlane((int)group, f);
+    } else {
+      const int f = krow(c), pg = __shfl(pages, f);
+      const uint32_t key = (uint32_t)(kb + f), at = pg < 0 ? 0 : key - div_by(key, p.c.page) * p.c.page.d;
+      return (uint64_t)(uint32_t)max(pg, 0) * ps + (uint64_t)at * ts;
+    }
+  };
+  auto load_k = [&](int kb) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
       kr[c] = *reinterpret_cast<const u32x4 *>(
-          (const char *)(kc + row_at(kb, pages, c, (uint32_t)p.c.kp, (uint32_t)p.c.ks)) + koff(c));
+          (const char *)(kc + row_at(kb, c, gk, page_k, (uint32_t)p.c.kp, (uint32_t)p.c.ks)) + koff(c));
   };
   auto load_v = [&](int kb, int pages) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
       vr[c] = *reinterpret_cast<const u32x4 *>(
-          (const char *)(vc + row_at(kb, pages, c, (uint32_t)p.c.vp, (uint32_t)p.c.vs)) + voff(c));
+          (const char *)(vc + row_at(kb, c, gv, pages, (uint32_t)p.c.vp, (uint32_t)p.c.vs)) + voff(c));
   };
   constexpr bool kRagged = kTK * PC % (64 * W) != 0; // some threads have no last piece
-  auto store_k = [&](__bf16 *tile) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (kRagged && c * 64 * W + (int)threadIdx.x >= kTK * PC) continue;
-      *reinterpret_cast<u32x4 *>(tile + kat(c)) = none(c) ? u32x4{0, 0, 0, 0} : kr[c];
-    }
+  auto store = [&](int c, __bf16 *tile, int at, u32x4 v) {
+    if (!kRagged || c * 64 * W + (int)threadIdx.x < kTK * PC) *reinterpret_cast<u32x4 *>(tile + at) = v;
   };
-  // Rows of V that no query of the workgroup sees are zero in LDS, whatever they held.  True
-  // if another row of an edge tile holds an infinity or a NaN.
-  auto store_v = [&](__bf16 *tile, uint64_t seen, bool edge) {
+  auto store_k = [&](int c, __bf16 *tile) { store(c, tile, kat(c), none(c) ? u32x4{0, 0, 0, 0} : kr[c]); };
+  auto store_v = [&](int c, __bf16 *tile) { store(c, tile, vat(c), vr[c]); };
+  // An edge tile: rows of V that no query of the workgroup sees are zero in LDS, whatever
+  // they held.  True if another row holds an infinity or a NaN.
+  auto clean_v = [&](__bf16 *tile, uint64_t seen) {
     bool odd = false;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (kRagged && c * 64 * W + (int)threadIdx.x >= kTK * PC) continue;
-      u32x4 v = vr[c];
-      if (edge) {
-        if (!(seen >> krow(c) & 1)) v = u32x4{0, 0, 0, 0};
-        odd |= odd_values(v, __bf16());
-      }
-      *reinterpret_cast<u32x4 *>(tile + vat(c)) = v;
+      if (seen >> krow(c) & 1) odd |= odd_values(vr[c], __bf16());
+      else store(c, tile, vat(c), u32x4{0, 0, 0, 0});
     }
     return odd;
   };
@@ -246,16 +269,15 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   for (int e = 0; e < 16; ++e) zero[e] = 0.f;
   // Tile t's V and tile t + 1's K lie in LDS, tile t's scores in registers.  While t's
   // weights are formed, the scores of t + 1 run on the matrix cores.
-  int kb = k0 & ~(kTK - 1);
+  int kb = kstart;
   uint64_t have0 = 0, have1 = 0; // keys of this tile and of the next that lie on a page
-  int page1 = -1, entry = -1;    // of the lane's key: of the next tile the page, of the one after that the table's entry
-  auto publish_v = [&](int tile_kb, uint64_t have, __bf16 *tile) {
+  // behind the stores of a tile
+  auto publish = [&](int tile_kb, uint64_t have, __bf16 *tile) {
     if (have == kAll && tile_kb >= all0 && tile_kb + kTK <= all1) {
-      store_v(tile, 0, false);
       odd = 0;
       __syncthreads();
     } else {
-      odd = __syncthreads_or(store_v(tile, have & bits(k0 - tile_kb, k1 - tile_kb), true));
+      odd = __syncthreads_or(clean_v(tile, have & bits(k0 - tile_kb, k1 - tile_kb)));
       odd_ever |= odd;
     }
   };
@@ -266,17 +288,17 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   for (int x = threadIdx.x; x < kTK * PC; x += 64 * W)
     *reinterpret_cast<u32x4 *>(&vtile[2][8 * x]) = u32x4{0, 0, 0, 0};
   if (kb < k1) {
-    const int page0 = page_of(kb, entry_of(kb));
-    page1 = page_of(kb + kTK, entry_of(kb + kTK));
-    have0 = __builtin_amdgcn_ballot_w64(page0 >= 0);
-    have1 = __builtin_amdgcn_ballot_w64(page1 >= 0);
-    load_k(kb, page0);
-    load_v(kb, page0);
-    store_k(ktile[0]);
-    load_k(kb + kTK, page1);
-    store_k(ktile[1]);
-    entry = entry_of(kb + 2 * kTK);
-    publish_v(kb, have0, vtile[0]);
+    entry = entry_of(kb);
+    have0 = locate(kb);
+    load_k(kb);
+    load_v(kb, page_k);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) store_k(c, ktile[0]), store_v(c, vtile[0]);
+    publish(kb, have0, vtile[0]);
+    have1 = locate(kb + kTK);
+    load_k(kb + kTK);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) store_k(c, ktile[1]);
     if (busy) {
 #pragma unroll
       for (int i = 0; i < KS * KG; ++i)
@@ -292,11 +314,9 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     const uint64_t here = have0;
     have0 = have1;
     if (next < k1) {
-      load_v(next, page1);
-      page1 = page_of(ahead, entry);
-      have1 = __builtin_amdgcn_ballot_w64(page1 >= 0);
-      load_k(ahead, page1);
-      entry = entry_of(ahead + kTK);
+      load_v(next, page_k);
+      have1 = locate(ahead);
+      load_k(ahead);
     }
     if (busy) {
       const bool full = here == kAll && kb >= wall0 && next <= wall1;
@@ -377,10 +397,10 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       }
       l = (part[0] + part[1]) + (part[2] + part[3]);
     }
-    if (next < k1) {
-      store_k(ktile[P]);
-      publish_v(next, have0, vtile[1 - P]);
-    }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) store_k(c, ktile[P]), store_v(c, vtile[1 - P]);
+
+    if (next < k1) publish(next, have0, vtile[1 - P]);
     kb = next;
   };
   while (kb < k1) {
@@ -393,8 +413,8 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   // may not: a product would have carried it to all.  Key by key, from the cache.
   if (odd_ever && busy) {
 #pragma unroll 1
-    for (kb = k0 & ~(kTK - 1); kb < k1; kb += kTK) {
-      const int pages = page_of(kb, entry_of(kb));
+    for (kb = kstart; kb < k1; kb += kTK) {
+      const int pages = page_of(kb, table[div_by((uint32_t)min(kb + lane, p.c.capacity - 1), p.c.page)]);
       const uint64_t have = __builtin_amdgcn_ballot_w64(pages >= 0);
       const uint64_t any = have & bits(k0 - kb, k1 - kb), seen = have & bits(w0 - kb, w1 - kb);
       if (seen == 0 || (any == kAll && kb >= all0 && kb + kTK <= all1)) continue;
