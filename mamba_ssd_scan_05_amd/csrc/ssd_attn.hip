@@ -32,12 +32,14 @@ template <typename T> constexpr int kKT = sizeof(T) == 2 ? 2 : 1; // groups of 1
 
 // Maximum over the four lane groups of a column.
 __device__ __forceinline__ float col_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const Both x = swap16(v);
+  const Both y = swap32(fmaxf(x.a, x.b));
+  return fmaxf(y.a, y.b);
 }
 __device__ __forceinline__ float col_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const Both x = swap16(v);
+  const Both y = swap32(x.a + x.b);
+  return y.a + y.b;
 }
 
 template <typename T> __device__ __forceinline__ typename FragOf<T>::type zero_frag() {
@@ -45,11 +47,22 @@ template <typename T> __device__ __forceinline__ typename FragOf<T>::type zero_f
   return pack8<T>(z);
 }
 
+template <int K> __device__ __forceinline__ void arrived(FragBF (&f)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) __asm__ volatile("" : "+v"(f[k].v));
+}
+template <int K> __device__ __forceinline__ void arrived(FragF32 (&f)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) __asm__ volatile("" : "+v"(f[k].v[e]));
+}
+
 // UNI: the page size is a multiple of 16, so that 16 keys from a multiple of 16 on
 // lie in one page and their page is looked up once, by the scalar unit; otherwise
 // every lane looks up the rows it loads.
 template <typename T, int NP, bool UNI>
-__global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
+__global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnParams p) {
   constexpr int KT = kKT<T>, TK = 16 * KT, ES = sizeof(T);
   constexpr int KK = NP / 32, ND = NP / 16;    // steps of 32 dims, tiles of 16 dims
   constexpr int PC = NP * ES / 16, PI = PC / 4; // 16-byte pieces of a row, loads of 16 rows
@@ -69,10 +82,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
   const int hk = (int)(id % (uint32_t)p.Hk), slot = (int)(id / (uint32_t)p.Hk);
   Piece pc;
   if (!piece_of<kThreads>(p, slot, sh, &pc)) return;
-  pc.i = __builtin_amdgcn_readfirstlane(pc.i);
-  pc.index = __builtin_amdgcn_readfirstlane(pc.index);
-  pc.size = __builtin_amdgcn_readfirstlane(pc.size);
-  const Row row = row_of(p, pc.i);
+  const Row row = pc.row;
   if (p.workers > 1 && pc.index == 0 && hk == 0 && tile == 0 && threadIdx.x == 0)
     p.pieces[pc.i] = make_int2(pc.first, pc.count);
   const int nrows = row.n * p.G, r0 = tile * kRows;
@@ -82,8 +92,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
   const int t_first = (int)div_by((uint32_t)r0, p.group);
   const int t_last = (int)div_by((uint32_t)(min(r0 + kRows, nrows) - 1), p.group);
   const int64_t cap = p.c.capacity;
-  auto last_key = [&](int t) { return (int)min(max(row.start + t + 1, (int64_t)0), cap); };
-  auto first_key = [&](int t) { return p.window ? (int)min(max(row.start + t + 1 - p.window, (int64_t)0), cap) : 0; };
+  auto last_key = [&](int t) { return (int)min(max((int64_t)row.start + t + 1, (int64_t)0), cap); };
+  auto first_key = [&](int t) { return p.window ? (int)min(max((int64_t)row.start + t + 1 - p.window, (int64_t)0), cap) : 0; };
   int k0 = first_key(t_first), k1 = last_key(t_last);
   const int all0 = first_key(t_last), all1 = last_key(t_first); // seen by every query: [all0, all1)
   {
@@ -135,34 +145,57 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
     return *ok ? pg : 0;
   };
   int vrow[PI], vcol[PI]; // of the lane's pieces of 16 rows of V
+  uint32_t voff[PI], koff = (uint32_t)((UNI ? li * p.c.ks : 0) * ES); // offsets from a group's first row, bytes
 #pragma unroll
   for (int i = 0; i < PI; ++i) {
     const int x = i * 64 + lane;
     vrow[i] = x / PC, vcol[i] = x % PC * (16 / ES);
+    voff[i] = (uint32_t)(((UNI ? vrow[i] * p.c.vs : 0) + (vcol[i] < p.N ? vcol[i] : 0)) * ES);
   }
+  // UNI: lane l keeps the places of the l-th 16 keys of a batch of 1024, found once for the
+  // batch, and which of them are on a page; the table's entries for the next one are on
+  // their way.
+  const int kstart = k0 & ~(kWaves * TK - 1);
+  constexpr int kBatch = 64 * 16;
+  uint64_t gk = 0, gv = 0, gok = 0;
+  int entry = -1;
+  auto entry_of = [&](int kb) { return table[div_by((uint32_t)min(kb + 16 * lane, p.c.capacity - 1), p.c.page)]; };
+  auto locate = [&](int kb) { // the batch that begins at kb
+    const uint32_t key = (uint32_t)(kb + 16 * lane), at = key - div_by(key, p.c.page) * p.c.page.d;
+    const bool ok = (int)key < p.c.capacity && entry >= 0 && entry < p.c.pages;
+    gk = ok ? (uint64_t)(uint32_t)entry * (uint32_t)p.c.kp + (uint64_t)at * (uint32_t)p.c.ks : 0;
+    gv = ok ? (uint64_t)(uint32_t)entry * (uint32_t)p.c.vp + (uint64_t)at * (uint32_t)p.c.vs : 0;
+    gok = __builtin_amdgcn_ballot_w64(ok);
+    if (kb + kBatch < k1) entry = entry_of(kb + kBatch);
+  };
+  auto of_group = [](uint64_t x, int f) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), f) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)x, f);
+  };
   Frag kf[KT][KK];
   u32x4 vr[KT * PI];
   uint32_t have_k = 0, have_v = 0; // keys of the tile that lie on a page, one bit each
   auto load_k = [&](int kb) {
+    if (UNI && (kb - kstart) % kBatch < kWaves * TK) locate(kb - (kb - kstart) % kBatch);
     have_k = 0;
 #pragma unroll
     for (int g = 0; g < KT; ++g) {
-      bool ok;
-      int at;
       const T *src;
       if constexpr (UNI) {
-        const int pg = lookup(kb + 16 * g, &ok, &at);
-        src = kc + pg * p.c.kp + at * p.c.ks + li * p.c.ks;
-        if (ok) have_k |= 0xFFFFu << (16 * g);
+        const int f = (kb - kstart) / 16 % 64 + g;
+        src = kc + of_group(gk, f);
+        if (gok >> f & 1) have_k |= 0xFFFFu << (16 * g);
       } else {
+        bool ok;
+        int at;
         const int pg = lookup(kb + 16 * g + li, &ok, &at);
-        src = kc + pg * p.c.kp + at * p.c.ks;
+        src = kc + (uint64_t)(uint32_t)pg * (uint32_t)p.c.kp + (uint64_t)(uint32_t)at * (uint32_t)p.c.ks;
         have_k |= (uint32_t)(__builtin_amdgcn_ballot_w64(ok) & 0xFFFFu) << (16 * g);
       }
 #pragma unroll
       for (int k = 0; k < KK; ++k) {
         const int d = 32 * k + 8 * lg;
-        if (d < p.N) load_frag(kf[g][k], src + d);
+        if (d < p.N) load_frag(kf[g][k], (const T *)((const char *)src + koff) + d);
         else kf[g][k] = zero_frag<T>();
       }
     }
@@ -170,14 +203,17 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
   auto load_v = [&](int kb) {
 #pragma unroll
     for (int g = 0; g < KT; ++g) {
-      bool ok;
-      int at, pg = 0;
-      if constexpr (UNI) pg = lookup(kb + 16 * g, &ok, &at);
+      uint64_t base = 0;
+      if constexpr (UNI) base = of_group(gv, (kb - kstart) / 16 % 64 + g);
 #pragma unroll
       for (int i = 0; i < PI; ++i) {
-        if constexpr (!UNI) pg = lookup(kb + 16 * g + vrow[i], &ok, &at);
-        const T *src = vc + pg * p.c.vp + at * p.c.vs + (UNI ? vrow[i] * p.c.vs : 0);
-        vr[g * PI + i] = *reinterpret_cast<const u32x4 *>(src + (vcol[i] < p.N ? vcol[i] : 0));
+        if constexpr (!UNI) {
+          bool ok;
+          int at;
+          const int pg = lookup(kb + 16 * g + vrow[i], &ok, &at);
+          base = (uint64_t)(uint32_t)pg * (uint32_t)p.c.vp + (uint64_t)(uint32_t)at * (uint32_t)p.c.vs;
+        }
+        vr[g * PI + i] = *reinterpret_cast<const u32x4 *>((const char *)(vc + base) + voff[i]);
       }
     }
   };
@@ -186,9 +222,17 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
 #pragma unroll
   for (int d = 0; d < ND; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
+  bool left_out = false; // this wave left products out
   T *const vt = reinterpret_cast<T *>(lds + wave * kTile);
-  int kb = (k0 & ~(TK - 1)) + wave * TK;
-  if (kb < k1) load_k(kb), load_v(kb);
+  int kb = kstart + wave * TK;
+  if (kb < k1) {
+    if constexpr (UNI) entry = entry_of(kstart);
+    load_k(kb);
+    load_v(kb);
+  }
+  // The queries are there from here on: as loads still on their way they would be waited
+  // for in every round, and with them the next tile's.
+  arrived(qf);
   for (; kb < k1; kb += kWaves * TK) {
     const int next = kb + kWaves * TK;
     // S^T = K Q^T
@@ -202,7 +246,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
     have_v = have_k;
     if (next < k1) load_k(next);
     // the keys of the tile that any query of the workgroup sees, and whether all see them all
-    const uint32_t lo_bits = k0 > kb ? ~0u << min(k0 - kb, 31) : ~0u;
+    const uint32_t lo_bits = k0 - kb >= 32 ? 0u : k0 > kb ? ~0u << (k0 - kb) : ~0u;
     const uint32_t hi_bits = k1 - kb < 32 ? (1u << (k1 - kb)) - 1 : ~0u;
     const uint32_t seen = have_v & lo_bits & hi_bits;
     const bool full = seen == (TK == 32 ? ~0u : 0xFFFFu) && kb >= all0 && kb + TK <= all1;
@@ -253,27 +297,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
       }
     if (next < k1) load_v(next);
     if (!full && __builtin_amdgcn_ballot_w64(odd) != 0) {
-      // an infinity or a NaN in a value that some queries see and others may not (a
-      // product would carry it to all): key by key
-      for (int j = 0; j < TK; ++j) {
-        const int from = li + 16 * (j % 16 / 4);
-        float pj = 0.f;
-#pragma unroll
-        for (int g = 0; g < KT; ++g)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = __shfl(w[4 * g + e], from);
-            if (j / 16 == g && j % 4 == e) pj = x;
-          }
-        const bool see = (seen >> j & 1) && kb + j >= q0 && kb + j < q1;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          const T *v = vt + SW::at(j, d) + 4 * lg;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (see) o[d][e] = fmaf(pj, to_f(v[e]), o[d][e]);
-        }
-      }
+      left_out = true; // added behind the loop
     } else if constexpr (ES == 2) {
       // O^T += V^T P^T; P rounded to bf16: half a step of it, 2^-8 of each weight, less
       // than the output's own rounding where values of one size are averaged
@@ -298,6 +322,54 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
     }
   }
 
+  // The tiles with an infinity or a NaN in a value that some queries see and others may not:
+  // a product would have carried it to all.  Key by key, from the cache.
+  if (left_out) {
+#pragma unroll 1
+    for (kb = kstart + wave * TK; kb < k1; kb += kWaves * TK) {
+      bool ok;
+      int at;
+      const int pg = lookup(kb + lane, &ok, &at);
+      const uint32_t seen = (uint32_t)__builtin_amdgcn_ballot_w64(ok && kb + lane >= k0 && kb + lane < k1 && lane < TK);
+      if (seen == (TK == 32 ? ~0u : 0xFFFFu) && kb >= all0 && kb + TK <= all1) continue;
+      const uint64_t krow = (uint64_t)pg * p.c.kp + (uint64_t)at * p.c.ks, vrow1 = (uint64_t)pg * p.c.vp + (uint64_t)at * p.c.vs;
+      auto of_lane = [&](uint64_t x, int j) {
+        return (uint64_t)(uint32_t)__shfl((int)(x >> 32), j) << 32 | (uint32_t)__shfl((int)x, j);
+      };
+      bool odd = false;
+#pragma unroll 1
+      for (int x = lane; x < TK * PC; x += 64) {
+        const int j = x / PC, d = x % PC * (16 / ES);
+        const T *v = vc + of_lane(vrow1, j) + d;
+        if (d < p.N && (seen >> j & 1)) odd |= odd_values(*reinterpret_cast<const u32x4 *>(v), T());
+      }
+      if (__builtin_amdgcn_ballot_w64(odd) == 0) continue;
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+      for (uint32_t left = seen; left; left &= left - 1) {
+        const int j = __builtin_ctz(left);
+        const T *ks = kc + of_lane(krow, j), *vs = vc + of_lane(vrow1, j);
+        float sj = 0.f;
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+          const int d = 32 * k + 8 * lg;
+          if (d >= p.N) continue;
+          Frag a;
+          load_frag(a, ks + d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sj = fmaf(elem(a, e), elem(qf[k], e), sj);
+        }
+        const float w = hw_exp2(fmaf(col_sum(sj), p.scale, -base));
+        if (kb + j < q0 || kb + j >= q1) continue;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * d + 4 * lg < p.N) o[d][e] = fmaf(w, to_f(vs[16 * d + 4 * lg + e]), o[d][e]);
+      }
+    }
+  }
+
   // join the waves
   l = col_sum(l);
   __syncthreads();
@@ -307,7 +379,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnParams p) {
   if (lg == 0) ml[wave][li] = make_float2(m, l);
   __syncthreads();
   const bool whole = pc.count == 1;
-  const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * kRows;
+  const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * p.prow;
   for (int x = threadIdx.x; x < 16 * (NP / 4); x += kThreads) {
     const int q = x / (NP / 4), c = x % (NP / 4) * 4;
     if (r0 + q >= nrows || c >= p.N) continue;
@@ -350,8 +422,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void attn_join_kern
   const int2 pc = p.pieces[i];
   if (pc.y <= 1) return;
   const int hk = (int)div_by((uint32_t)h, p.group), r = t * p.G + h - hk * p.G;
-  const int64_t step = (int64_t)p.Hk * p.tiles * p.rows;
-  const int64_t first = ((int64_t)pc.x * p.Hk + hk) * p.tiles * p.rows + r;
+  const int64_t step = (int64_t)p.Hk * p.tiles * p.prow;
+  const int64_t first = ((int64_t)pc.x * p.Hk + hk) * p.tiles * p.prow + r;
   const int tid = threadIdx.x;
   float top = -INFINITY;
   for (int c = tid; c < pc.y; c += kThreads) top = fmaxf(top, p.part_ml[first + c * step].x);
@@ -416,20 +488,25 @@ constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
 
 int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t vecs = (int64_t)p->L * p->G;
-  p->rows = dtype == 1 && vecs > 64 ? attn_rows(p->N) : kRows;
-  const int64_t target = p->rows == kRows ? 1024 : 512; // workgroups that fill the device
+  const bool wide = dtype == 1 && vecs > 64;
+  p->rows = wide ? attn_rows(p->N) : kRows;
   const int64_t tiles = (vecs + p->rows - 1) / p->rows, heads = p->Hk * tiles;
   p->tiles = (int)tiles;
-  p->workers = heads * p->b >= (p->rows == kRows ? 8 : 1) * target ? 1 : (int)((target + heads - 1) / heads);
+  const int64_t prefer = wide ? 512 : p->N <= 128 ? 1024 : 512, most = wide ? 512 : 4096;
+  p->workers = heads * p->b >= (wide ? 512 : 8192) ? 1 : (int)((most + heads - 1) / heads);
+  p->prefer = (int)((prefer + heads - 1) / heads);
+  p->enough = (int)((1 << 20) / (2 * kAttnUnit * p->N * (dtype == 1 ? 2 : 4)));
+  if (p->enough < 2) p->enough = 2;
   p->slots = p->workers == 1 ? p->b : p->workers + p->b;
+  p->prow = (int)(vecs < p->rows ? vecs : p->rows);
   if (p->slots * heads > kMaxGroups) return -1;
   if (p->workers == 1) return 0;
-  const int64_t rows = p->slots * heads * p->rows;
+  const int64_t rows = p->slots * heads * p->prow;
   return up256(rows * p->N * 4) + up256(rows * 8) + up256((int64_t)p->b * 8);
 }
 
 void attn_workspace(AttnParams *p, void *workspace) {
-  const int64_t rows = (int64_t)p->slots * p->Hk * p->tiles * p->rows;
+  const int64_t rows = (int64_t)p->slots * p->Hk * p->tiles * p->prow;
   char *w = (char *)workspace;
   p->part = (float *)w;
   p->part_ml = (float2 *)(w + up256(rows * p->N * 4));

@@ -21,8 +21,7 @@ __device__ __forceinline__ int wave_incl_scan_i(int v) {
 // A row of the batch: how many new tokens it has, where the first one stands and
 // the keys that any of them sees, [lo, hi).
 struct Row {
-  int n, lo, hi;
-  int64_t start;
+  int n, lo, hi, start;
   // kAttnUnit-key units from lo, rounded down to a unit, to hi; a row with tokens
   // but no keys has one, in which nothing is seen
   __device__ __forceinline__ int units() const {
@@ -36,8 +35,8 @@ __device__ __forceinline__ Row row_of(const AttnParams &p, int i) {
   r.start = p.c.start[i];
   r.n = p.c.tokens ? min(max(p.c.tokens[i], 0), p.L) : p.L;
   const int64_t cap = p.c.capacity;
-  const int64_t hi = min(max(r.start + r.n, (int64_t)0), cap);
-  const int64_t lo = p.window ? min(max(r.start + 1 - p.window, (int64_t)0), hi) : 0;
+  const int64_t hi = min(max((int64_t)r.start + r.n, (int64_t)0), cap);
+  const int64_t lo = p.window ? min(max((int64_t)r.start + 1 - p.window, (int64_t)0), hi) : 0;
   r.lo = (int)lo, r.hi = (int)hi;
   return r;
 }
@@ -45,29 +44,39 @@ __device__ __forceinline__ Row row_of(const AttnParams &p, int i) {
 // A piece: keys [k0, k1) of row i, its `index`th of `count`.
 struct Piece {
   int i, index, count, first, size; // first: the row's first piece; size: units of a piece
+  Row row;
 };
 // sh: 11 words of LDS.  The plan, the same in every workgroup: all rows' lengths together are cut into
 // about p.workers pieces of equal size, so that a batch of one long row and many
 // short ones keeps the device as busy as an even one.  Piece `slot` of that list.
 // The sum of the units stays below 2^31 (checked on the host).
+__device__ __forceinline__ int piece_units(const AttnParams &p, int total) {
+  const int least = (total + p.workers - 1) / p.workers;
+  return max(max(least, min((total + p.prefer - 1) / p.prefer, p.enough)), 2);
+}
 template <int THREADS>
 __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh, Piece *pc) {
   if (p.workers == 1) {
-    *pc = Piece{slot, 0, 1, slot, INT32_MAX};
-    return slot < p.b;
+    *pc = Piece{slot, 0, 1, slot, INT32_MAX, row_of(p, slot)}; // slots = b
+    return true;
   }
   const int tid = threadIdx.x, lane = tid & 63;
-  constexpr int kMinUnits = 4;
   if (p.b <= 64) { // every wave by itself
-    const int u = lane < p.b ? row_of(p, lane).units() : 0;
+    Row row{};
+    if (lane < p.b) row = row_of(p, lane);
+    const int u = row.units();
     const int total = __builtin_amdgcn_readlane(wave_incl_scan_i(u), 63);
-    const int size = max((total + p.workers - 1) / p.workers, kMinUnits);
+    const int size = piece_units(p, total);
     const int cnt = (u + size - 1) / size, end = wave_incl_scan_i(cnt);
     const uint64_t m = __builtin_amdgcn_ballot_w64(end > slot);
     if (m == 0) return false;
     const int i = (int)__builtin_ctzll(m);
     const int c = __builtin_amdgcn_readlane(cnt, i), f = __builtin_amdgcn_readlane(end, i) - c;
-    *pc = Piece{i, slot - f, c, f, size};
+    *pc = Piece{i, slot - f, c, f, size, row};
+    pc->row.n = __builtin_amdgcn_readlane(row.n, i);
+    pc->row.lo = __builtin_amdgcn_readlane(row.lo, i);
+    pc->row.hi = __builtin_amdgcn_readlane(row.hi, i);
+    pc->row.start = __builtin_amdgcn_readlane(row.start, i);
     return true;
   }
   // each thread a run of rows
@@ -80,7 +89,7 @@ __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh,
   int total = 0;
   for (int w = 0; w < THREADS / 64; ++w) total += sh[w];
   __syncthreads();
-  const int size = max((total + p.workers - 1) / p.workers, kMinUnits);
+  const int size = piece_units(p, total);
   int cnt = 0;
   for (int i = i0; i < i1; ++i) cnt += (row_of(p, i).units() + size - 1) / size;
   const int incl = wave_incl_scan_i(cnt);
@@ -99,10 +108,12 @@ __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh,
       before += c;
     }
   __syncthreads();
-  const int i = sh[8], f = sh[9], c = sh[10];
+  const int i = __builtin_amdgcn_readfirstlane(sh[8]), f = __builtin_amdgcn_readfirstlane(sh[9]),
+            c = __builtin_amdgcn_readfirstlane(sh[10]);
   __syncthreads();
-  *pc = Piece{i, slot - f, c, f, size};
-  return i >= 0;
+  if (i < 0) return false;
+  *pc = Piece{i, slot - f, c, f, __builtin_amdgcn_readfirstlane(size), row_of(p, i)};
+  return true;
 }
 
 // A V tile of a wave in LDS: 16-byte pieces of its rows as they come, but the

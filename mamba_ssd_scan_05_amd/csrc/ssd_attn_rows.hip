@@ -73,10 +73,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   const int hk = (int)(id % (uint32_t)p.Hk), slot = (int)(id / (uint32_t)p.Hk);
   Piece pc;
   if (!piece_of<64 * W>(p, slot, sh, &pc)) return;
-  pc.i = __builtin_amdgcn_readfirstlane(pc.i);
-  pc.index = __builtin_amdgcn_readfirstlane(pc.index);
-  pc.size = __builtin_amdgcn_readfirstlane(pc.size);
-  const Row row = row_of(p, pc.i);
+  const Row row = pc.row;
   if (p.workers > 1 && pc.index == 0 && hk == 0 && tile == 0 && threadIdx.x == 0)
     p.pieces[pc.i] = make_int2(pc.first, pc.count);
   const int nrows = row.n * p.G, r0 = tile * kRows;
@@ -84,8 +81,8 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
 
   const int64_t cap = p.c.capacity;
   auto token = [&](int r) { return (int)div_by((uint32_t)r, p.group); };
-  auto last_key = [&](int t) { return (int)min(max(row.start + t + 1, (int64_t)0), cap); };
-  auto first_key = [&](int t) { return p.window ? (int)min(max(row.start + t + 1 - p.window, (int64_t)0), cap) : 0; };
+  auto last_key = [&](int t) { return (int)min(max((int64_t)row.start + t + 1, (int64_t)0), cap); };
+  auto first_key = [&](int t) { return p.window ? (int)min(max((int64_t)row.start + t + 1 - p.window, (int64_t)0), cap) : 0; };
   const int64_t base_key = (int64_t)(row.lo / kAttnUnit) * kAttnUnit, size = (int64_t)pc.size * kAttnUnit;
   const int64_t piece0 = base_key + pc.index * size, piece1 = piece0 + size;
   auto from = [&](int t) { return (int)max((int64_t)first_key(t), piece0); };
@@ -281,10 +278,6 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       odd_ever |= odd;
     }
   };
-  // The queries are there from here on: as loads still on their way they would be waited for
-  // at the first product of every tile, and with them the loads of the tile to come.
-#pragma unroll
-  for (int k = 0; k < KS; ++k) __asm__ volatile("" : "+v"(qf[k]));
   for (int x = threadIdx.x; x < kTK * PC; x += 64 * W)
     *reinterpret_cast<u32x4 *>(&vtile[2][8 * x]) = u32x4{0, 0, 0, 0};
   if (kb < k1) {
@@ -292,6 +285,10 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
     have0 = locate(kb);
     load_k(kb);
     load_v(kb, page_k);
+    // The queries are there from here on: as loads still on their way they would be waited for
+    // at the first product of every tile, and with them the loads of the tile to come.
+#pragma unroll
+    for (int k = 0; k < KS; ++k) __asm__ volatile("" : "+v"(qf[k]));
 #pragma unroll
     for (int c = 0; c < CH; ++c) store_k(c, ktile[0]), store_v(c, vtile[0]);
     publish(kb, have0, vtile[0]);
@@ -479,7 +476,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       }
     if (p.lse && half == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + hw_log2(l)) * kLn2;
   } else {
-    const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * kRows + r - r0;
+    const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * p.prow + r - r0;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll

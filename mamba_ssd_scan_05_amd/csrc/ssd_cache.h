@@ -73,11 +73,13 @@ struct AttnParams {
   int b, L, Hq, Hk, G, N;
   FastDiv group;                    // G
   // set by attn_plan
-  int workers;                      // pieces that the rows' lengths are cut into, over all rows; 1: one piece a row
+  int workers;                      // pieces of all rows' lengths together, at most; 1: one piece a row
+  int prefer, enough;               // as many, but no larger than `enough` units, if workers allows
   int slots;                        // pieces at most
   int rows, tiles;                  // query vectors of a tile, tiles of a row and key head
-  float *part;                      // [slots, Hk, tiles, rows, N], products' sums
-  float2 *part_ml;                  // [slots, Hk, tiles, rows], maximum and sum
+  int prow;                         // query vectors of a tile that may be there
+  float *part;                      // [slots, Hk, tiles, prow, N], products' sums
+  float2 *part_ml;                  // [slots, Hk, tiles, prow], maximum and sum
   int2 *pieces;                     // [b]: a row's first piece and how many
 };
 // Fills workers, slots, rows and tiles; workspace bytes, -1 if the call is too large.
