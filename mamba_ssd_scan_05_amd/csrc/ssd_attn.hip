@@ -76,10 +76,8 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
 
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint32_t id = blockIdx.x;
-  const int tile = (int)(id % (uint32_t)p.tiles);
-  id /= (uint32_t)p.tiles;
-  const int hk = (int)(id % (uint32_t)p.Hk), slot = (int)(id / (uint32_t)p.Hk);
+  int tile, hk, slot;
+  place_of(p, blockIdx.x, &tile, &hk, &slot);
   Piece pc;
   if (!piece_of<kThreads>(p, slot, sh, &pc)) return;
   const Row row = pc.row;
@@ -97,7 +95,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   int k0 = first_key(t_first), k1 = last_key(t_last);
   const int all0 = first_key(t_last), all1 = last_key(t_first); // seen by every query: [all0, all1)
   {
-    const int64_t base = (int64_t)(row.lo / kAttnUnit) * kAttnUnit, size = (int64_t)pc.size * kAttnUnit;
+    const int64_t base = (int64_t)(row.lo / kAttnUnit) * kAttnUnit, size = (int64_t)pc.size() * kAttnUnit;
     const int64_t a = base + pc.index * size;
     k0 = (int)max((int64_t)k0, a);
     k1 = (int)min((int64_t)k1, a + size);
@@ -488,11 +486,11 @@ constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
 
 int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t vecs = (int64_t)p->L * p->G;
-  const bool wide = dtype == 1 && vecs > 64;
+  const bool wide = dtype == 1 && vecs > kRows;
   p->rows = wide ? attn_rows(p->N) : kRows;
   const int64_t tiles = (vecs + p->rows - 1) / p->rows, heads = p->Hk * tiles;
   p->tiles = (int)tiles;
-  const int64_t prefer = wide ? 512 : p->N <= 128 ? 1024 : 512, most = wide ? 512 : 4096;
+  const int64_t prefer = wide ? 512 : p->N <= 128 ? 512 : 256, most = wide ? 512 : 4096;
   p->workers = heads * p->b >= (wide ? 512 : 8192) ? 1 : (int)((most + heads - 1) / heads);
   p->prefer = (int)((prefer + heads - 1) / heads);
   p->enough = (int)((1 << 20) / (2 * kAttnUnit * p->N * (dtype == 1 ? 2 : 4)));
@@ -503,6 +501,21 @@ int64_t attn_plan(AttnParams *p, int dtype) {
   if (p->workers == 1) return 0;
   const int64_t rows = p->slots * heads * p->prow;
   return up256(rows * p->N * 4) + up256(rows * 8) + up256((int64_t)p->b * 8);
+}
+
+// Pieces that there can be with this table and window: a row has no more units than its
+// table or its window and new tokens, and a piece no fewer than piece_units gives it.
+// (Workgroups without a piece cost their launch, behind all others: 3700 of them 12 us.)
+void attn_slots(AttnParams *p) {
+  if (p->workers == 1) return;
+  int64_t keys = p->c.capacity;
+  if (p->window && p->window + p->L < keys) keys = p->window + p->L;
+  const int64_t total = (int64_t)p->b * ((keys + kAttnUnit - 1) / kAttnUnit + 1);
+  int64_t n = (total + p->enough - 1) / p->enough;
+  if (n < p->prefer) n = p->prefer;
+  if (n > (total + 1) / 2) n = (total + 1) / 2;
+  if (n > p->workers) n = p->workers;
+  p->slots = (int)n + p->b;
 }
 
 void attn_workspace(AttnParams *p, void *workspace) {

@@ -18,6 +18,20 @@ __device__ __forceinline__ int wave_incl_scan_i(int v) {
   return v;
 }
 
+// What workgroup `id` does: a tile of the query vectors of a key head of a piece.  The
+// tiles of a piece and head read the same keys: they go to one XCD (workgroups are dealt to
+// the eight in turn) where that gives each the same number of them (bf16 prompt b4 L4096
+// 1320 -> 924 us at the time, its 8 MB of keys and values a head more than an L2 holds); the
+// longest ones first.
+__device__ __forceinline__ void place_of(const AttnParams &p, uint32_t id, int *tile, int *hk, int *slot) {
+  const bool deal = p.tiles > 1 && (uint32_t)p.slots * (uint32_t)p.Hk % 8 == 0;
+  const uint32_t n = deal ? id >> 3 : id, group = n / (uint32_t)p.tiles;
+  *tile = p.tiles - 1 - (int)(n - group * (uint32_t)p.tiles);
+  const uint32_t g = deal ? group * 8 + (id & 7) : group;
+  *slot = (int)(g / (uint32_t)p.Hk);
+  *hk = (int)(g - (uint32_t)*slot * (uint32_t)p.Hk);
+}
+
 // A row of the batch: how many new tokens it has, where the first one stands and
 // the keys that any of them sees, [lo, hi).
 struct Row {
@@ -41,10 +55,12 @@ __device__ __forceinline__ Row row_of(const AttnParams &p, int i) {
   return r;
 }
 
-// A piece: keys [k0, k1) of row i, its `index`th of `count`.
+// A piece: the `index`th of `count` of row i.
 struct Piece {
-  int i, index, count, first, size; // first: the row's first piece; size: units of a piece
+  int i, index, count, first; // first: the row's first piece
   Row row;
+  // units of each of the row's pieces
+  __device__ __forceinline__ int size() const { return count == 1 ? INT32_MAX : (row.units() + count - 1) / count; }
 };
 // sh: 11 words of LDS.  The plan, the same in every workgroup: all rows' lengths together are cut into
 // about p.workers pieces of equal size, so that a batch of one long row and many
@@ -54,10 +70,14 @@ __device__ __forceinline__ int piece_units(const AttnParams &p, int total) {
   const int least = (total + p.workers - 1) / p.workers;
   return max(max(least, min((total + p.prefer - 1) / p.prefer, p.enough)), 2);
 }
+// Pieces of a row of u units: a rest of up to a quarter of a piece is spread over the others.
+__device__ __forceinline__ int pieces_of(int u, int size) {
+  return u == 0 ? 0 : max((u + size - 1 - size / 4) / size, 1);
+}
 template <int THREADS>
 __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh, Piece *pc) {
   if (p.workers == 1) {
-    *pc = Piece{slot, 0, 1, slot, INT32_MAX, row_of(p, slot)}; // slots = b
+    *pc = Piece{slot, 0, 1, slot, row_of(p, slot)}; // slots = b
     return true;
   }
   const int tid = threadIdx.x, lane = tid & 63;
@@ -67,12 +87,12 @@ __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh,
     const int u = row.units();
     const int total = __builtin_amdgcn_readlane(wave_incl_scan_i(u), 63);
     const int size = piece_units(p, total);
-    const int cnt = (u + size - 1) / size, end = wave_incl_scan_i(cnt);
+    const int cnt = pieces_of(u, size), end = wave_incl_scan_i(cnt);
     const uint64_t m = __builtin_amdgcn_ballot_w64(end > slot);
     if (m == 0) return false;
     const int i = (int)__builtin_ctzll(m);
     const int c = __builtin_amdgcn_readlane(cnt, i), f = __builtin_amdgcn_readlane(end, i) - c;
-    *pc = Piece{i, slot - f, c, f, size, row};
+    *pc = Piece{i, slot - f, c, f, row};
     pc->row.n = __builtin_amdgcn_readlane(row.n, i);
     pc->row.lo = __builtin_amdgcn_readlane(row.lo, i);
     pc->row.hi = __builtin_amdgcn_readlane(row.hi, i);
@@ -91,7 +111,7 @@ __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh,
   __syncthreads();
   const int size = piece_units(p, total);
   int cnt = 0;
-  for (int i = i0; i < i1; ++i) cnt += (row_of(p, i).units() + size - 1) / size;
+  for (int i = i0; i < i1; ++i) cnt += pieces_of(row_of(p, i).units(), size);
   const int incl = wave_incl_scan_i(cnt);
   if (lane == 63) sh[tid >> 6] = incl;
   if (tid == 0) sh[8] = -1;
@@ -100,7 +120,7 @@ __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh,
   for (int w = 0; w < (tid >> 6); ++w) before += sh[w];
   if (slot >= before && slot < before + cnt)
     for (int i = i0; i < i1; ++i) {
-      const int c = (row_of(p, i).units() + size - 1) / size;
+      const int c = pieces_of(row_of(p, i).units(), size);
       if (slot < before + c) {
         sh[8] = i, sh[9] = before, sh[10] = c;
         break;
@@ -112,7 +132,7 @@ __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh,
             c = __builtin_amdgcn_readfirstlane(sh[10]);
   __syncthreads();
   if (i < 0) return false;
-  *pc = Piece{i, slot - f, c, f, __builtin_amdgcn_readfirstlane(size), row_of(p, i)};
+  *pc = Piece{i, slot - f, c, f, row_of(p, i)};
   return true;
 }
 

@@ -62,15 +62,8 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
 
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // The tiles of a row and key head read the same keys: they go to one XCD (workgroups
-  // are dealt to the eight in turn) where that gives each the same number of them;
-  // the longest ones first.
-  uint32_t id = blockIdx.x;
-  const bool deal = (uint32_t)p.slots * (uint32_t)p.Hk % 8 == 0;
-  const uint32_t n = deal ? id >> 3 : id, group = n / (uint32_t)p.tiles;
-  const int tile = p.tiles - 1 - (int)(n - group * (uint32_t)p.tiles);
-  id = deal ? group * 8 + (id & 7) : group;
-  const int hk = (int)(id % (uint32_t)p.Hk), slot = (int)(id / (uint32_t)p.Hk);
+  int tile, hk, slot;
+  place_of(p, blockIdx.x, &tile, &hk, &slot);
   Piece pc;
   if (!piece_of<64 * W>(p, slot, sh, &pc)) return;
   const Row row = pc.row;
@@ -83,7 +76,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   auto token = [&](int r) { return (int)div_by((uint32_t)r, p.group); };
   auto last_key = [&](int t) { return (int)min(max((int64_t)row.start + t + 1, (int64_t)0), cap); };
   auto first_key = [&](int t) { return p.window ? (int)min(max((int64_t)row.start + t + 1 - p.window, (int64_t)0), cap) : 0; };
-  const int64_t base_key = (int64_t)(row.lo / kAttnUnit) * kAttnUnit, size = (int64_t)pc.size * kAttnUnit;
+  const int64_t base_key = (int64_t)(row.lo / kAttnUnit) * kAttnUnit, size = (int64_t)pc.size() * kAttnUnit;
   const int64_t piece0 = base_key + pc.index * size, piece1 = piece0 + size;
   auto from = [&](int t) { return (int)max((int64_t)first_key(t), piece0); };
   auto to = [&](int t) { return (int)min((int64_t)last_key(t), piece1); };

@@ -87,6 +87,8 @@ int64_t attn_plan(AttnParams *p, int dtype);
 // Many query vectors of a row and key head, bf16 (ssd_attn_rows.hip); query vectors of its tile.
 int attn_rows(int N);
 hipError_t launch_attn_rows(const AttnParams &p, hipStream_t stream);
+// Fewer slots where the cache (c, window) has no room for more pieces.
+void attn_slots(AttnParams *p);
 void attn_workspace(AttnParams *p, void *workspace);
 hipError_t launch_attn(int dtype, const AttnParams &p, hipStream_t stream);
 } // namespace ssd

@@ -207,6 +207,7 @@ int attn(const ssd_tensor *q, const ssd_tensor *k_cache, const ssd_tensor *v_cac
   p.scale = fabsf(scale) * 1.4426950408889634f;
   p.negate = scale < 0.f;
   p.window = window < kMaxWindow ? window : 0; // one that reaches past every position is none
+  attn_slots(&p);
   if (need) attn_workspace(&p, workspace);
   const hipError_t e = launch_attn(q->dtype, p, (hipStream_t)stream);
   return e == hipSuccess ? SSD_OK : hip_fail(e, "attention launch");
