@@ -150,46 +150,48 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
     vrow[i] = x / PC, vcol[i] = x % PC * (16 / ES);
     voff[i] = (uint32_t)(((UNI ? vrow[i] * p.c.vs : 0) + (vcol[i] < p.N ? vcol[i] : 0)) * ES);
   }
-  // UNI: lane l keeps the places of the l-th 16 keys of a batch of 1024, found once for the
-  // batch, and which of them are on a page; the table's entries for the next one are on
-  // their way.
+  // Where the keys lie.  UNI: lane l keeps the places of the l-th 16 keys of a batch of 1024,
+  // found once for the batch.  Otherwise lane l keeps those of the tile's l-th key.  The
+  // table's entries for the next batch or tile are on their way.
   const int kstart = k0 & ~(kWaves * TK - 1);
   constexpr int kBatch = 64 * 16;
-  uint64_t gk = 0, gv = 0, gok = 0;
+  uint64_t gk = 0, gv = 0, gok = 0; // gok: the lanes whose key is on a page
   int entry = -1;
-  auto entry_of = [&](int kb) { return table[div_by((uint32_t)min(kb + 16 * lane, p.c.capacity - 1), p.c.page)]; };
-  auto locate = [&](int kb) { // the batch that begins at kb
-    const uint32_t key = (uint32_t)(kb + 16 * lane), at = key - div_by(key, p.c.page) * p.c.page.d;
+  auto entry_of = [&](int kb) {
+    return table[div_by((uint32_t)min(kb + (UNI ? 16 : 1) * lane, p.c.capacity - 1), p.c.page)];
+  };
+  auto locate = [&](int kb, int next) { // the batch or tile at kb; the one behind it
+    const uint32_t key = (uint32_t)(kb + (UNI ? 16 : 1) * lane), at = key - div_by(key, p.c.page) * p.c.page.d;
     const bool ok = (int)key < p.c.capacity && entry >= 0 && entry < p.c.pages;
     gk = ok ? (uint64_t)(uint32_t)entry * (uint32_t)p.c.kp + (uint64_t)at * (uint32_t)p.c.ks : 0;
     gv = ok ? (uint64_t)(uint32_t)entry * (uint32_t)p.c.vp + (uint64_t)at * (uint32_t)p.c.vs : 0;
     gok = __builtin_amdgcn_ballot_w64(ok);
-    if (kb + kBatch < k1) entry = entry_of(kb + kBatch);
+    if (next < k1) entry = entry_of(next);
   };
-  auto of_group = [](uint64_t x, int f) {
-    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), f) << 32 |
-           (uint32_t)__builtin_amdgcn_readlane((int)x, f);
+  auto of_lane = [](uint64_t x, int f) {
+    if constexpr (UNI)
+      return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), f) << 32 |
+             (uint32_t)__builtin_amdgcn_readlane((int)x, f);
+    else
+      return (uint64_t)(uint32_t)__shfl((int)(x >> 32), f) << 32 | (uint32_t)__shfl((int)x, f);
   };
   Frag kf[KT][KK];
   u32x4 vr[KT * PI];
   uint32_t have_k = 0, have_v = 0; // keys of the tile that lie on a page, one bit each
   auto load_k = [&](int kb) {
-    if (UNI && (kb - kstart) % kBatch < kWaves * TK) locate(kb - (kb - kstart) % kBatch);
-    have_k = 0;
+    const int f = (kb - kstart) / 16 % 64; // the tile's first group
+    if constexpr (UNI) {
+      if (f < kWaves * KT) locate(kb - 16 * f, kb - 16 * f + kBatch);
+      have_k = 0;
+#pragma unroll
+      for (int g = 0; g < KT; ++g) have_k |= gok >> (f + g) & 1 ? 0xFFFFu << (16 * g) : 0;
+    } else {
+      locate(kb, kb + kWaves * TK);
+      have_k = (uint32_t)gok & (TK == 32 ? ~0u : 0xFFFFu);
+    }
 #pragma unroll
     for (int g = 0; g < KT; ++g) {
-      const T *src;
-      if constexpr (UNI) {
-        const int f = (kb - kstart) / 16 % 64 + g;
-        src = kc + of_group(gk, f);
-        if (gok >> f & 1) have_k |= 0xFFFFu << (16 * g);
-      } else {
-        bool ok;
-        int at;
-        const int pg = lookup(kb + 16 * g + li, &ok, &at);
-        src = kc + (uint64_t)(uint32_t)pg * (uint32_t)p.c.kp + (uint64_t)(uint32_t)at * (uint32_t)p.c.ks;
-        have_k |= (uint32_t)(__builtin_amdgcn_ballot_w64(ok) & 0xFFFFu) << (16 * g);
-      }
+      const T *src = kc + of_lane(gk, UNI ? f + g : 16 * g + li);
 #pragma unroll
       for (int k = 0; k < KK; ++k) {
         const int d = 32 * k + 8 * lg;
@@ -200,20 +202,12 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   };
   auto load_v = [&](int kb) {
 #pragma unroll
-    for (int g = 0; g < KT; ++g) {
-      uint64_t base = 0;
-      if constexpr (UNI) base = of_group(gv, (kb - kstart) / 16 % 64 + g);
+    for (int g = 0; g < KT; ++g)
 #pragma unroll
       for (int i = 0; i < PI; ++i) {
-        if constexpr (!UNI) {
-          bool ok;
-          int at;
-          const int pg = lookup(kb + 16 * g + vrow[i], &ok, &at);
-          base = (uint64_t)(uint32_t)pg * (uint32_t)p.c.vp + (uint64_t)(uint32_t)at * (uint32_t)p.c.vs;
-        }
+        const uint64_t base = of_lane(gv, UNI ? (kb - kstart) / 16 % 64 + g : 16 * g + vrow[i]);
         vr[g * PI + i] = *reinterpret_cast<const u32x4 *>((const char *)(vc + base) + voff[i]);
       }
-    }
   };
 
   f32x4 o[ND];
@@ -224,7 +218,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   T *const vt = reinterpret_cast<T *>(lds + wave * kTile);
   int kb = kstart + wave * TK;
   if (kb < k1) {
-    if constexpr (UNI) entry = entry_of(kstart);
+    entry = entry_of(UNI ? kstart : kb);
     load_k(kb);
     load_v(kb);
   }
@@ -331,14 +325,14 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
       const uint32_t seen = (uint32_t)__builtin_amdgcn_ballot_w64(ok && kb + lane >= k0 && kb + lane < k1 && lane < TK);
       if (seen == (TK == 32 ? ~0u : 0xFFFFu) && kb >= all0 && kb + TK <= all1) continue;
       const uint64_t krow = (uint64_t)pg * p.c.kp + (uint64_t)at * p.c.ks, vrow1 = (uint64_t)pg * p.c.vp + (uint64_t)at * p.c.vs;
-      auto of_lane = [&](uint64_t x, int j) {
+      auto at_lane = [&](uint64_t x, int j) {
         return (uint64_t)(uint32_t)__shfl((int)(x >> 32), j) << 32 | (uint32_t)__shfl((int)x, j);
       };
       bool odd = false;
 #pragma unroll 1
       for (int x = lane; x < TK * PC; x += 64) {
         const int j = x / PC, d = x % PC * (16 / ES);
-        const T *v = vc + of_lane(vrow1, j) + d;
+        const T *v = vc + at_lane(vrow1, j) + d;
         if (d < p.N && (seen >> j & 1)) odd |= odd_values(*reinterpret_cast<const u32x4 *>(v), T());
       }
       if (__builtin_amdgcn_ballot_w64(odd) == 0) continue;
@@ -346,7 +340,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
 #pragma unroll 1
       for (uint32_t left = seen; left; left &= left - 1) {
         const int j = __builtin_ctz(left);
-        const T *ks = kc + of_lane(krow, j), *vs = vc + of_lane(vrow1, j);
+        const T *ks = kc + at_lane(krow, j), *vs = vc + at_lane(vrow1, j);
         float sj = 0.f;
 #pragma unroll
         for (int k = 0; k < KK; ++k) {
@@ -407,52 +401,57 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   }
 }
 
-// Joins the pieces of the rows that have more than one: a workgroup an output
-// vector, N / 4 threads a piece.
-template <typename T> __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnParams p) {
-  __shared__ float red[kThreads / 64], acc_sh[kThreads][4], sum_sh[kThreads];
-  uint32_t id = blockIdx.x;
-  const int h = (int)(id % (uint32_t)p.Hq);
-  id /= (uint32_t)p.Hq;
-  const int t = (int)(id % (uint32_t)p.L), i = (int)(id / (uint32_t)p.L);
-  const int n = p.c.tokens ? min(max(p.c.tokens[i], 0), p.L) : p.L;
-  if (t >= n) return;
-  const int2 pc = p.pieces[i];
-  if (pc.y <= 1) return;
+// Joins the pieces of the rows that have more than one: WPV waves an output vector, N / 4
+// threads a piece, as many pieces at once as that leaves, each group of threads with its
+// own running maximum (a maximum over all pieces first would be one more wait for memory).
+template <typename T, int WPV> __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnParams p) {
+  __shared__ float acc_sh[kThreads][4];
+  __shared__ float2 ml_sh[kThreads];
+  constexpr int TPV = 64 * WPV; // threads of a vector
+  const int tid = threadIdx.x % TPV, first_tid = threadIdx.x - tid;
+  const uint32_t vec = blockIdx.x * (kThreads / TPV) + threadIdx.x / TPV;
+  const uint32_t vt = vec / (uint32_t)p.Hq;
+  const int h = (int)(vec - vt * (uint32_t)p.Hq);
+  const int i = (int)(vt / (uint32_t)p.L), t = (int)(vt - (uint32_t)i * (uint32_t)p.L);
+  int2 pc = make_int2(0, 0);
+  if (i < p.b && (!p.c.tokens || t < p.c.tokens[i])) pc = p.pieces[i];
+  const bool mine = pc.y > 1;
   const int hk = (int)div_by((uint32_t)h, p.group), r = t * p.G + h - hk * p.G;
+  const int tile = r / p.rows;
   const int64_t step = (int64_t)p.Hk * p.tiles * p.prow;
-  const int64_t first = ((int64_t)pc.x * p.Hk + hk) * p.tiles * p.prow + r;
-  const int tid = threadIdx.x;
-  float top = -INFINITY;
-  for (int c = tid; c < pc.y; c += kThreads) top = fmaxf(top, p.part_ml[first + c * step].x);
-#pragma unroll
-  for (int k = 32; k; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
-  if ((tid & 63) == 0) red[tid >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const float base = top == -INFINITY ? 0.f : top;
-  const int nv = p.N / 4, lanes = kThreads / nv; // threads of a piece, pieces at once
+  const int64_t first = (((int64_t)pc.x * p.Hk + hk) * p.tiles + tile) * p.prow + r - tile * p.rows;
+  const int nv = p.N / 4, groups = TPV / nv;
   const int g = tid / nv, c4 = (tid - g * nv) * 4;
   f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
-  if (g < lanes) {
+  float m = -INFINITY, sum = 0.f;
+  if (mine && g < groups) {
 #pragma unroll 4
-    for (int c = g; c < pc.y; c += lanes) {
+    for (int c = g; c < pc.y; c += groups) {
       const float2 e = p.part_ml[first + c * step];
-      const float a = hw_exp2(e.x - base);
-      sum = fmaf(a, e.y, sum);
-      acc += a * *reinterpret_cast<const f32x4 *>(p.part + (first + c * step) * p.N + c4);
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(p.part + (first + c * step) * p.N + c4);
+      const float mn = fmaxf(m, e.x), base = mn == -INFINITY ? 0.f : mn;
+      const float a = hw_exp2(m - base), w = hw_exp2(e.x - base);
+      sum = fmaf(sum, a, w * e.y);
+      acc = acc * a + w * v;
+      m = mn;
     }
   }
-  *reinterpret_cast<f32x4 *>(acc_sh[tid]) = acc;
-  sum_sh[tid] = sum;
+  *reinterpret_cast<f32x4 *>(acc_sh[threadIdx.x]) = acc;
+  ml_sh[threadIdx.x] = make_float2(m, sum);
   __syncthreads();
-  if (tid >= nv) return;
-  for (int k = 1; k < lanes; ++k) {
-    acc += *reinterpret_cast<const f32x4 *>(acc_sh[k * nv + tid]);
-    sum += sum_sh[k * nv + tid];
+  if (!mine || tid >= nv) return;
+  float top = -INFINITY;
+  for (int k = 0; k < groups; ++k) top = fmaxf(top, ml_sh[first_tid + k * nv].x);
+  const float base = top == -INFINITY ? 0.f : top;
+  acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  sum = 0.f;
+  for (int k = 0; k < groups; ++k) {
+    const float2 e = ml_sh[first_tid + k * nv];
+    const float w = hw_exp2(e.x - base);
+    sum = fmaf(w, e.y, sum);
+    acc += w * *reinterpret_cast<const f32x4 *>(acc_sh[first_tid + k * nv + tid]);
   }
-  const int64_t at = ((int64_t)i * p.L + t) * p.Hq + h;
+  const int64_t at = (int64_t)vt * p.Hq + h;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   st4<T>((T *)p.out + at * p.N + c4, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
   if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
@@ -475,7 +474,11 @@ template <typename T> hipError_t launch_t(const AttnParams &p, hipStream_t st) {
   else launch_np<T, 256>(p, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.workers == 1) return e;
-  attn_join_kernel<T><<<(uint32_t)((int64_t)p.b * p.L * p.Hq), kThreads, 0, st>>>(p);
+  const int64_t vecs = (int64_t)p.b * p.L * p.Hq;
+  // a wave each where they fill the device: b3 L777 5 heads N96 fp32 43.8 us, four 49.2; fewer
+  // vectors wait longer for their pieces: b1 262143 keys 32 heads 203 us, with four waves 197
+  if (vecs >= 4096) attn_join_kernel<T, 1><<<(uint32_t)((vecs + 3) / 4), kThreads, 0, st>>>(p);
+  else attn_join_kernel<T, 4><<<(uint32_t)vecs, kThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 
