@@ -16,9 +16,18 @@
 // leave the registers.  The four waves of a workgroup take every fourth tile of
 // keys, each with its own m, l and O, and are joined in LDS at the end.
 // K rows go to registers as A operands; V tiles pass through LDS, a wave's own
-// part of it, written as rows and read transposed (ds_read_b64_tr_b16).
+// part of it, written as rows and read transposed (ds_read_b64_tr_b16).  The next
+// tile's K and V are on their way while one is worked on.
 //
 // Long caches are cut into pieces (see piece_of); attn_join_kernel joins them.
+//
+// Bound by HBM: b128 rows of up to 16384 keys, 32 + 8 heads N128 bf16 780 us (5.5 TB/s;
+// a large copy reaches 4.9, reading and writing), one row of 262143 keys 200 us (5.4), b32
+// 2047 keys 48 us (5.6).  Small calls by their chain of waits (start, page table, keys,
+// join): b1 1000 keys 10.3 us in a graph, of which 3.5 are two launches that do
+// nothing and 3.4 the join.  fp32 with many queries by the matrix cores and the reads of K
+// and V for every 16 rows: b1 L2048 32 + 8 heads N128 425 us, 81 TFLOP/s of the 154 that a
+// large product reaches.
 #include "ssd_attn_device.h"
 
 namespace ssd {
@@ -26,9 +35,9 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = 4, kRows = 16;
 
-// Keys of a tile: the K of the second product's matrix instruction (bf16 32,
+// Groups of 16 keys in a tile: the K of the second product's matrix instruction (bf16 32,
 // fp32 four times 4).
-template <typename T> constexpr int kKT = sizeof(T) == 2 ? 2 : 1; // groups of 16 keys
+template <typename T> constexpr int kKT = sizeof(T) == 2 ? 2 : 1;
 
 // Maximum over the four lane groups of a column.
 __device__ __forceinline__ float col_max(float v) {
@@ -47,6 +56,7 @@ template <typename T> __device__ __forceinline__ typename FragOf<T>::type zero_f
   return pack8<T>(z);
 }
 
+// A use of the fragments that costs nothing but the wait for them.
 template <int K> __device__ __forceinline__ void arrived(FragBF (&f)[K]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) __asm__ volatile("" : "+v"(f[k].v));
@@ -58,9 +68,10 @@ template <int K> __device__ __forceinline__ void arrived(FragF32 (&f)[K]) {
     for (int e = 0; e < 8; ++e) __asm__ volatile("" : "+v"(f[k].v[e]));
 }
 
-// UNI: the page size is a multiple of 16, so that 16 keys from a multiple of 16 on
-// lie in one page and their page is looked up once, by the scalar unit; otherwise
-// every lane looks up the rows it loads.
+// UNI: the page size is a multiple of 16, so that 16 keys from a multiple of 16 on lie in
+// one page, one behind the other (see locate).  Wide heads hold so much of a tile that one
+// workgroup to a compute unit is all there is room for (two, with 91 registers in scratch:
+// b64, a window of 2048 keys, 10 + 1 heads N256 104 us, one 48).
 template <typename T, int NP, bool UNI>
 __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnParams p) {
   constexpr int KT = kKT<T>, TK = 16 * KT, ES = sizeof(T);
@@ -487,6 +498,15 @@ constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
 
 } // namespace
 
+// More than one tile of query vectors in bf16 goes to attn_rows_kernel, which reads K and V
+// once for 256 (128) of them: b4, 8 new tokens behind 8000, 32 + 8 heads N128 40 us, by two
+// tiles of 16 here 47; 16 tokens 43 and 86.
+//
+// Pieces: as many as run at once (512 workgroups, 256 of wide heads; with twice as many b8
+// 2047 keys 20.6 us, so 18.3), but none larger than a MB of keys and values while there are
+// fewer than 4096 workgroups (b128 rows of 0 to 16384 keys: 1024 929 us, 2048 844, 4096 796;
+// with one row of 262143 keys 199, 211 and 232, since a workgroup costs 8 us before its
+// first key).  8192 workgroups and more need no pieces.
 int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t vecs = (int64_t)p->L * p->G;
   const bool wide = dtype == 1 && vecs > kRows;

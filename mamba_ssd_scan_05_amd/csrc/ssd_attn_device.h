@@ -62,10 +62,10 @@ struct Piece {
   // units of each of the row's pieces
   __device__ __forceinline__ int size() const { return count == 1 ? INT32_MAX : (row.units() + count - 1) / count; }
 };
-// sh: 11 words of LDS.  The plan, the same in every workgroup: all rows' lengths together are cut into
-// about p.workers pieces of equal size, so that a batch of one long row and many
-// short ones keeps the device as busy as an even one.  Piece `slot` of that list.
-// The sum of the units stays below 2^31 (checked on the host).
+// The plan, the same in every workgroup: all rows' lengths together are cut into pieces of
+// about equal size, so that a batch of one long row and many short ones keeps the device as
+// busy as an even one.  Units of a piece, for all rows' `total`, which stays below 2^31
+// (checked on the host):
 __device__ __forceinline__ int piece_units(const AttnParams &p, int total) {
   const int least = (total + p.workers - 1) / p.workers;
   return max(max(least, min((total + p.prefer - 1) / p.prefer, p.enough)), 2);
@@ -74,6 +74,7 @@ __device__ __forceinline__ int piece_units(const AttnParams &p, int total) {
 __device__ __forceinline__ int pieces_of(int u, int size) {
   return u == 0 ? 0 : max((u + size - 1 - size / 4) / size, 1);
 }
+// Piece `slot` of the list; false behind its end.  sh: 11 words of LDS.
 template <int THREADS>
 __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh, Piece *pc) {
   if (p.workers == 1) {
