@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
     load_v(kb);
   }
   // The queries are there from here on: as loads still on their way they would be waited
-  // for in every round, and with them the next tile's.
+  // for in every pass of the loop, and with them the next tile's.
   arrived(qf);
   for (; kb < k1; kb += kWaves * TK) {
     const int next = kb + kWaves * TK;

@@ -1,9 +1,29 @@
-// ssd_attn_rows.hip -- attention of many new tokens of a row (prompts and pieces of
-// them) over the paged cache, bf16.  The products and the orientation are those of
-// ssd_attn.hip, S^T = K Q^T and O^T = V^T P^T, but with 32 x 32 tiles: a wave owns 32
-// query vectors for all keys, W waves share the K and V tiles of 64 keys in LDS, two
-// buffers of them, the next tile's rows on their way to registers while one is
-// worked on.  Bound by the matrix cores together with the exponentials.
+// ssd_attn_rows.hip -- attention of more than 16 query vectors of a row and key head
+// (prompts, pieces of them, drafted tokens) over the paged cache, bf16.  The products and
+// the orientation are those of ssd_attn.hip, S^T = K Q^T and O^T = V^T P^T, with 32 x 32
+// tiles: a lane holds the scores of one query (its column), 16 keys of 32 with those of the
+// lane 32 further, and eight of them are the B operand of 16 keys of the second product
+// as they stand.  A wave owns 32 query vectors for all keys; W waves share tiles of 64 keys
+// in LDS.
+//
+// A pass of the loop works on a tile whose scores lie in registers: between the products of the next
+// tile's scores and those of its own sums its weights are formed, so that the matrix cores
+// and the vector ALU run at the same time, and the next tile's maximum is taken.  K of the
+// tile after the next and V of the next are on their way to registers meanwhile.  The
+// running maximum that the weights refer to moves only when one would pass 2^8, which
+// spares the sums' scaling nearly always.
+//
+// Measured, 32 + 8 heads N128 (bf16): prompt b4 L4096 627 us (877 TFLOP/s counted on the
+// pairs that are seen; a large product reaches 1358), 512 tokens behind 32000 292 us (926).
+// Of a pass's 5000 cycles the matrix cores work 38 %, the vector ALU 43 (32 exponentials a
+// lane are 512 of its 1000 cycles a wave); LDS reads have no conflicts.  Without the loads,
+// stores and barrier of a pass the second case took 249 of 314 us, without exponentials
+// 300.  Steps that did not pay: four waves a workgroup and two of them a compute unit (788
+// against 775), one barrier for two tiles (777 against 737), reads three or four products
+// ahead (648 and 654 against 650), the stores between the products (661 against 621).
+// 96 registers hold O and Q and 64 two tiles' scores, so eight waves are all a compute unit
+// takes.  Wide heads (N > 128): four waves with the whole register file, tiles of 32 keys;
+// b4 L2048 10 + 1 heads N256 235 us, 365 TFLOP/s, some 40 registers in scratch.
 #include <type_traits>
 
 #include "ssd_attn_device.h"
@@ -44,17 +64,14 @@ __device__ __forceinline__ uint64_t bits(int a, int b) {
 }
 
 // UNI: the page size is a multiple of 16; the 64 pieces a wave loads at once lie in
-// 16 rows of one page then, which is found by the scalar unit.
+// 16 rows of one page then, one behind the other.
 template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 128 ? 2 : 1) void attn_rows_kernel(AttnParams p) {
   constexpr int kTK = tile_keys(NP), KG = kTK / 32;       // groups of 32 keys
   constexpr uint64_t kAll = kTK == 64 ? ~0ull : 0xFFFFFFFFull;
   constexpr int KS = NP / 16, DT = NP / 32;               // steps of 16 dims, tiles of 32 dims
   constexpr int PC = NP / 8, CH = (kTK * PC + 64 * W - 1) / (64 * W); // pieces of a row, of a thread
   constexpr int kRows = 32 * W;
-#ifndef AH
-#define AH 2
-#endif
-  constexpr int AHEAD = AH;
+  constexpr int AHEAD = 2; // reads from LDS ahead of their products
   using KW = KSwizzle<NP>;
   using VW = VSwizzle<NP>;
   __shared__ __align__(16) __bf16 ktile[2][kTK * NP], vtile[3][kTK * NP]; // vtile[2]: zeros
@@ -387,10 +404,11 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       }
       l = (part[0] + part[1]) + (part[2] + part[3]);
     }
+    if (next < k1) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) store_k(c, ktile[P]), store_v(c, vtile[1 - P]);
-
-    if (next < k1) publish(next, have0, vtile[1 - P]);
+      publish(next, have0, vtile[1 - P]);
+    }
     kb = next;
   };
   while (kb < k1) {
@@ -485,10 +503,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
 
 } // namespace
 
-#ifndef WV
-#define WV 8
-#endif
-int attn_rows(int N) { return N <= 128 ? 32 * WV : 128; }
+int attn_rows(int N) { return N <= 128 ? 256 : 128; }
 
 template <int NP, int W> static void launch_np(const AttnParams &p, hipStream_t st) {
   const uint32_t grid = (uint32_t)((int64_t)p.slots * p.Hk * p.tiles);
@@ -496,10 +511,10 @@ template <int NP, int W> static void launch_np(const AttnParams &p, hipStream_t 
   else attn_rows_kernel<NP, W, false><<<grid, 64 * W, 0, st>>>(p);
 }
 hipError_t launch_attn_rows(const AttnParams &p, hipStream_t st) {
-  if (p.N <= 32) launch_np<32, WV>(p, st);
-  else if (p.N <= 64) launch_np<64, WV>(p, st);
-  else if (p.N <= 96) launch_np<96, WV>(p, st);
-  else if (p.N <= 128) launch_np<128, WV>(p, st);
+  if (p.N <= 32) launch_np<32, 8>(p, st);
+  else if (p.N <= 64) launch_np<64, 8>(p, st);
+  else if (p.N <= 96) launch_np<96, 8>(p, st);
+  else if (p.N <= 128) launch_np<128, 8>(p, st);
   else if (p.N <= 192) launch_np<192, 4>(p, st);
   else launch_np<256, 4>(p, st);
   return hipGetLastError();
