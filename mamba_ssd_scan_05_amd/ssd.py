@@ -601,7 +601,7 @@ def ssd_attn_fwd(q, k_cache, v_cache, page_table, start, *, tokens=None, scale: 
     with _on_device(q):
         st = _stream(stream, q)
         keep, d = _descs(q, k_cache, v_cache, page_table, start, tokens, out, lse)
-        status = lib().ssd_attn_fwd(*d, q.shape[-1] ** -0.5 if scale is None else scale, int(window),
+        status = lib().ssd_attn_fwd(*d, q.shape[-1] ** -0.5 if scale is None else float(scale), int(window),
                                     ws.data_ptr() if ws is not None else None,
                                     ws.numel() if ws is not None else 0, st)
     _check(status)
@@ -620,7 +620,7 @@ def ssd_attn_step(q, k_cache, v_cache, page_table, start, *, scale: float = None
     with _on_device(q):
         st = _stream(stream, q)
         keep, d = _descs(q, k_cache, v_cache, page_table, start, out, lse)
-        status = lib().ssd_attn_step(*d, q.shape[-1] ** -0.5 if scale is None else scale, int(window),
+        status = lib().ssd_attn_step(*d, q.shape[-1] ** -0.5 if scale is None else float(scale), int(window),
                                      ws.data_ptr() if ws is not None else None,
                                      ws.numel() if ws is not None else 0, st)
     _check(status)
