@@ -630,7 +630,7 @@ int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk,
  * of prompts: any L.  Rows of any lengths share the device evenly.
  * Arithmetic: scores, maxima, sums and outputs in fp32; with bf16 inputs
  * the weights e^{s - m} are rounded to bf16 for the product with the values (2^-8
- * of each); out is rounded once.  The sums of weighted values, weights up to 2^8, have to
+ * of each); out is rounded once.  The sums of weighted values, weights up to 4, have to
  * stay in fp32's range.  Results do not vary from run to run; a row's do depend, to
  * rounding, on the other rows' lengths (which say where it is cut).
  * out and lse may not overlap any other argument.  b * L * Hq at most 2^27.

@@ -10,11 +10,14 @@
 // tile's scores and those of its own sums its weights are formed, so that the matrix cores
 // and the vector ALU run at the same time, and the next tile's maximum is taken.  K of the
 // tile after the next and V of the next are on their way to registers meanwhile.  The
-// running maximum that the weights refer to moves only when one would pass 2^8, which
-// spares the sums' scaling nearly always.
+// running maximum that the weights refer to moves only when one would pass 4, which mostly
+// spares the sums' scaling.  (Where it always moves, the largest weight is 1 and rounds to
+// itself: error against 64 bits 0.0019 of the output's norm, 656 us for the prompt below
+// when this took 647 with 0.0019 to 0.0020; moved past 2^8: 0.0022, 638 us.  The output's
+// rounding alone is 0.0016.)
 //
-// Measured, 32 + 8 heads N128 (bf16): prompt b4 L4096 627 us (877 TFLOP/s counted on the
-// pairs that are seen; a large product reaches 1358), 512 tokens behind 32000 292 us (926).
+// Measured, 32 + 8 heads N128 (bf16): prompt b4 L4096 647 us (850 TFLOP/s counted on the
+// pairs that are seen; a large product reaches 1358), 512 tokens behind 32000 302 us (896).
 // Of a pass's 5000 cycles the matrix cores work 38 %, the vector ALU 43 (32 exponentials a
 // lane are 512 of its 1000 cycles a wave); LDS reads have no conflicts.  Without the loads,
 // stores and barrier of a pass the second case took 249 of 314 us, without exponentials
@@ -340,8 +343,8 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       }
       const Both tops = swap32(top);
       const float highest = fmaxf(tops.a, tops.b) * p.scale;
-      // the weights' reference moves only when some weight would pass 2^8
-      if (__builtin_amdgcn_ballot_w64(highest > m + 8.f) != 0) {
+      // the weights' reference moves only when some weight would pass 4
+      if (__builtin_amdgcn_ballot_w64(highest > m + 2.f) != 0) {
         const float mn = fmaxf(m, highest), a = hw_exp2(m - (mn == -INFINITY ? 0.f : mn));
         l *= a;
 #pragma unroll
