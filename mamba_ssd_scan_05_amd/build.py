@@ -29,8 +29,10 @@ SOURCES = ["ssd_api.hip", "ssd_kernels.hip", "ssd_prep.hip", "ssd_quad.hip", "ss
            "ssd_attn_rows.hip"]
 # Per-source flags.  The row walk keeps its MFMA accumulators (the state
 # tile) in ordinary VGPRs; otherwise the compiler places them in accumulator
-# registers and copies them to VGPRs and back on every sub-block.
-EXTRA = {"ssd_rwalk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# registers and copies them to VGPRs and back on every sub-block.  Likewise the
+# scores of the attention's prompts (wide heads: N 256 775 -> 642 us).
+EXTRA = {"ssd_rwalk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+         "ssd_attn_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 COMMON = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",

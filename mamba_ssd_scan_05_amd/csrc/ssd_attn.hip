@@ -514,7 +514,7 @@ int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t tiles = (vecs + p->rows - 1) / p->rows, heads = p->Hk * tiles;
   p->tiles = (int)tiles;
   const int64_t prefer = wide ? 512 : p->N <= 128 ? 512 : 256, most = wide ? 512 : 4096;
-  p->workers = heads * p->b >= (wide ? 512 : 8192) ? 1 : (int)((most + heads - 1) / heads);
+  p->workers = heads * p->b >= (tiles > 1 ? 512 : 8192) ? 1 : (int)((most + heads - 1) / heads);
   p->prefer = (int)((prefer + heads - 1) / heads);
   p->enough = (int)((1 << 20) / (2 * kAttnUnit * p->N * (dtype == 1 ? 2 : 4)));
   if (p->enough < 2) p->enough = 2;

@@ -43,9 +43,11 @@ constexpr int tile_keys(int NP) { return NP <= 128 ? 64 : 32; }
 // read at once lie on different banks.
 template <int NP> struct KSwizzle {
   static constexpr int pow2(int n) { return n % 2 ? 1 : 2 * pow2(n / 2); }
-  static constexpr int C2 = pow2(NP / 8) < 16 ? pow2(NP / 8) : 16;
+  // a period of 8 rows for the widest heads, of which a thread's pieces lie 8 rows apart
+  static constexpr int kMost = NP == 256 ? 8 : 16;
+  static constexpr int C2 = pow2(NP / 8) < kMost ? pow2(NP / 8) : kMost;
   __device__ static __forceinline__ int at(int row, int piece) {
-    return row * NP + (piece ^ (row / (16 / C2) & (C2 - 1))) * 8;
+    return row * NP + (piece ^ (row / (kMost / C2) & (C2 - 1))) * 8;
   }
 };
 
@@ -144,7 +146,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   // Where pieces of one thread lie whole periods of the exchanges apart, one register holds
   // each of these for all of them.
   constexpr int RW = 64 * W / PC;
-  constexpr bool kEven = 64 * W % PC == 0 && RW % 16 == 0;
+  constexpr bool kEven = 64 * W % PC == 0 && RW % KW::kMost == 0;
   constexpr int CA = kEven ? 1 : CH;
   int krow_[CA], kat_[CA], vat_[CA];
   uint32_t koff_[CA], voff_[CA];
@@ -163,8 +165,9 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   auto krow = [&](int c) { return kEven ? krow_[0] + c * RW : krow_[c]; };
   auto kat = [&](int c) { return kEven ? kat_[0] + c * RW * NP : kat_[c]; };
   auto vat = [&](int c) { return kEven ? vat_[0] + c * RW * NP : vat_[c]; };
-  auto koff = [&](int c) { return koff_[kEven ? 0 : c]; };
-  auto voff = [&](int c) { return voff_[kEven ? 0 : c]; };
+  // (of rows 8 apart those of a group's second half lie further on)
+  auto koff = [&](int c) { return kEven ? koff_[0] + (UNI ? (uint32_t)(c * RW % 16 * p.c.ks * 2) : 0) : koff_[c]; };
+  auto voff = [&](int c) { return kEven ? voff_[0] + (UNI ? (uint32_t)(c * RW % 16 * p.c.vs * 2) : 0) : voff_[c]; };
   auto none = [&](int c) { return none_[kEven ? 0 : c]; };
   // Where the rows of a tile lie.  UNI: lane l keeps the page and the places of the l-th 16 keys
   // of a batch of 16 or 32 tiles, found once for the batch; a wave's loads read their group's
@@ -383,6 +386,9 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
           pf[x / 8][x % 8] = (__bf16)w;
         }
       };
+      // one of a SIMD's two waves goes first, so that the other's vector work falls between
+      // its products (prompt b4 L4096 660 -> 651 us; all waves alike 665 -> 660)
+      if (W == 8 && (wave & 4)) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) ka[i] = kfrag(i);
       __builtin_amdgcn_sched_barrier(0);
@@ -406,6 +412,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
         __builtin_amdgcn_sched_barrier(0);
       }
       l = (part[0] + part[1]) + (part[2] + part[3]);
+      if constexpr (W == 8) __builtin_amdgcn_s_setprio(0);
     }
     if (next < k1) {
 #pragma unroll
