@@ -78,6 +78,22 @@ def test_append_sizes_and_options_refused():
     assert append(a)[0] == 5
 
 
+def test_strides_of_pages():
+    # a page stride just below 2^32 elements passes, one of 2^32 does not
+    import ctypes
+    for stride, ok in (((1 << 32) - 8, True), (1 << 32, False)):
+        a = append_args()
+        keep, d = ssd._descs(*a.values())
+        d = list(d)
+        for i in (8, 9):
+            p = ssd.describe(a["k_cache" if i == 8 else "v_cache"])
+            p.contents.data = (1 << 44) * (i - 6)  # far from each other, never touched
+            p.contents.strides[0] = stride
+            d[i] = ctypes.cast(p, ctypes.c_void_p)
+        st = ssd.lib().ssd_kv_append(*d, 0, None)
+        assert (st == 4 and passes(st, ssd.ssd_last_error())) if ok else st == 5, (st, ssd.ssd_last_error())
+
+
 def test_append_takes_what_is_documented():
     assert passes(*append(append_args()))
     a = append_args()
