@@ -514,7 +514,7 @@ int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t tiles = (vecs + p->rows - 1) / p->rows, heads = p->Hk * tiles;
   p->tiles = (int)tiles;
   const int64_t prefer = wide ? 512 : p->N <= 128 ? 512 : 256, most = wide ? 512 : 4096;
-  p->workers = heads * p->b >= (tiles > 1 ? 512 : 8192) ? 1 : (int)((most + heads - 1) / heads);
+  p->workers = heads * p->b >= 8192 ? 1 : (int)((most + heads - 1) / heads);
   p->prefer = (int)((prefer + heads - 1) / heads);
   p->enough = (int)((1 << 20) / (2 * kAttnUnit * p->N * (dtype == 1 ? 2 : 4)));
   if (p->enough < 2) p->enough = 2;
@@ -529,10 +529,22 @@ int64_t attn_plan(AttnParams *p, int dtype) {
 // Pieces that there can be with this table and window: a row has no more units than its
 // table or its window and new tokens, and a piece no fewer than piece_units gives it.
 // (Workgroups without a piece cost their launch, behind all others: 3700 of them 12 us.)
+//
+// No pieces where every row has several tiles, the workgroups fill the device without them
+// and even the longest that the table allows takes little of the whole: fp32 b3 L777
+// window 500 29.6 us, with pieces 35.5; bf16 b16 L1024 behind up to 4000 keys 847 and 910.
+// Where the table is wide one row may be all the work: b32 L128, one row behind 131000 keys
+// and 31 behind 1000, 32 + 8 heads N128 4540 us without and 545 with pieces (all 32 behind
+// 8000: 643 and 661); b8 L512 behind 0 to 30000 1610 and 1370.
 void attn_slots(AttnParams *p) {
   if (p->workers == 1) return;
   int64_t keys = p->c.capacity;
   if (p->window && p->window + p->L < keys) keys = p->window + p->L;
+  const int64_t groups = (int64_t)p->Hk * p->tiles * p->b;
+  if (p->tiles > 1 && groups >= 512 && keys <= 4 * (groups / 512) * p->L) {
+    p->workers = 1, p->slots = p->b;
+    return;
+  }
   const int64_t total = (int64_t)p->b * ((keys + kAttnUnit - 1) / kAttnUnit + 1);
   int64_t n = (total + p->enough - 1) / p->enough;
   if (n < p->prefer) n = p->prefer;

@@ -119,3 +119,19 @@ def test_small_tables_need_little():
     wide[:, 100:100 + t.table.shape[1]] = t.table.to(DEV)
     d = ssd.ssd_attn_step(t.q[:, 0].to(DEV), t.kc, t.vc, wide[:, 100:100 + t.table.shape[1]], s, scale=0.1)
     assert torch.equal(d, a[:, 0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("window", [0, 1100])
+def test_a_long_row_among_short_ones(window, dtype):
+    # workgroups enough without pieces, but the table allows a row many times its new tokens
+    starts = [5000 if i == 9 else 30 + i for i in range(32)]
+    t = Batch(starts, [70 - i % 3 for i in range(32)], 70, 32, 8, 32, 16, dtype, seed=4, spare=0)
+    some(t, [0, 8, 9, 10, 31], window=window)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_rows_of_several_tiles_uncut(dtype):
+    # no pieces, though below 8192 workgroups; keys past the 1024 whose places are found at once
+    t = Batch([800 - 9 * i for i in range(22)], [300 - i for i in range(22)], 300, 16, 8, 24, 16, dtype, seed=5, spare=0)
+    some(t, [0, 1, 21])
