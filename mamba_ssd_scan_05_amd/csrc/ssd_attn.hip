@@ -506,7 +506,8 @@ constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
 // 2047 keys 20.6 us, so 18.3), but none larger than a MB of keys and values while there are
 // fewer than 4096 workgroups (b128 rows of 0 to 16384 keys: 1024 929 us, 2048 844, 4096 796;
 // with one row of 262143 keys 199, 211 and 232, since a workgroup costs 8 us before its
-// first key).  8192 workgroups and more need no pieces.
+// first key).  8192 workgroups and more get no pieces, whose sums would take GBs; one tile of
+// 16, whose sums are small, gets them up to 65536.
 int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t vecs = (int64_t)p->L * p->G;
   const bool wide = dtype == 1 && vecs > kRows;
@@ -514,7 +515,7 @@ int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t tiles = (vecs + p->rows - 1) / p->rows, heads = p->Hk * tiles;
   p->tiles = (int)tiles;
   const int64_t prefer = wide ? 512 : p->N <= 128 ? 512 : 256, most = wide ? 512 : 4096;
-  p->workers = heads * p->b >= 8192 ? 1 : (int)((most + heads - 1) / heads);
+  p->workers = heads * p->b >= (wide || tiles > 1 ? 8192 : 65536) ? 1 : (int)((most + heads - 1) / heads);
   p->prefer = (int)((prefer + heads - 1) / heads);
   p->enough = (int)((1 << 20) / (2 * kAttnUnit * p->N * (dtype == 1 ? 2 : 4)));
   if (p->enough < 2) p->enough = 2;
@@ -535,13 +536,16 @@ int64_t attn_plan(AttnParams *p, int dtype) {
 // window 500 29.6 us, with pieces 35.5; bf16 b16 L1024 behind up to 4000 keys 847 and 910.
 // Where the table is wide one row may be all the work: b32 L128, one row behind 131000 keys
 // and 31 behind 1000, 32 + 8 heads N128 4540 us without and 545 with pieces (all 32 behind
-// 8000: 643 and 661); b8 L512 behind 0 to 30000 1610 and 1370.
+// 8000: 643 and 661); b8 L512 behind 0 to 30000 1610 and 1370.  Of one tile a row, 8192
+// workgroups of up to 4096 keys: b1024, one row of 16000 keys and the others of 200, 8 heads
+// N64 204 us without and 154 with pieces; b256, 32000 and 500, 32 heads N128 647 and 478; even
+// rows of 5000 or 0 to 8000 keys the same within 2 %.
 void attn_slots(AttnParams *p) {
   if (p->workers == 1) return;
   int64_t keys = p->c.capacity;
   if (p->window && p->window + p->L < keys) keys = p->window + p->L;
   const int64_t groups = (int64_t)p->Hk * p->tiles * p->b;
-  if (p->tiles > 1 && groups >= 512 && keys <= 4 * (groups / 512) * p->L) {
+  if (p->tiles > 1 ? groups >= 512 && keys <= 4 * (groups / 512) * p->L : groups >= 8192 && keys <= 4096) {
     p->workers = 1, p->slots = p->b;
     return;
   }

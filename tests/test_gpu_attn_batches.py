@@ -135,3 +135,11 @@ def test_rows_of_several_tiles_uncut(dtype):
     # no pieces, though below 8192 workgroups; keys past the 1024 whose places are found at once
     t = Batch([800 - 9 * i for i in range(22)], [300 - i for i in range(22)], 300, 16, 8, 24, 16, dtype, seed=5, spare=0)
     some(t, [0, 1, 21])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_a_long_row_among_a_thousand(dtype):
+    # 8240 workgroups without pieces; the table allows more keys than one should walk alone
+    starts = [4500 if i == 700 else 20 + i % 30 for i in range(1030)]
+    t = Batch(starts, [1] * 1030, 1, 8, 8, 16, 16, dtype, seed=6, spare=0)
+    some(t, [0, 1, 699, 700, 701, 1029], step=True)
