@@ -574,8 +574,8 @@ int ssd_norm_rotate_bwd(const ssd_tensor *q, const ssd_tensor *k,
  * no element may be two (strides that overlap), and k_cache and v_cache may lie
  * in each other's gaps, such as halves of one tensor [pages, 2, page_size, Hk, N].  page_table
  * may have a batch stride.  Offsets are 64 bits wide.
- * Supported: f32 or bf16, N a multiple of 8 up to 256, b at most 2^16, L at most 2^24,
- * b * L at most 2^25, width * page_size at most 2^30 and b times that at most
+ * Supported: f32 or bf16, N a multiple of 8 up to 256, b, Hq and Hk at most 2^16, L at most
+ * 2^24, b * L at most 2^25, width * page_size at most 2^30 and b times that at most
  * 2^36.  The calls allocate nothing and may be captured into a HIP graph.
  */
 
@@ -632,8 +632,9 @@ int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk,
  * the weights e^{s - m} are rounded to bf16 for the product with the values (2^-8
  * of each); out is rounded once.  The sums of weighted values, weights up to 4, have to
  * stay in fp32's range.  Results do not vary from run to run; a row's do depend, to
- * rounding, on the other rows' lengths (which say where it is cut).
- * out and lse may not overlap any other argument.  b * L * Hq at most 2^27.
+ * rounding, on the other rows' lengths, the table's width and the window (which say
+ * where it is cut).  out and lse may not overlap any other argument.
+ * b * Hk * ceil(L * Hq / Hk / 16) at most 2^23.
  */
 int ssd_attn_fwd(const ssd_tensor *q, const ssd_tensor *k_cache,
                  const ssd_tensor *v_cache, const ssd_tensor *page_table,

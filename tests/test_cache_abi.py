@@ -261,3 +261,15 @@ def test_reference_turn_against_complex_numbers(interleaved):
     w = a * np.exp(1j * pos[..., None] * f)
     got = y[..., :8:2] + 1j * y[..., 1:8:2] if interleaved else y[..., :4] + 1j * y[..., 4:8]
     assert np.allclose(got, w, rtol=1e-12, atol=1e-12) and (y[..., 8:] == x[..., 8:]).all() and (e[..., 8:] == 0).all()
+
+
+def test_largest_attention_sizes():
+    # b * Hk * ceil(L * Hq / Hk / 16) up to 2^23
+    assert ssd.ssd_attn_workspace(1 << 16, 1, 128, 128, 64) == 0
+    assert ssd.ssd_attn_workspace(1 << 16, 1, 129, 129, 64) == -1
+    assert ssd.ssd_attn_workspace(1 << 16, 16, 128, 128, 64) == 0
+    assert ssd.ssd_attn_workspace(1 << 16, 17, 128, 128, 64) == -1
+    assert ssd.ssd_attn_workspace(1, 1 << 24, 8, 8, 64) == 0
+    assert ssd.ssd_attn_workspace(1, 1 << 24, 9, 9, 64) == -1
+    assert ssd.ssd_attn_workspace(1, 1, 1 << 16, 1, 64) > 0
+    assert ssd.ssd_attn_workspace(1, 1, 1 << 17, 1, 64) == -1
