@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   constexpr int kTile = TK * NP * ES, kJoin = 16 * LO * 4;
   __shared__ __align__(16) char lds[kWaves * (kTile > kJoin ? kTile : kJoin)];
   __shared__ float2 ml[kWaves][16];
-  __shared__ int sh[11];
+  __shared__ int sh[19];
 
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -550,7 +550,10 @@ void attn_slots(AttnParams *p) {
     return;
   }
   const int64_t total = (int64_t)p->b * ((keys + kAttnUnit - 1) / kAttnUnit + 1);
+  // largest pieces, or twice as many where uneven rows' are halved (below 2 * prefer then)
   int64_t n = (total + p->enough - 1) / p->enough;
+  const int64_t halved = 2 * n < 4 * (int64_t)p->prefer ? 2 * n : 4 * (int64_t)p->prefer;
+  if (n < halved) n = halved;
   if (n < p->prefer) n = p->prefer;
   if (n > (total + 1) / 2) n = (total + 1) / 2;
   if (n > p->workers) n = p->workers;

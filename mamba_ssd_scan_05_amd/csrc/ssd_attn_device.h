@@ -17,6 +17,16 @@ __device__ __forceinline__ int wave_incl_scan_i(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
   return v;
 }
+// Maximum over a wave of values from 0 on.
+__device__ __forceinline__ int wave_max_i(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
 
 // What workgroup `id` does: a tile of the query vectors of a key head of a piece.  The
 // tiles of a piece and head read the same keys: they go to one XCD (workgroups are dealt to
@@ -65,16 +75,20 @@ struct Piece {
 // The plan, the same in every workgroup: all rows' lengths together are cut into pieces of
 // about equal size, so that a batch of one long row and many short ones keeps the device as
 // busy as an even one.  Units of a piece, for all rows' `total`, which stays below 2^31
-// (checked on the host):
-__device__ __forceinline__ int piece_units(const AttnParams &p, int total) {
-  const int least = (total + p.workers - 1) / p.workers;
-  return max(max(least, min((total + p.prefer - 1) / p.prefer, p.enough)), 2);
+// (checked on the host).  Pieces of few rounds of workgroups are halved where rows are uneven, `longest`
+// more than 1.25 times their mean: b100 0 to 2000 keys 32 + 8 heads N128 108 -> 94 us, b40 0 to
+// 6000 keys 16 + 2 heads N256 62 -> 52; of even rows those would slow down, b64 4000 keys
+// N256 fp32 109 and 121.
+__device__ __forceinline__ int piece_units(const AttnParams &p, int total, int longest) {
+  const int least = (total + p.workers - 1) / p.workers, one = (total + p.prefer - 1) / p.prefer;
+  const bool halve = one < 2 * p.enough && (int64_t)longest * p.b > total + (int64_t)total / 4;
+  return max(max(least, min(one, halve ? (p.enough + 1) / 2 : p.enough)), 2);
 }
 // Pieces of a row of u units: a rest of up to a quarter of a piece is spread over the others.
 __device__ __forceinline__ int pieces_of(int u, int size) {
   return u == 0 ? 0 : max((u + size - 1 - size / 4) / size, 1);
 }
-// Piece `slot` of the list; false behind its end.  sh: 11 words of LDS.
+// Piece `slot` of the list; false behind its end.  sh: 19 words of LDS.
 template <int THREADS>
 __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh, Piece *pc) {
   if (p.workers == 1) {
@@ -87,7 +101,7 @@ __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh,
     if (lane < p.b) row = row_of(p, lane);
     const int u = row.units();
     const int total = __builtin_amdgcn_readlane(wave_incl_scan_i(u), 63);
-    const int size = piece_units(p, total);
+    const int size = piece_units(p, total, wave_max_i(u));
     const int cnt = pieces_of(u, size), end = wave_incl_scan_i(cnt);
     const uint64_t m = __builtin_amdgcn_ballot_w64(end > slot);
     if (m == 0) return false;
@@ -102,15 +116,18 @@ __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh,
   }
   // each thread a run of rows
   const int per = (p.b + THREADS - 1) / THREADS, i0 = min(tid * per, p.b), i1 = min(i0 + per, p.b);
-  int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += row_of(p, i).units();
-  sum = wave_incl_scan_i(sum);
-  if (lane == 63) sh[tid >> 6] = sum;
+  int sum = 0, longest = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int u = row_of(p, i).units();
+    sum += u, longest = max(longest, u);
+  }
+  sum = wave_incl_scan_i(sum), longest = wave_max_i(longest);
+  if (lane == 63) sh[tid >> 6] = sum, sh[11 + (tid >> 6)] = longest;
   __syncthreads();
   int total = 0;
-  for (int w = 0; w < THREADS / 64; ++w) total += sh[w];
+  for (int w = 0; w < THREADS / 64; ++w) total += sh[w], longest = max(longest, sh[11 + w]);
   __syncthreads();
-  const int size = piece_units(p, total);
+  const int size = piece_units(p, total, longest);
   int cnt = 0;
   for (int i = i0; i < i1; ++i) cnt += pieces_of(row_of(p, i).units(), size);
   const int incl = wave_incl_scan_i(cnt);

@@ -81,7 +81,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   using KW = KSwizzle<NP>;
   using VW = VSwizzle<NP>;
   __shared__ __align__(16) __bf16 ktile[2][kTK * NP], vtile[3][kTK * NP]; // vtile[2]: zeros
-  __shared__ int sh[11];
+  __shared__ int sh[19];
 
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
