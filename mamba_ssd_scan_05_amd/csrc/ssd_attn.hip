@@ -550,7 +550,7 @@ void attn_slots(AttnParams *p) {
     return;
   }
   const int64_t total = (int64_t)p->b * ((keys + kAttnUnit - 1) / kAttnUnit + 1);
-  // largest pieces, or twice as many where uneven rows' are halved (below 2 * prefer then)
+  // of the largest pieces, or twice as many (below 4 * prefer) where uneven rows halve them
   int64_t n = (total + p->enough - 1) / p->enough;
   const int64_t halved = 2 * n < 4 * (int64_t)p->prefer ? 2 * n : 4 * (int64_t)p->prefer;
   if (n < halved) n = halved;

@@ -143,3 +143,13 @@ def test_a_long_row_among_a_thousand(dtype):
     starts = [4500 if i == 700 else 20 + i % 30 for i in range(1030)]
     t = Batch(starts, [1] * 1030, 1, 8, 8, 16, 16, dtype, seed=6, spare=0)
     some(t, [0, 1, 699, 700, 701, 1029], step=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b", [6, 70])
+def test_pieces_of_uneven_rows(b, dtype):
+    # as many keys as make pieces of few rounds: those of uneven rows are halved
+    top = 5500 if b == 6 else 450
+    starts = [top * (i % 6 + 1) // 6 - 1 if i % 6 else 2 * top - 1 for i in range(b)]
+    t = Batch(starts, [1] * b, 1, 16, 8, 256, 64, dtype, seed=7, spare=0)
+    some(t, sorted({0, 1, 5, b // 2, b - 1}), step=True)
