@@ -499,8 +499,8 @@ constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
 } // namespace
 
 // More than one tile of query vectors in bf16 goes to attn_rows_kernel, which reads K and V
-// once for 256 (128) of them: b4, 8 new tokens behind 8000, 32 + 8 heads N128 40 us, by two
-// tiles of 16 here 47; 16 tokens 43 and 86.
+// once for 256 (128) of them: b4, 8 new tokens behind 8000, 32 + 8 heads N128 41 us, by two
+// tiles of 16 here 47; 16 tokens 44 and 86.
 //
 // Pieces: as many as run at once (512 workgroups, 256 of wide heads; with twice as many b8
 // 2047 keys 20.6 us, so 18.3), but none larger than a MB of keys and values while there are
