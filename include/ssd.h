@@ -629,8 +629,9 @@ int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk,
  * (NaN and infinities among it).  One or several new tokens a row, prompts and pieces
  * of prompts: any L.  Rows of any lengths share the device evenly.
  * Arithmetic: scores, maxima, sums and outputs in fp32; with bf16 inputs
- * the weights e^{s - m} are rounded to bf16 for the product with the values (2^-8
- * of each); out is rounded once.  The sums of weighted values, weights up to 4, have to
+ * the weights e^{s - m} are held to 1.25 2^-15 of each for the product with the values, and
+ * to 2^-8 (one bf16) where a row has more than 16 query vectors L Hq / Hk of a key head; out
+ * is rounded once.  The sums of weighted values, weights up to 4, have to
  * stay in fp32's range.  Results do not vary from run to run; a row's do depend, to
  * rounding, on the other rows' lengths, the table's width and the window (which say
  * where it is cut).  out and lse may not overlap any other argument.

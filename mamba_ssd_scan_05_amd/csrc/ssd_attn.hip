@@ -302,9 +302,21 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
     if (!full && __builtin_amdgcn_ballot_w64(odd) != 0) {
       left_out = true; // added behind the loop
     } else if constexpr (ES == 2) {
-      // O^T += V^T P^T; P rounded to bf16: half a step of it, 2^-8 of each weight, less
-      // than the output's own rounding where values of one size are averaged
-      const FragBF pf = pack8<__bf16>(w);
+      // O^T += V^T P^T, P as the sum of two bf16 parts: off by 1.25 2^-15 of each weight (one
+      // rounded part: 2^-8, which the output's rounding does not hide: error against 64 bits
+      // 0.0017 of the output's norm, two 0.0016).  HBM bounds these calls, so the second
+      // product costs little: b128 rows of up to 16384 keys 779 us, by one part 778, b8 2047
+      // keys 18.7 and 18.5, b64 a window of 2048 keys 10 + 1 heads N256 31.5 and 31.1.
+      // The first part is w cut off a quarter of bf16's last place below it, so that what is
+      // left is above 0 where w is, and takes an infinity in V to the same side.
+      float w1[8], w2[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = __builtin_elementwise_sub_sat(__builtin_bit_cast(uint32_t, w[e]), 0x4000u) & 0xFFFF0000u;
+        w1[e] = __builtin_bit_cast(float, u);
+        w2[e] = w[e] - w1[e];
+      }
+      const FragBF pf = pack8<__bf16>(w1), pr = pack8<__bf16>(w2);
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
         FragBF vf;
@@ -314,7 +326,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
                                                 (__attribute__((address_space(3))) lds_bf16x4 *)(a)));
         };
         vf.v = __builtin_shufflevector(tr(0), tr(16), 0, 1, 2, 3, 4, 5, 6, 7);
-        o[d] = mma(vf, pf, o[d]);
+        o[d] = mma(vf, pr, mma(vf, pf, o[d]));
       }
     } else {
 #pragma unroll
