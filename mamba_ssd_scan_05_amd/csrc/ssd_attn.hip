@@ -415,6 +415,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
       const int tq = (int)div_by((uint32_t)(r0 + q), p.group), hq = hk * p.G + r0 + q - tq * p.G;
       const int64_t at = ((int64_t)pc.i * p.L + tq) * p.Hq + hq;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      if (sum == 0.f) acc = f32x4{0.f, 0.f, 0.f, 0.f}; // (0 times an infinity in V among them)
       st4<T>((T *)p.out + at * p.N + c, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
       if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
     } else {
@@ -476,6 +477,7 @@ template <typename T, int WPV> __global__ __launch_bounds__(kThreads) void attn_
   }
   const int64_t at = (int64_t)vt * p.Hq + h;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (sum == 0.f) acc = f32x4{0.f, 0.f, 0.f, 0.f};
   st4<T>((T *)p.out + at * p.N + c4, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
   if (p.lse && tid == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + hw_log2(sum)) * kLn2;
 }

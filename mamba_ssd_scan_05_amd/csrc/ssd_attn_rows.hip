@@ -487,6 +487,11 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   if (pc.count == 1) {
     const int64_t at = ((int64_t)pc.i * p.L + t) * p.Hq + h;
     const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (l == 0.f) // no key, or weights of 0 only, whatever V holds (0 times an infinity)
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
     __bf16 *const dst = (__bf16 *)p.out + at * p.N;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
