@@ -30,9 +30,13 @@ template <typename T, bool VEC> __device__ __forceinline__ void move8(T *lo, T *
     uint16_t *a = reinterpret_cast<uint16_t *>(lo), *b = reinterpret_cast<uint16_t *>(hi);
 #pragma unroll
     for (int e = 0; e < 4; ++e) a[e] = (uint16_t)(r.d[e] >> 16), b[e] = (uint16_t)(r.d[4 + e] >> 16);
-  } else {
+  } else if constexpr (VEC) {
     *reinterpret_cast<u32x4 *>(lo) = u32x4{r.d[0], r.d[1], r.d[2], r.d[3]};
     *reinterpret_cast<u32x4 *>(hi) = u32x4{r.d[4], r.d[5], r.d[6], r.d[7]};
+  } else {
+    uint32_t *a = reinterpret_cast<uint32_t *>(lo), *b = reinterpret_cast<uint32_t *>(hi);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = r.d[e], b[e] = r.d[4 + e];
   }
 }
 
