@@ -606,7 +606,7 @@ int ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *v,
 /* Workspace bytes of ssd_attn_fwd (and, with L = 1, of ssd_attn_step), see
  * Workspace above; 0 where none is needed, -1 for sizes they refuse.  Host only.
  * It does not depend on the cache or on the rows' lengths, and suffices for either
- * dtype. */
+ * dtype.  At most about 220 MB. */
 int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk,
                            int64_t N);
 
@@ -627,7 +627,8 @@ int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk,
  * A query that sees no key, or only scores of -infinity, has out 0 and lse
  * -infinity.  Keys that a query does not see do not reach it, whatever they hold
  * (NaN and infinities among it).  One or several new tokens a row, prompts and pieces
- * of prompts: any L.  Rows of any lengths share the device evenly.
+ * of prompts: any L.  Rows of any lengths share the device evenly (below half a million
+ * workgroups b * Hk * ceil(L * Hq / Hk / 16); above, a row is not spread over several).
  * Arithmetic: scores, maxima, sums and outputs in fp32; with bf16 inputs
  * the weights e^{s - m} are held to 1.25 2^-15 of each for the product with the values, and
  * to 2^-8 (one bf16) where a row has more than 16 query vectors L Hq / Hk of a key head; out

@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   constexpr int kTile = TK * NP * ES, kJoin = 16 * LO * 4;
   __shared__ __align__(16) char lds[kWaves * (kTile > kJoin ? kTile : kJoin)];
   __shared__ float2 ml[kWaves][16];
-  __shared__ int sh[19];
+  __shared__ int sh[12];
 
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -92,8 +92,8 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   Piece pc;
   if (!piece_of<kThreads>(p, slot, sh, &pc)) return;
   const Row row = pc.row;
-  if (p.workers > 1 && pc.index == 0 && hk == 0 && tile == 0 && threadIdx.x == 0)
-    p.pieces[pc.i] = make_int2(pc.first, pc.count);
+  if (p.workers > 1 && !p.list && pc.index == 0 && hk == 0 && tile == 0 && threadIdx.x == 0)
+    p.pieces[pc.i] = make_int2(pc.place, pc.count);
   const int nrows = row.n * p.G, r0 = tile * kRows;
   if (r0 >= nrows) return;
 
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   if (lg == 0) ml[wave][li] = make_float2(m, l);
   __syncthreads();
   const bool whole = pc.count == 1;
-  const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * p.prow;
+  const int64_t pr = (((int64_t)pc.place * p.Hk + hk) * p.tiles + tile) * p.prow;
   for (int x = threadIdx.x; x < 16 * (NP / 4); x += kThreads) {
     const int q = x / (NP / 4), c = x % (NP / 4) * 4;
     if (r0 + q >= nrows || c >= p.N) continue;
@@ -425,10 +425,60 @@ __global__ __launch_bounds__(kThreads, NP <= 128 ? 2 : 1) void attn_kernel(AttnP
   }
 }
 
+// The plan of a batch of many rows, by one workgroup: p.list and p.cut.  Every workgroup for
+// itself would read all rows (b60000 of 200 keys, one head N64: 27 ms, so 0.52; b1024 8 heads 138 us and 91).
+constexpr int kPlanThreads = 1024, kPlanRows = 4; // rows of a thread at once
+__global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnParams p) {
+  constexpr int kW = kPlanThreads / 64;
+  __shared__ int sh[2][kW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int total = 0, longest = 0;
+#pragma unroll 4
+  for (int i = tid; i < p.b; i += kPlanThreads) {
+    const int u = row_of(p, i).units();
+    total += u, longest = max(longest, u);
+  }
+  total = wave_incl_scan_i(total), longest = wave_max_i(longest);
+  if (lane == 63) sh[0][wave] = total, sh[1][wave] = longest;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < kW; ++w) total += sh[0][w], longest = max(longest, sh[1][w]);
+  const int size = piece_units(p, total, longest);
+  // Pieces before a row, and in one word of 16 bits each the places and the cut rows before it
+  int pieces = 0, stored = 0;
+  for (int i0 = 0; i0 < p.b; i0 += kPlanThreads * kPlanRows) {
+    int cnt[kPlanRows], c = 0, s = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanRows; ++k) {
+      const int i = i0 + tid * kPlanRows + k;
+      cnt[k] = i < p.b ? pieces_of(row_of(p, i).units(), size) : 0;
+      c += cnt[k], s += places_of(cnt[k]) | (cnt[k] > 1) << 16;
+    }
+    const int ce = wave_incl_scan_i(c), se = wave_incl_scan_i(s);
+    __syncthreads();
+    if (lane == 63) sh[0][wave] = ce, sh[1][wave] = se;
+    __syncthreads();
+    int at = pieces + ce - c, st = stored + se - s;
+    for (int w = 0; w < kW; ++w) {
+      if (w < wave) at += sh[0][w], st += sh[1][w];
+      pieces += sh[0][w], stored += sh[1][w];
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanRows; ++k) {
+      const int i = i0 + tid * kPlanRows + k;
+      for (int x = 0; x < cnt[k]; ++x) p.list[at++] = make_int4(i, x, cnt[k], (st & 0xFFFF) + x);
+      if (cnt[k] > 1) p.cut[st >> 16] = make_int4(i, st & 0xFFFF, cnt[k], 0), st += cnt[k] | 1 << 16;
+    }
+  }
+  for (int x = pieces + tid; x < p.slots; x += kPlanThreads) p.list[x] = make_int4(-1, 0, 0, 0);
+  for (int x = (stored >> 16) + tid; x < p.cuts; x += kPlanThreads) p.cut[x] = make_int4(-1, 0, 0, 0);
+}
+
 // Joins the pieces of the rows that have more than one: WPV waves an output vector, N / 4
 // threads a piece, as many pieces at once as that leaves, each group of threads with its
 // own running maximum (a maximum over all pieces first would be one more wait for memory).
-template <typename T, int WPV> __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnParams p) {
+// LIST: of the rows in p.cut, otherwise of all rows.
+template <typename T, int WPV, bool LIST> __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnParams p) {
   __shared__ float acc_sh[kThreads][4];
   __shared__ float2 ml_sh[kThreads];
   constexpr int TPV = 64 * WPV; // threads of a vector
@@ -436,9 +486,16 @@ template <typename T, int WPV> __global__ __launch_bounds__(kThreads) void attn_
   const uint32_t vec = blockIdx.x * (kThreads / TPV) + threadIdx.x / TPV;
   const uint32_t vt = vec / (uint32_t)p.Hq;
   const int h = (int)(vec - vt * (uint32_t)p.Hq);
-  const int i = (int)(vt / (uint32_t)p.L), t = (int)(vt - (uint32_t)i * (uint32_t)p.L);
+  int i = (int)(vt / (uint32_t)p.L);
+  const int t = (int)(vt - (uint32_t)i * (uint32_t)p.L);
   int2 pc = make_int2(0, 0);
-  if (i < p.b && (!p.c.tokens || t < p.c.tokens[i])) pc = p.pieces[i];
+  if constexpr (LIST) {
+    const int4 e = i < p.cuts ? p.cut[i] : make_int4(-1, 0, 0, 0);
+    i = e.x;
+    if (i >= 0 && (!p.c.tokens || t < p.c.tokens[i])) pc = make_int2(e.y, e.z);
+  } else {
+    if (i < p.b && (!p.c.tokens || t < p.c.tokens[i])) pc = p.pieces[i];
+  }
   const bool mine = pc.y > 1;
   const int hk = (int)div_by((uint32_t)h, p.group), r = t * p.G + h - hk * p.G;
   const int tile = r / p.rows;
@@ -475,7 +532,7 @@ template <typename T, int WPV> __global__ __launch_bounds__(kThreads) void attn_
     sum = fmaf(w, e.y, sum);
     acc += w * *reinterpret_cast<const f32x4 *>(acc_sh[first_tid + k * nv + tid]);
   }
-  const int64_t at = (int64_t)vt * p.Hq + h;
+  const int64_t at = ((int64_t)i * p.L + t) * p.Hq + h;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   if (sum == 0.f) acc = f32x4{0.f, 0.f, 0.f, 0.f};
   st4<T>((T *)p.out + at * p.N + c4, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
@@ -487,7 +544,20 @@ template <typename T, int NP> void launch_np(const AttnParams &p, hipStream_t st
   if (p.c.page.d % 16 == 0) attn_kernel<T, NP, true><<<grid, kThreads, 0, st>>>(p);
   else attn_kernel<T, NP, false><<<grid, kThreads, 0, st>>>(p);
 }
+template <typename T, bool LIST> hipError_t launch_join(const AttnParams &p, hipStream_t st) {
+  const int64_t vecs = (int64_t)(LIST ? p.cuts : p.b) * p.L * p.Hq;
+  // a wave each where they fill the device: b3 L777 5 heads N96 fp32 43.8 us, four 49.2; fewer
+  // vectors wait longer for their pieces: b1 262143 keys 32 heads 203 us, with four waves 197
+  if (vecs >= 4096) attn_join_kernel<T, 1, LIST><<<(uint32_t)((vecs + 3) / 4), kThreads, 0, st>>>(p);
+  else attn_join_kernel<T, 4, LIST><<<(uint32_t)vecs, kThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
 template <typename T> hipError_t launch_t(const AttnParams &p, hipStream_t st) {
+  if (p.list) {
+    attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   if (p.rows != kRows) {
     const hipError_t e = launch_attn_rows(p, st);
     if (e != hipSuccess) return e;
@@ -499,16 +569,21 @@ template <typename T> hipError_t launch_t(const AttnParams &p, hipStream_t st) {
   else launch_np<T, 256>(p, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.workers == 1) return e;
-  const int64_t vecs = (int64_t)p.b * p.L * p.Hq;
-  // a wave each where they fill the device: b3 L777 5 heads N96 fp32 43.8 us, four 49.2; fewer
-  // vectors wait longer for their pieces: b1 262143 keys 32 heads 203 us, with four waves 197
-  if (vecs >= 4096) attn_join_kernel<T, 1><<<(uint32_t)((vecs + 3) / 4), kThreads, 0, st>>>(p);
-  else attn_join_kernel<T, 4><<<(uint32_t)vecs, kThreads, 0, st>>>(p);
-  return hipGetLastError();
+  return p.list ? launch_join<T, true>(p, st) : launch_join<T, false>(p, st);
 }
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
+constexpr int64_t kMaxCut = (int64_t)1 << 19;    // without pieces, from which on there are none
+
+// n sizes of units in all rows together, at most: the pieces, their places and the cut rows.
+void set_pieces(AttnParams *p, int64_t n) {
+  const int64_t places = 8 * n / 5;
+  p->slots = (int)n + p->b;
+  p->stores = places < p->slots ? (int)places : p->slots;
+  p->cuts = p->stores / 2 < p->b ? p->stores / 2 : p->b;
+}
+void uncut(AttnParams *p) { p->workers = 1, p->slots = p->b, p->stores = p->cuts = 0; }
 
 } // namespace
 
@@ -520,8 +595,9 @@ constexpr int64_t kMaxGroups = (int64_t)1 << 23; // workgroups of one launch
 // 2047 keys 20.6 us, so 18.3), but none larger than a MB of keys and values while there are
 // fewer than 4096 workgroups (b128 rows of 0 to 16384 keys: 1024 929 us, 2048 844, 4096 796;
 // with one row of 262143 keys 199, 211 and 232, since a workgroup costs 8 us before its
-// first key).  8192 workgroups and more get no pieces, whose sums would take GBs; one tile of
-// 16, whose sums are small, gets them up to 65536.
+// first key).  Only cut rows' pieces have sums, at most 1.6 times as many as that and the heads once
+// more: 100 to 220 MB, whatever the batch (as many as pieces and rows b127 L512 32 heads N128 had
+// 1.1 GB).  From half a million workgroups on, 1000 rounds of the device, rows are not cut.
 int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t vecs = (int64_t)p->L * p->G;
   const bool wide = dtype == 1 && vecs > kRows;
@@ -529,16 +605,20 @@ int64_t attn_plan(AttnParams *p, int dtype) {
   const int64_t tiles = (vecs + p->rows - 1) / p->rows, heads = p->Hk * tiles;
   p->tiles = (int)tiles;
   const int64_t prefer = wide ? 512 : p->N <= 128 ? 512 : 256, most = wide ? 512 : 4096;
-  p->workers = heads * p->b >= (wide || tiles > 1 ? 8192 : 65536) ? 1 : (int)((most + heads - 1) / heads);
+  p->workers = heads * p->b >= kMaxCut ? 1 : (int)((most + heads - 1) / heads);
   p->prefer = (int)((prefer + heads - 1) / heads);
   p->enough = (int)((1 << 20) / (2 * kAttnUnit * p->N * (dtype == 1 ? 2 : 4)));
   if (p->enough < 2) p->enough = 2;
-  p->slots = p->workers == 1 ? p->b : p->workers + p->b;
   p->prow = (int)(vecs < p->rows ? vecs : p->rows);
-  if (p->slots * heads > kMaxGroups) return -1;
-  if (p->workers == 1) return 0;
-  const int64_t rows = p->slots * heads * p->prow;
-  return up256(rows * p->N * 4) + up256(rows * 8) + up256((int64_t)p->b * 8);
+  if (heads * p->b > kMaxGroups) return -1;
+  if (p->workers == 1) {
+    uncut(p);
+    return 0;
+  }
+  set_pieces(p, p->workers);
+  const int64_t rows = p->stores * heads * p->prow;
+  return up256(rows * p->N * 4) + up256(rows * 8) +
+         up256((int64_t)p->slots * 16) + up256((int64_t)p->cuts * 16); // (or 8 b)
 }
 
 // Pieces that there can be with this table and window: a row has no more units than its
@@ -559,10 +639,8 @@ void attn_slots(AttnParams *p) {
   int64_t keys = p->c.capacity;
   if (p->window && p->window + p->L < keys) keys = p->window + p->L;
   const int64_t groups = (int64_t)p->Hk * p->tiles * p->b;
-  if (p->tiles > 1 ? groups >= 512 && keys <= 4 * (groups / 512) * p->L : groups >= 8192 && keys <= 4096) {
-    p->workers = 1, p->slots = p->b;
-    return;
-  }
+  if (p->tiles > 1 ? groups >= 512 && keys <= 4 * (groups / 512) * p->L : groups >= 8192 && keys <= 4096)
+    return uncut(p);
   const int64_t total = (int64_t)p->b * ((keys + kAttnUnit - 1) / kAttnUnit + 1);
   // of the largest pieces, or twice as many (below 4 * prefer) where uneven rows halve them
   int64_t n = (total + p->enough - 1) / p->enough;
@@ -571,15 +649,30 @@ void attn_slots(AttnParams *p) {
   if (n < p->prefer) n = p->prefer;
   if (n > (total + 1) / 2) n = (total + 1) / 2;
   if (n > p->workers) n = p->workers;
-  p->slots = (int)n + p->b;
+  if (n == 1) return uncut(p);
+  set_pieces(p, n);
 }
 
 void attn_workspace(AttnParams *p, void *workspace) {
-  const int64_t rows = (int64_t)p->slots * p->Hk * p->tiles * p->prow;
+  if (p->workers == 1) return;
+  const int64_t rows = (int64_t)p->stores * p->Hk * p->tiles * p->prow;
   char *w = (char *)workspace;
   p->part = (float *)w;
-  p->part_ml = (float2 *)(w + up256(rows * p->N * 4));
-  p->pieces = (int2 *)(w + up256(rows * p->N * 4) + up256(rows * 8));
+  w += up256(rows * p->N * 4);
+  p->part_ml = (float2 *)w;
+  w += up256(rows * 8);
+  // The plan by a kernel of its own (3 us) for more rows than a workgroup has threads for (b300 0 to 200
+  // keys 16 + 4 heads N128 31 us, by every workgroup for itself 37; b128 1000 keys 8 + 2 heads N64 23.4
+  // and 19.4), among several tokens, whose workgroups are few and long, than a wave has lanes (b128 L8 0 to
+  // 2000 keys 32 + 8 heads N128 182 us and 185).  Also where few of the rows can be cut, of so many vectors that
+  // it costs less than to start the join for all (fp32 b256 L20 0 to 2000 keys 1195 us and 1228).
+  if (p->b > (p->rows == kRows ? kThreads : 64) ||
+      (2 * p->cuts <= p->b && (int64_t)p->b * p->L * p->Hq >= 65536)) {
+    p->list = (int4 *)w;
+    p->cut = (int4 *)(w + up256((int64_t)p->slots * 16));
+  } else {
+    p->pieces = (int2 *)w;
+  }
 }
 
 hipError_t launch_attn(int dtype, const AttnParams &p, hipStream_t st) {

@@ -67,7 +67,7 @@ __device__ __forceinline__ Row row_of(const AttnParams &p, int i) {
 
 // A piece: the `index`th of `count` of row i.
 struct Piece {
-  int i, index, count, first; // first: the row's first piece
+  int i, index, count, place; // place: its own in p.part, if the row has more pieces
   Row row;
   // units of each of the row's pieces
   __device__ __forceinline__ int size() const { return count == 1 ? INT32_MAX : (row.units() + count - 1) / count; }
@@ -88,69 +88,76 @@ __device__ __forceinline__ int piece_units(const AttnParams &p, int total, int l
 __device__ __forceinline__ int pieces_of(int u, int size) {
   return u == 0 ? 0 : max((u + size - 1 - size / 4) / size, 1);
 }
-// Piece `slot` of the list; false behind its end.  sh: 19 words of LDS.
-template <int THREADS>
+// Places in p.part are given to rows of more than one piece only.  Such a row has more than 1.25
+// sizes of units and, its rest spread, less than 0.75 more pieces than sizes: 1.6 times
+// as many places as there are sizes in all the rows are enough, whatever the batch.
+__device__ __forceinline__ int places_of(int cnt) { return cnt > 1 ? cnt : 0; }
+
+// Piece `slot`; false behind the last.  ROWS: the rows up to which a workgroup makes the plan for
+// itself, 64 or as many as threads; sh: 12 words of LDS for more than 64.  Counts of pieces and of places are
+// added up in one word, 16 bits each (at most 4096 + 256 and 1.6 * 4096).
+template <int ROWS>
 __device__ __forceinline__ bool piece_of(const AttnParams &p, int slot, int *sh, Piece *pc) {
   if (p.workers == 1) {
     *pc = Piece{slot, 0, 1, slot, row_of(p, slot)}; // slots = b
     return true;
   }
+  if (p.list) {
+    const int4 e = p.list[slot];
+    const int i = __builtin_amdgcn_readfirstlane(e.x);
+    if (i < 0) return false;
+    *pc = Piece{i, __builtin_amdgcn_readfirstlane(e.y), __builtin_amdgcn_readfirstlane(e.z),
+                __builtin_amdgcn_readfirstlane(e.w), row_of(p, i)};
+    return true;
+  }
   const int tid = threadIdx.x, lane = tid & 63;
-  if (p.b <= 64) { // every wave by itself
+  if (p.b <= 64) { // every wave by itself, a row a lane
     Row row{};
     if (lane < p.b) row = row_of(p, lane);
     const int u = row.units();
     const int total = __builtin_amdgcn_readlane(wave_incl_scan_i(u), 63);
     const int size = piece_units(p, total, wave_max_i(u));
-    const int cnt = pieces_of(u, size), end = wave_incl_scan_i(cnt);
-    const uint64_t m = __builtin_amdgcn_ballot_w64(end > slot);
+    const int cnt = pieces_of(u, size), end = wave_incl_scan_i(cnt | places_of(cnt) << 16);
+    const uint64_t m = __builtin_amdgcn_ballot_w64((end & 0xFFFF) > slot);
     if (m == 0) return false;
     const int i = (int)__builtin_ctzll(m);
-    const int c = __builtin_amdgcn_readlane(cnt, i), f = __builtin_amdgcn_readlane(end, i) - c;
-    *pc = Piece{i, slot - f, c, f, row};
+    const int c = __builtin_amdgcn_readlane(cnt, i), e = __builtin_amdgcn_readlane(end, i);
+    const int index = slot - ((e & 0xFFFF) - c);
+    *pc = Piece{i, index, c, (e >> 16) - places_of(c) + index, row};
     pc->row.n = __builtin_amdgcn_readlane(row.n, i);
     pc->row.lo = __builtin_amdgcn_readlane(row.lo, i);
     pc->row.hi = __builtin_amdgcn_readlane(row.hi, i);
     pc->row.start = __builtin_amdgcn_readlane(row.start, i);
     return true;
   }
-  // each thread a run of rows
-  const int per = (p.b + THREADS - 1) / THREADS, i0 = min(tid * per, p.b), i1 = min(i0 + per, p.b);
-  int sum = 0, longest = 0;
-  for (int i = i0; i < i1; ++i) {
-    const int u = row_of(p, i).units();
-    sum += u, longest = max(longest, u);
-  }
-  sum = wave_incl_scan_i(sum), longest = wave_max_i(longest);
-  if (lane == 63) sh[tid >> 6] = sum, sh[11 + (tid >> 6)] = longest;
+  if constexpr (ROWS <= 64) return false; // not reached, more rows have the list
+  // a row a thread
+  constexpr int kW = ROWS / 64;
+  static_assert(ROWS % 64 == 0 && kW <= 4, "waves of a workgroup of ROWS threads");
+  Row row{};
+  if (tid < p.b) row = row_of(p, tid);
+  const int u = row.units(), sum = wave_incl_scan_i(u);
+  int longest = wave_max_i(u);
+  if (lane == 63) sh[tid >> 6] = sum, sh[4 + (tid >> 6)] = longest;
   __syncthreads();
   int total = 0;
-  for (int w = 0; w < THREADS / 64; ++w) total += sh[w], longest = max(longest, sh[11 + w]);
+  for (int w = 0; w < kW; ++w) total += sh[w], longest = max(longest, sh[4 + w]);
   __syncthreads();
-  const int size = piece_units(p, total, longest);
-  int cnt = 0;
-  for (int i = i0; i < i1; ++i) cnt += pieces_of(row_of(p, i).units(), size);
-  const int incl = wave_incl_scan_i(cnt);
-  if (lane == 63) sh[tid >> 6] = incl;
+  const int size = piece_units(p, total, longest), cnt = pieces_of(u, size);
+  int end = wave_incl_scan_i(cnt | places_of(cnt) << 16);
+  if (lane == 63) sh[tid >> 6] = end;
   if (tid == 0) sh[8] = -1;
   __syncthreads();
-  int before = incl - cnt;
-  for (int w = 0; w < (tid >> 6); ++w) before += sh[w];
+  for (int w = 0; w < (tid >> 6); ++w) end += sh[w];
+  const int before = (end & 0xFFFF) - cnt;
   if (slot >= before && slot < before + cnt)
-    for (int i = i0; i < i1; ++i) {
-      const int c = pieces_of(row_of(p, i).units(), size);
-      if (slot < before + c) {
-        sh[8] = i, sh[9] = before, sh[10] = c;
-        break;
-      }
-      before += c;
-    }
+    sh[8] = tid, sh[9] = before, sh[10] = cnt, sh[11] = (end >> 16) - places_of(cnt);
   __syncthreads();
   const int i = __builtin_amdgcn_readfirstlane(sh[8]), f = __builtin_amdgcn_readfirstlane(sh[9]),
-            c = __builtin_amdgcn_readfirstlane(sh[10]);
+            c = __builtin_amdgcn_readfirstlane(sh[10]), at = __builtin_amdgcn_readfirstlane(sh[11]);
   __syncthreads();
   if (i < 0) return false;
-  *pc = Piece{i, slot - f, c, f, row_of(p, i)};
+  *pc = Piece{i, slot - f, c, at + slot - f, row_of(p, i)};
   return true;
 }
 

@@ -81,17 +81,16 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
   using KW = KSwizzle<NP>;
   using VW = VSwizzle<NP>;
   __shared__ __align__(16) __bf16 ktile[2][kTK * NP], vtile[3][kTK * NP]; // vtile[2]: zeros
-  __shared__ int sh[19];
 
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tile, hk, slot;
   place_of(p, blockIdx.x, &tile, &hk, &slot);
   Piece pc;
-  if (!piece_of<64 * W>(p, slot, sh, &pc)) return;
+  if (!piece_of<64>(p, slot, nullptr, &pc)) return;
   const Row row = pc.row;
-  if (p.workers > 1 && pc.index == 0 && hk == 0 && tile == 0 && threadIdx.x == 0)
-    p.pieces[pc.i] = make_int2(pc.first, pc.count);
+  if (p.workers > 1 && !p.list && pc.index == 0 && hk == 0 && tile == 0 && threadIdx.x == 0)
+    p.pieces[pc.i] = make_int2(pc.place, pc.count);
   const int nrows = row.n * p.G, r0 = tile * kRows;
   if (r0 >= nrows) return;
 
@@ -503,7 +502,7 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
       }
     if (p.lse && half == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + hw_log2(l)) * kLn2;
   } else {
-    const int64_t pr = (((int64_t)slot * p.Hk + hk) * p.tiles + tile) * p.prow + r - r0;
+    const int64_t pr = (((int64_t)pc.place * p.Hk + hk) * p.tiles + tile) * p.prow + r - r0;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll

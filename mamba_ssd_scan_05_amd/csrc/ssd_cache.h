@@ -76,13 +76,17 @@ struct AttnParams {
   int workers;                      // pieces of all rows' lengths together, at most; 1: one piece a row
   int prefer, enough;               // as many, but no larger than `enough` units, if workers allows
   int slots;                        // pieces at most
+  int stores, cuts;                 // pieces of rows that have more than one, and such rows, at most
   int rows, tiles;                  // query vectors of a tile, tiles of a row and key head
   int prow;                         // query vectors of a tile that may be there
-  float *part;                      // [slots, Hk, tiles, prow, N], products' sums
-  float2 *part_ml;                  // [slots, Hk, tiles, prow], maximum and sum
-  int2 *pieces;                     // [b]: a row's first piece and how many
+  float *part;                      // [stores, Hk, tiles, prow, N], products' sums
+  float2 *part_ml;                  // [stores, Hk, tiles, prow], maximum and sum
+  int2 *pieces;                     // [b]: the place in part of a row's first piece, and how many it has
+  int4 *list;                       // [slots]: row (-1: none), index, count, place; null: every workgroup
+                                    // makes the plan for itself
+  int4 *cut;                        // [cuts], with list: row (-1: none), first place, count
 };
-// Fills workers, slots, rows and tiles; workspace bytes, -1 if the call is too large.
+// Fills workers, slots, stores, cuts, rows and tiles; workspace bytes, -1 if the call is too large.
 int64_t attn_plan(AttnParams *p, int dtype);
 // Many query vectors of a row and key head, bf16 (ssd_attn_rows.hip); query vectors of its tile.
 int attn_rows(int N);
