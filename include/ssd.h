@@ -621,7 +621,7 @@ int64_t ssd_attn_workspace(int64_t b, int64_t L, int64_t Hq, int64_t Hk,
  *   q    [b, L, Hq, N]  f32 or bf16; views allowed as for ssd_kv_append
  *   out  [b, L, Hq, N]  dtype of q, dense, 16-byte aligned, written
  *   lse  [b, L, Hq]     f32, written                           NULL => skip
- *   scale               finite, not 0 (1 / sqrt(N) is usual); may be negative
+ *   scale               2^-126 to 1e30 in size (1 / sqrt(N) is usual); may be negative
  *   window              0 => all keys
  *
  * A query that sees no key, or only scores of -infinity, has out 0 and lse

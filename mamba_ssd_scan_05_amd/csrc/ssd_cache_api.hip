@@ -179,7 +179,7 @@ int attn(const ssd_tensor *q, const ssd_tensor *k_cache, const ssd_tensor *v_cac
     return fail(SSD_ERR_UNSUPPORTED, "problem too large: b=%lld L=%lld Hq=%lld", (long long)b, (long long)L,
                 (long long)Hq);
   if (!(fabsf(scale) >= FLT_MIN && fabsf(scale) <= 1e30f))
-    return fail(SSD_ERR_UNSUPPORTED, "scale=%g is not a finite number other than 0", (double)scale);
+    return fail(SSD_ERR_UNSUPPORTED, "scale=%g is not in size between 2^-126 and 1e30", (double)scale);
   if (window < 0) return fail(SSD_ERR_UNSUPPORTED, "window=%lld is negative", (long long)window);
   SSD_CHECK(act_dtype(q, "q"));
   AttnParams p{};

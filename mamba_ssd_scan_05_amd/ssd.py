@@ -578,8 +578,15 @@ def ssd_attn_workspace(b: int, L: int, Hq: int, Hk: int, N: int) -> int:
     return int(lib().ssd_attn_workspace(int(b), int(L), int(Hq), int(Hk), int(N)))
 
 
+def _attn_scale(q, scale):
+    if scale is not None:
+        return float(scale)
+    N = q.shape[-1] if q.dim() else 0
+    return N ** -0.5 if N else 1.0  # refused by the call
+
+
 def _attn_workspace(q, k_cache):
-    if q.dim() not in (3, 4) or k_cache.dim() != 4:
+    if q.dim() not in (3, 4) or k_cache is None or k_cache.dim() != 4:
         return None  # refused by the call
     b, L = (q.shape[0], 1) if q.dim() == 3 else q.shape[:2]
     return _workspace(ssd_attn_workspace(b, L, q.shape[-2], k_cache.shape[2], q.shape[-1]), q)
@@ -601,7 +608,7 @@ def ssd_attn_fwd(q, k_cache, v_cache, page_table, start, *, tokens=None, scale: 
     with _on_device(q):
         st = _stream(stream, q)
         keep, d = _descs(q, k_cache, v_cache, page_table, start, tokens, out, lse)
-        status = lib().ssd_attn_fwd(*d, q.shape[-1] ** -0.5 if scale is None else float(scale), int(window),
+        status = lib().ssd_attn_fwd(*d, _attn_scale(q, scale), int(window),
                                     ws.data_ptr() if ws is not None else None,
                                     ws.numel() if ws is not None else 0, st)
     _check(status)
@@ -620,7 +627,7 @@ def ssd_attn_step(q, k_cache, v_cache, page_table, start, *, scale: float = None
     with _on_device(q):
         st = _stream(stream, q)
         keep, d = _descs(q, k_cache, v_cache, page_table, start, out, lse)
-        status = lib().ssd_attn_step(*d, q.shape[-1] ** -0.5 if scale is None else float(scale), int(window),
+        status = lib().ssd_attn_step(*d, _attn_scale(q, scale), int(window),
                                      ws.data_ptr() if ws is not None else None,
                                      ws.numel() if ws is not None else 0, st)
     _check(status)
