@@ -559,7 +559,9 @@ def ssd_kv_append(k, v, k_cache, v_cache, page_table, start, *, q=None, freqs=No
     [pages, page_size, Hk, N], the keys turned by their positions start[i] + t
     on the way, and queries q [b, L, Hq, N] turned in the same pass (``freqs`` as
     for ssd_norm_rotate_fwd, None: not turned).  page_table [b, width], start [b]
-    and tokens [b] (None: all L) are int32.  Returns q_out (None without q)."""
+    and tokens [b] are int32; row i has tokens[i] of the L tokens (None: all).
+    Returns q_out (None without q); tokens behind a row's are not written, so a
+    q_out of this call's own holds anything there."""
     if q is not None and q_out is None:
         with _on_stream(stream, k):
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -597,8 +599,10 @@ def ssd_attn_fwd(q, k_cache, v_cache, page_table, start, *, tokens=None, scale: 
     """Attention of the new tokens q [b, L, Hq, N], at positions start[i] + t, over
     the paged caches, which hold them already (see ssd_kv_append): each sees the
     keys up to its own position, with ``window`` the last ``window`` of them.
-    scale: of the scores (default 1 / sqrt(N)).  Returns (out, lse or None), lse
-    [b, L, Hq] the logarithm of the sum of e^score."""
+    tokens [b] int32: how many of the L tokens row i has (None: all).  scale: of the
+    scores (default 1 / sqrt(N)).  Returns (out, lse or None), lse [b, L, Hq] the
+    logarithm of the sum of e^score; tokens behind a row's are not written, so an
+    out and lse of this call's own hold anything there."""
     with _on_stream(stream, q):
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
