@@ -24,9 +24,9 @@
 // Bound by HBM: b128 rows of up to 16384 keys, 32 + 8 heads N128 bf16 780 us (5.5 TB/s;
 // a large copy reaches 4.9, reading and writing), one row of 262143 keys 200 us (5.4), b32
 // 2047 keys 48 us (5.6).  Small calls by their chain of waits (start, page table, keys,
-// join): b1 1000 keys 10.3 us in a graph, of which 3.5 are two launches that do
-// nothing and 3.4 the join.  fp32 with many queries by the matrix cores and the reads of K
-// and V for every 16 rows: b1 L2048 32 + 8 heads N128 425 us, 81 TFLOP/s of the 154 that a
+// join): b1 1000 keys 10.5 us in a graph, of which 3.5 are two launches that do
+// nothing and 3.6 the join.  fp32 with many queries by the matrix cores and the reads of K
+// and V for every 16 rows: b1 L2048 32 + 8 heads N128 430 us, 80 TFLOP/s of the 154 that a
 // large product reaches.
 #include "ssd_attn_device.h"
 
@@ -632,7 +632,7 @@ int64_t attn_plan(AttnParams *p, int dtype) {
 // and 31 behind 1000, 32 + 8 heads N128 4540 us without and 545 with pieces (all 32 behind
 // 8000: 643 and 661); b8 L512 behind 0 to 30000 1610 and 1370.  Of one tile a row, 8192
 // workgroups of up to 4096 keys: b1024, one row of 16000 keys and the others of 200, 8 heads
-// N64 204 us without and 154 with pieces; b256, 32000 and 500, 32 heads N128 647 and 478; even
+// N64 204 us without and 113 with pieces; b256, 32000 and 500, 32 heads N128 647 and 478; even
 // rows of 5000 or 0 to 8000 keys the same within 2 %.
 void attn_slots(AttnParams *p) {
   if (p->workers == 1) return;

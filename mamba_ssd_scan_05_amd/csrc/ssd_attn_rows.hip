@@ -16,9 +16,9 @@
 // when this took 647 with 0.0019 to 0.0020; moved past 2^8: 0.0022, 638 us.  The output's
 // rounding alone is 0.0016.)
 //
-// Measured, 32 + 8 heads N128 (bf16): prompt b4 L4096 647 us (850 TFLOP/s counted on the
-// pairs that are seen; a large product reaches 1358), 512 tokens behind 32000 295 us (915)
-// with their join.
+// Measured, 32 + 8 heads N128 (bf16): prompt b4 L4096 636 to 666 us (826 to 865 TFLOP/s counted
+// on the pairs that are seen; a large product reaches 1358), 512 tokens behind 32000 289 to 328 us
+// (825 to 936) with their join, by the clock.
 // Of a pass's 5000 cycles the matrix cores work 37 %, the vector ALU 44 (32 exponentials a
 // lane are 512 of its 1000 cycles a wave); LDS reads have no conflicts.  Without the loads,
 // stores and barrier of a pass the second case took 249 of 314 us, without exponentials
@@ -27,7 +27,7 @@
 // ahead (648 and 654 against 650), the stores between the products (661 against 621).
 // 96 registers hold O and Q and 64 two tiles' scores, so eight waves are all a compute unit
 // takes.  Wide heads (N > 128): four waves with the whole register file, tiles of 32 keys;
-// b4 L2048 10 + 1 heads N256 209 us, 411 TFLOP/s, 8 registers in scratch.
+// b4 L2048 10 + 1 heads N256 208 us, 413 TFLOP/s.
 #include <type_traits>
 
 #include "ssd_attn_device.h"
