@@ -382,7 +382,9 @@ template <int NP, int W, bool UNI> __global__ __launch_bounds__(64 * W, NP <= 12
         for (int x = from; x < to; ++x) {
           const float w = hw_exp2(fmaf(s[x / 16][x % 16], p.scale, -base));
           part[x % 4] += w;
-          // rounded to bf16 for the product (half a step, 2^-8 of each)
+          // rounded to bf16 for the product (half a step, 2^-8 of each).  A second part, as in
+          // attn_kernel: prompt b4 L4096 644 -> 810 us, 512 tokens behind 32000 294 -> 386, wide heads
+          // b4 L4096 638 -> 719, 8 tokens behind 8000 41.5 -> 45.2
           pf[x / 8][x % 8] = (__bf16)w;
         }
       };
