@@ -106,3 +106,23 @@ def test_one_long_row_of_several_tokens(dtype):
     uneven = shared(b, L, 32, 8, 64, 66000, [300] * (b - 1) + [300 + 65536], dtype)
     print("%d rows: %.0f us, one of them long %.0f" % (b, even, uneven), flush=True)
     assert uneven < 2 * even
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b", [3, 100, 300])
+def test_rows_without_any_token(b, dtype):
+    # nothing is written, in the pieces' plans of any number of rows; then one row has a token
+    t = Batch([5000 if i == 1 else 30 for i in range(b)], [0] * b, 20, 4, 2, 16, 16, dtype, seed=2, spare=0)
+    out, lse = t.call(0.25, 0)
+    assert (out == 9.0).all() and (lse == 9.0).all()
+    t.counts[1], t.starts[1] = 1, t.starts[1] - 1  # its key is the last cached one
+    out, lse = t.call(0.25, 0)
+    keep = out[1, 0].clone(), lse[1, 0].clone()
+    out[1, 0], lse[1, 0] = 9.0, 9.0
+    assert (out == 9.0).all() and (lse == 9.0).all()
+    out[1, 0], lse[1, 0] = keep
+    part = object.__new__(Batch)
+    part.__dict__.update(t.__dict__, b=1, starts=t.starts[1:2], counts=[1], k=[t.k[1]], v=[t.v[1]], q=t.q[1:2], table=t.table[1:2])
+    want, wl, eo, el = part.expect(0.25, 0)
+    check("out", out[1:2], want, eo)
+    check("lse", lse[1:2], wl, el)
